@@ -1,0 +1,139 @@
+// Host side of the attention over the 4-bit paged cache: the handle and the launch.
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "ar_decode_attn.h"
+
+namespace {
+
+// Query columns (16 rows each) of a tile: as many as the rows of an average request fill, up to
+// what the registers hold. More columns read the cache for more rows at once; columns that stay
+// empty cost their matrix instructions.
+int max_columns(int dtype, int head_dim) {
+  if (dtype == AR_BFLOAT16) return head_dim <= 128 ? 4 : 2;
+  return head_dim <= 128 ? 2 : 1;
+}
+
+int pick_columns(const ar_kv4* h, const ar_kv4_attention_args* a) {
+  const int64_t rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
+  const int64_t each = (rows + a->nreq - 1) / a->nreq;
+  const int most = max_columns(a->dtype, h->head_dim);
+  int n = 1;
+  while (n < most && each > 16 * n) n *= 2;
+  return n;
+}
+
+// Partial results of a launch: at most two slots an item of the split, each R rows of head_dim
+// sums and a {max, sum} pair.
+size_t part_bytes(int columns, int head_dim) {
+  return (size_t(2) << ard::target_shift(columns)) * 16 * columns * (head_dim + 2) * sizeof(float);
+}
+
+constexpr size_t kArrivedBytes = (size_t(2) << 10) * sizeof(uint32_t);
+
+}  // namespace
+
+extern "C" {
+
+ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
+  if (kv_heads < 1 || kv_heads > 1024) {
+    ar_fail(AR_EINVAL, "kv_heads must be in [1, 1024], got %d", kv_heads);
+    return nullptr;
+  }
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256) {
+    ar_fail(AR_ENOTSUP, "head_dim must be 64, 96, 128, 192 or 256, got %d", head_dim);
+    return nullptr;
+  }
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) {
+    ar_fail(AR_EINVAL, "page_size must be a power of two in [16, 1024], got %d", page_size);
+    return nullptr;
+  }
+  ar_kv4* h = new (std::nothrow) ar_kv4;
+  if (h == nullptr) {
+    ar_fail(AR_ENORES, "out of host memory");
+    return nullptr;
+  }
+  *h = ar_kv4{kv_heads, head_dim, page_size, __builtin_ctz(page_size), nullptr, 0};
+  for (int n = 1; n <= max_columns(AR_BFLOAT16, head_dim); n *= 2)
+    h->work_bytes = std::max(h->work_bytes, part_bytes(n, head_dim));
+  int devices = 0;
+  if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
+    (void)hipGetLastError();
+    return h;
+  }
+  hipError_t e = hipMalloc(&h->work, h->work_bytes + kArrivedBytes);
+  if (e == hipSuccess) e = hipMemset(static_cast<uint8_t*>(h->work) + h->work_bytes, 0, kArrivedBytes);
+  if (e == hipSuccess) e = hipDeviceSynchronize();
+  if (e != hipSuccess) {
+    ar_fail_hip(e, "the workspace of ar_kv4_create");
+    if (h->work != nullptr) (void)hipFree(h->work);
+    delete h;
+    return nullptr;
+  }
+  return h;
+}
+
+void ar_kv4_destroy(ar_kv4* h) {
+  if (h == nullptr) return;
+  if (h->work != nullptr) {
+    (void)hipDeviceSynchronize();
+    (void)hipFree(h->work);
+  }
+  delete h;
+}
+
+int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
+  using namespace ard;
+  if (int rc = check_handle(h)) return rc;
+  if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
+  if (int rc = check_dtype(a->dtype)) return rc;
+  if (a->ntokens < 0 || a->nreq < 0 || a->table_width < 0) return ar_fail(AR_EINVAL, "negative size");
+  if (a->q_heads < 1 || a->q_heads % h->heads != 0)
+    return ar_fail(AR_EINVAL, "q_heads must be a multiple of the %d kv heads, got %d", h->heads, a->q_heads);
+  if (a->q_heads > 65536) return ar_fail(AR_ETOOBIG, "too many heads");
+  if (a->window < 0) return ar_fail(AR_EINVAL, "window must not be negative, got %d", a->window);
+  if (!std::isfinite(a->scale)) return ar_fail(AR_EINVAL, "scale must be finite");
+  if (int rc = check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (a->table_stride < a->table_width) return ar_fail(AR_EINVAL, "table_stride is below table_width");
+  if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
+  if (a->q == nullptr || a->out == nullptr) return ar_fail(AR_EINVAL, "null q or out");
+  if (a->kv_len == nullptr || a->q_start == nullptr || (a->table_width > 0 && a->table == nullptr))
+    return ar_fail(AR_EINVAL, "null request buffer");
+  const int64_t unit = a->dtype == AR_BFLOAT16 ? 8 : 4;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token % unit != 0 || a->q_head % unit != 0 ||
+      a->o_token % unit != 0 || a->o_head % unit != 0)
+    return ar_fail(AR_EINVAL, "q and out: addresses and strides must be multiples of 16 bytes");
+  if (a->q_token < 0 || a->q_head < 0 || a->o_token < 0 || a->o_head < 0)
+    return ar_fail(AR_EINVAL, "negative stride");
+  if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
+
+  const int columns = pick_columns(h, a);
+  AttnArgs args;
+  args.a = *a;
+  args.cache = Cache{const_cast<uint8_t*>(a->data), const_cast<uint8_t*>(a->scales), a->num_pages,
+                     h->heads, h->page_shift};
+  args.group = a->q_heads / h->heads;
+  args.target_shift = target_shift(columns);
+  args.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  args.part = static_cast<uint8_t*>(h->work);
+  args.part_bytes = static_cast<uint32_t>(part_bytes(columns, h->head_dim));
+  args.stats_at = (2u << args.target_shift) * 16 * columns * h->head_dim * 4;
+  args.arrived = reinterpret_cast<uint32_t*>(args.part + h->work_bytes);
+  // Jobs: query tiles x kv heads. Cutting them into parts of equal length gives at most
+  // 2^target_shift parts more than that; workgroups beyond the parts that exist end at once.
+  const int64_t tiles = static_cast<int64_t>(a->ntokens) * args.group / (16 * columns) +
+                        std::min(a->nreq, a->ntokens);
+  const int64_t grid = tiles * h->heads + (int64_t(1) << args.target_shift);
+  if (grid > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  attn_fn fn = a->dtype == AR_BFLOAT16 ? select_attn_bf16(h->head_dim, columns)
+                                       : select_attn_f32(h->head_dim, columns);
+  if (fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
+  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0,
+                     static_cast<hipStream_t>(stream), args);
+  AR_HIP(hipGetLastError());
+  return AR_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,604 @@
+// Attention over the 4-bit paged cache (gfx950).
+//
+// Mathematics. One pass over the keys and values with a running reference m and sum l per row:
+// s = scale q.k in base-2 units, p = 2^(s - m), l += p, o += p v; where a row's maximum passes m by
+// more than 8, l and o are scaled by 2^(m - m') first (p then stays below 2^8, far from any
+// limit). Parts of a row are joined by the same rule.
+//
+// Shape. The products run transposed, so that nothing is moved between lanes in the loop:
+//   S^T [32 tokens x 16 rows]  = K  [tokens x D]  Q^T      two 16x16x32 tiles
+//   O^T [D x 16 rows]         += V^T [D x tokens] P^T
+// A lane (c = lane % 16, g = lane / 16) of the first product holds row c's scores of tokens
+// 4g .. 4g+3 of both 16-token halves, which is exactly its operand of the second. Keys: a lane
+// reads a quarter of token c's row, its operand of every step along D. Values: a lane reads eight
+// elements of four tokens at once (the cache's interleaved layout) and pairs tokens with one byte
+// permute per pair. Codes become bfloat16 with one conversion per two elements, the scale applied
+// by the conversion, exactly; no LDS is used before the join.
+//
+// Work. A job is a tile of query rows (16 * NQ: tokens x heads of the group) of one request and kv
+// head. The tokens a job sees are cut into parts of equal length for all jobs, chosen by every
+// workgroup from the requests' lengths so that about 2^target_shift parts exist; a workgroup takes
+// one part, its four waves every fourth 32-token tile. A job of several parts leaves partial sums
+// in the workspace and the last workgroup to arrive joins them in the order of the tokens, so the
+// result does not depend on who came last. Nothing waits for another workgroup.
+#pragma once
+
+#include "ar_decode_attn.h"
+
+namespace ard {
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ bf16x8 operand(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  const u32x4 v = {w0, w1, w2, w3};
+  return __builtin_bit_cast(bf16x8, v);
+}
+template <int BYTE>
+__device__ __forceinline__ uint32_t codes(uint32_t w, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, BYTE));
+}
+// Low (high) halves of a and b side by side.
+__device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Over the four lanes that hold one row: lane ^ 16, lane ^ 32.
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+__device__ __forceinline__ int row_or(int x) {
+  x |= __shfl_xor(x, 16);
+  return x | __shfl_xor(x, 32);
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x as a sum of PARTS bfloat16 values (three hold all 24 bits). An infinity or NaN stays in the
+// first part alone.
+template <int PARTS>
+__device__ __forceinline__ void split(const float* x, bf16x8* out) {
+  uint32_t w[PARTS][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      uint32_t v;
+      if (p + 1 < PARTS) {
+        // truncated, so that no finite value becomes infinite
+        v = pair_hi(__float_as_uint(a), __float_as_uint(b));
+        const float ra = a - bf16_lo(v), rb = b - bf16_hi(v);
+        a = fabsf(a) < INFINITY ? ra : 0.0f;
+        b = fabsf(b) < INFINITY ? rb : 0.0f;
+      } else {
+        v = ar::bf16x2_rne(a, b);
+      }
+      w[p][i] = v;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) out[p] = operand(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+struct Job {
+  int request, tile, head, chunk;
+  int slot;      // workspace slot of this part, its job's first is slot - chunk
+  int per_part;  // 32-token tiles of a part
+};
+
+// A request's cost as the work split sees it: tiles of rows, parts of a tile.
+struct Cost {
+  int q0, m, kv;
+  int tiles, span;
+};
+
+template <int R>
+__device__ __forceinline__ Cost cost_of(const AttnArgs& args, int b) {
+  const ar_kv4_attention_args& a = args.a;
+  Cost c = {0, 0, 0, 0, 0};
+  if (b < a.nreq) {
+    c.q0 = min(max(a.q_start[b], 0), a.ntokens);
+    c.m = max(min(a.q_start[b + 1], a.ntokens) - c.q0, 0);
+    c.kv = max(a.kv_len[b], 0);
+    c.tiles = static_cast<int>((static_cast<int64_t>(c.m) * args.group + R - 1) / R);
+    const int64_t most = static_cast<int64_t>(a.table_width) << args.cache.page_shift;
+    int64_t seen = c.kv < most ? c.kv : most;
+    if (a.window > 0) {
+      // a tile's rows are at most R / group + 1 tokens, its range starts at a multiple of 32
+      const int64_t far = static_cast<int64_t>(a.window) + R / args.group + 1 + 32;
+      seen = seen < far ? seen : far;
+    }
+    c.span = static_cast<int>((seen + 31) >> 5);
+  }
+  return c;
+}
+
+// The part of the work that workgroup `item` does; false where there is none. Every wave computes
+// it alone (lanes are requests), with no barrier.
+template <int R>
+__device__ __forceinline__ bool find_job(const AttnArgs& args, int item, Job& job, Cost& mine) {
+  const int lane = threadIdx.x & 63, n = args.a.nreq, heads = args.cache.heads;
+  int64_t total = 0;
+  Cost c = cost_of<R>(args, lane);
+  for (int b = 0; b < n; b += 64) {
+    const Cost x = b == 0 ? c : cost_of<R>(args, b + lane);
+    total += static_cast<int64_t>(x.tiles) * x.span;
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
+  total *= heads;
+  const int64_t each = (total + (int64_t(1) << args.target_shift) - 1) >> args.target_shift;
+  // a tile of 32 tokens for each wave at least
+  const int per = static_cast<int>(max<int64_t>(kAttnWaves, (each + kAttnWaves - 1) / kAttnWaves * kAttnWaves));
+  int64_t items = 0, slots = 0;
+  for (int b = 0; b < n; b += 64) {
+    const Cost x = b == 0 ? c : cost_of<R>(args, b + lane);
+    const int parts = max(1, (x.span + per - 1) / per);
+    const int64_t jobs = static_cast<int64_t>(x.tiles) * heads;
+    const int64_t my_items = jobs * parts, my_slots = parts > 1 ? my_items : 0;
+    int64_t upto = my_items, slot_upto = my_slots;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int64_t y = __shfl_up(upto, s), z = __shfl_up(slot_upto, s);
+      if (lane >= s) upto += y, slot_upto += z;
+    }
+    const uint64_t hit = __ballot(items + upto > item);
+    if (hit != 0) {
+      const int who = __builtin_ctzll(hit);
+      const int at = item - static_cast<int>(items + __shfl(upto - my_items, who));
+      const int tiles = __shfl(x.tiles, who), count = __shfl(parts, who);
+      job.request = uniform(b + who);
+      // neighbouring workgroups (on the eight XCDs in turn) take neighbouring heads, and the
+      // tiles with the longest ranges come first
+      const int rest = at / heads;
+      job.head = uniform(at - rest * heads);
+      job.chunk = uniform(rest / tiles);
+      job.tile = uniform(tiles - 1 - (rest - rest / tiles * tiles));
+      job.slot = uniform(static_cast<int>(slots + __shfl(slot_upto - my_slots, who)) +
+                         (job.tile * heads + job.head) * count + job.chunk);
+      job.per_part = uniform(per);
+      mine.q0 = uniform(__shfl(x.q0, who));
+      mine.m = uniform(__shfl(x.m, who));
+      mine.kv = uniform(__shfl(x.kv, who));
+      return true;
+    }
+    items += __shfl(upto, 63);
+    slots += __shfl(slot_upto, 63);
+  }
+  return false;
+}
+
+// Any byte above kMaxScale (252) in a word of scale bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x03030303u) & w & 0x80808080u;
+}
+
+// N consecutive dwords with the widest loads that their alignment allows (4 N bytes, N a divisor or
+// multiple of the width).
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* out) {
+  constexpr int W = N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1;
+  typedef uint32_t vec __attribute__((ext_vector_type(W)));
+#pragma unroll
+  for (int i = 0; i < N; i += W) {
+    const vec v = *reinterpret_cast<const vec*>(p + 4 * i);
+#pragma unroll
+    for (int j = 0; j < W; ++j) out[i + j] = v[j];
+  }
+}
+
+template <int D>
+struct Tile32 {  // a lane's share of 32 tokens, as loaded
+  static constexpr int kDw = D / 32;               // dwords of a quarter of a K row
+  static constexpr int kKs = kDw == 2 || kDw == 4 ? 1 : 2;  // 32-groups they lie in
+  static constexpr int kSets = (D / 8 + 15) / 16;  // chunks of eight elements / 16 lanes
+  uint32_t k[2][kDw];
+  uint32_t ks[2][kKs];
+  u32x4 v[2][kSets];
+  uint32_t vs[2][kSets];
+};
+
+template <int DT, int D, int NQ, int OCC>
+__global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args) {
+  constexpr int R = 16 * NQ;
+  constexpr int PARTS = DT == DT_BF16 ? 1 : 3;
+  constexpr int NC = D / 8;
+  typedef Tile32<D> Tile;
+  constexpr int kDw = Tile::kDw, kKs = Tile::kKs, kSets = Tile::kSets;
+  constexpr int kPitch = D + 4;  // LDS row: 16 rows' 16-byte accesses fall into different banks
+  __shared__ float join[kAttnWaves * 16 * kPitch];
+  __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
+  __shared__ int last;
+
+  const ar_kv4_attention_args& a = args.a;
+  Job job;
+  Cost me;
+  if (!find_job<R>(args, blockIdx.x, job, me)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int group = args.group, shift = args.cache.page_shift;
+
+  // Rows of this tile and what each sees.
+  const int rows = me.m * group;
+  const int row0 = job.tile * R;
+  const int i0 = row0 / group, i1 = (min(row0 + R, rows) - 1) / group;
+  const int64_t room = static_cast<int64_t>(a.table_width) << shift;
+  const int kv_end = static_cast<int>(min<int64_t>(me.kv, room));
+  const int first_pos = me.kv - me.m;  // position of the request's first new token
+  const int end = min(max(first_pos + i1 + 1, 0), kv_end);
+  int begin = 0;
+  if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
+  const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
+  const int parts = max(1, (ntiles + job.per_part - 1) / job.per_part);
+  if (job.chunk >= parts) return;
+  const int t_first = job.chunk * job.per_part, t_last = min(t_first + job.per_part, ntiles);
+
+  int hi[NQ], lo[NQ];
+  bf16x8 q[NQ][PARTS][kDw];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int row = row0 + n * 16 + c;
+    const bool real = row < rows;
+    const int i = real ? row / group : 0;
+    const int pos = first_pos + i;
+    hi[n] = real ? min(pos + 1, kv_end) : 0;
+    lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+    const int64_t at = static_cast<int64_t>(me.q0 + i) * a.q_token +
+                       static_cast<int64_t>(job.head * group + (real ? row - i * group : 0)) * a.q_head + g * (D / 4);
+#pragma unroll
+    for (int s = 0; s < kDw; ++s) {
+      if (DT == DT_BF16) {
+        u32x4 w = {0, 0, 0, 0};
+        if (real) w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at + s * 8);
+        q[n][0][s] = __builtin_bit_cast(bf16x8, w);
+      } else {
+        float x[8] = {};
+        if (real) {
+          const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at + s * 8);
+          const f32x4 v0 = p[0], v1 = p[1];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = v0[j], x[4 + j] = v1[j];
+        }
+        bf16x8 w[PARTS];
+        split<PARTS>(x, w);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) q[n][p][s] = w[p];
+      }
+    }
+  }
+  // Tiles from here on need masks: the first row's end, the last row's window.
+  const int whole_end = min(first_pos + i0 + 1, kv_end);
+  const int whole_begin = a.window > 0 ? first_pos + i1 - a.window + 1 : 0;
+
+  f32x4 acc[NQ][kSets][8];
+  float m[NQ], l[NQ];
+  int nan_groups[NQ];  // groups of 32 elements in which a visible value is NaN
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
+#pragma unroll
+    for (int e = 0; e < kSets; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
+  }
+
+  // Per-lane offsets within a page's K and V.
+  const int page = 1 << shift;
+  const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
+  int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
+  int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
+  const uint8_t* data = args.cache.data + static_cast<int64_t>(job.head) * 2 * k_bytes;
+  const uint8_t* scales = args.cache.scales + static_cast<int64_t>(job.head) * 2 * s_bytes;
+  const int32_t* table = a.table + job.request * a.table_stride;
+  const int num_pages = static_cast<int>(args.cache.num_pages);
+  const int k_group = (g * kDw) >> 2;  // 32-group of a lane's first K dword
+  int k_off = c * (D / 2) + g * (D / 8);
+  int v_off[kSets], vs_off[kSets];
+#pragma unroll
+  for (int e = 0; e < kSets; ++e) {
+    const int chunk = min(e * 16 + c, NC - 1);  // lanes beyond the row repeat its last chunk
+    v_off[e] = k_bytes + g * (D * 2) + chunk * 16;
+    vs_off[e] = s_bytes + (chunk >> 2) * page + g * 4;
+  }
+
+  // Pages of a tile's two halves; -1: nothing to see there.
+  auto pages = [&](int tile, int* id) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = begin + tile * 32 + u * 16;
+      int p = -1;
+      if (tile < t_last && t < end) p = table[t >> shift];
+      p = uniform(p);
+      id[u] = p >= 0 && p < num_pages ? p : -1;
+    }
+  };
+  auto load = [&](int tile, const int* id, Tile& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int off = (begin + tile * 32 + u * 16) & (page - 1);
+      const int64_t p = max(id[u], 0);
+      const uint8_t* kd = data + p * page_bytes + off * (D / 2);
+      const uint8_t* sd = scales + p * page_scales + off;
+      load_dwords<kDw>(kd + k_off, x.k[u]);
+#pragma unroll
+      for (int s = 0; s < kKs; ++s)
+        x.ks[u][s] = sd[min(k_group + s, D / 32 - 1) * page + c];
+#pragma unroll
+      for (int e = 0; e < kSets; ++e) {
+        x.v[u][e] = *reinterpret_cast<const u32x4*>(kd + v_off[e]);
+        x.vs[u][e] = *reinterpret_cast<const uint32_t*>(sd + vs_off[e]);
+      }
+    }
+  };
+
+  int id[2], id_next[2];
+  Tile now, next;
+  int tile = t_first + wave;
+  pages(tile, id);
+  load(tile, id, now);
+  pages(tile + kAttnWaves, id_next);
+
+  for (; tile < t_last; tile += kAttnWaves) {
+    load(tile + kAttnWaves, id_next, next);
+    int id_after[2];
+    pages(tile + 2 * kAttnWaves, id_after);
+
+    const int t0 = begin + tile * 32;
+    // Scores.
+    f32x4 s[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float sc[kKs];
+#pragma unroll
+      for (int i = 0; i < kKs; ++i) sc[i] = scale_of(now.ks[u][i]);
+#pragma unroll
+      for (int i = 0; i < kDw; ++i) {
+        float x = sc[0];
+        if (kKs > 1) x = ((g * kDw + i) >> 2) == k_group ? sc[0] : sc[kKs - 1];
+        const uint32_t w = now.k[u][i];
+        const bf16x8 kk = operand(codes<0>(w, x), codes<1>(w, x), codes<2>(w, x), codes<3>(w, x));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) s[n][u] = mfma(kk, q[n][p][i], s[n][u]);
+      }
+    }
+    const bool partial = t0 + 32 > whole_end || t0 < whole_begin || id[0] < 0 || id[1] < 0;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
+    if (partial) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + u * 16 + g * 4 + i;
+            if (t >= hi[n] || t < lo[n] || id[u] < 0) s[n][u][i] = -INFINITY;
+          }
+    }
+
+    // Values that are NaN (or bytes that were never written) must not meet the zeros of rows that
+    // do not see them: such groups are read as finite and the rows that do see them noted.
+    uint32_t odd = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < kSets; ++e) odd |= nan_bytes(now.vs[u][e]);
+    if (__any(odd != 0)) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < kSets; ++e) {
+          uint32_t bad = nan_bytes(now.vs[u][e]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // the groups of this set, held by lanes c = 4k
+            const int group32 = e * 4 + k;
+            if (group32 >= D / 32) break;
+            const uint32_t theirs = __shfl(static_cast<int>(bad), g * 16 + 4 * k);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = t0 + u * 16 + g * 4 + i;
+                if ((theirs >> (8 * i + 7) & 1) && t < hi[n] && t >= lo[n] && id[u] >= 0)
+                  nan_groups[n] |= 1 << group32;
+              }
+          }
+          bad |= bad >> 1, bad |= bad >> 2, bad |= bad >> 4;
+          now.vs[u][e] &= ~bad;  // 2^-127 or so: finite
+        }
+    }
+
+    // Probabilities.
+    bf16x8 pr[NQ][PARTS];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3];
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+      if (__any(top > m[n] + 8.0f)) {
+        const float to = fmaxf(m[n], row_max(top));
+        const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
+        m[n] = to;
+        l[n] *= f;
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
+      }
+      const float ref = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = exp2_fast(x[i] - ref);
+        l[n] += x[i];
+      }
+      split<PARTS>(x, pr[n]);
+    }
+
+    // Values.
+#pragma unroll
+    for (int e = 0; e < kSets; ++e) {
+      float sc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sc[i] = __uint_as_float((now.vs[i >> 2][e] >> (8 * (i & 3)) & 0xFFu) << 23);
+#define ARD_PAIR(B)                                                                              \
+  {                                                                                              \
+    uint32_t w[8];                                                                               \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) w[i] = codes<B>(now.v[i >> 2][e][i & 3], sc[i]); \
+    const bf16x8 v0 = operand(pair_lo(w[0], w[1]), pair_lo(w[2], w[3]), pair_lo(w[4], w[5]),     \
+                              pair_lo(w[6], w[7]));                                              \
+    const bf16x8 v1 = operand(pair_hi(w[0], w[1]), pair_hi(w[2], w[3]), pair_hi(w[4], w[5]),     \
+                              pair_hi(w[6], w[7]));                                              \
+    _Pragma("unroll") for (int n = 0; n < NQ; ++n) _Pragma("unroll") for (int p = 0; p < PARTS; ++p) { \
+      acc[n][e][2 * B] = mfma(v0, pr[n][p], acc[n][e][2 * B]);                                   \
+      acc[n][e][2 * B + 1] = mfma(v1, pr[n][p], acc[n][e][2 * B + 1]);                           \
+    }                                                                                            \
+  }
+      ARD_PAIR(0) ARD_PAIR(1) ARD_PAIR(2) ARD_PAIR(3)
+#undef ARD_PAIR
+    }
+    now = next;
+    id[0] = id_next[0], id[1] = id_next[1];
+    id_next[0] = id_after[0], id_next[1] = id_after[1];
+  }
+
+  // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    l[n] = row_sum(l[n]);
+    nan_groups[n] = row_or(nan_groups[n]);
+    if (g == 0) stat_m[wave][n * 16 + c] = m[n], stat_l[wave][n * 16 + c] = l[n];
+  }
+  __syncthreads();
+  const int seg_per = NC;  // eight elements a thread
+  const bool alone = parts == 1;
+  const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    float top = stat_m[0][n * 16 + c];
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][n * 16 + c]);
+    const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
+    float* mine = join + (wave * 16 + c) * kPitch;
+#pragma unroll
+    for (int e = 0; e < kSets; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int chunk = e * 16 + g * 4 + i;
+        if (chunk < NC) {
+          const float nan = nan_groups[n] >> (chunk >> 2) & 1 ? __uint_as_float(0x7FC00000u) : 0.0f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = acc[n][e][4 * h + j][i] * f + nan;
+            *reinterpret_cast<f32x4*>(mine + chunk * 8 + 4 * h) = v;
+          }
+        }
+      }
+    __syncthreads();
+    for (int x = tid; x < 16 * seg_per; x += kAttnThreads) {
+      const int r = x / seg_per, seg = x - r * seg_per, row = row0 + n * 16 + r;
+      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+      float rm = stat_m[0][n * 16 + r], rl = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kAttnWaves; ++w) rm = fmaxf(rm, stat_m[w][n * 16 + r]);
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float* p = join + (w * 16 + r) * kPitch + seg * 8;
+        o0 += *reinterpret_cast<const f32x4*>(p);
+        o1 += *reinterpret_cast<const f32x4*>(p + 4);
+        if (rm != -INFINITY) rl += stat_l[w][n * 16 + r] * exp2_fast(stat_m[w][n * 16 + r] - rm);
+      }
+      if (row >= rows) continue;
+      if (!alone) {
+        const uint32_t at = static_cast<uint32_t>(job.slot * R + n * 16 + r);
+        ar::st16<ar::kCoh>(part, (at * D + seg * 8) * 4, __builtin_bit_cast(u32x4, o0));
+        ar::st16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4, __builtin_bit_cast(u32x4, o1));
+        if (seg == 0)
+          ar::st8<ar::kCoh>(part, args.stats_at + at * 8, u32x2{__float_as_uint(rm), __float_as_uint(rl)});
+        continue;
+      }
+      const int i = row / group, head = job.head * group + row - i * group;
+      const int64_t token = me.q0 + i;
+      const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
+      o0 *= inv, o1 *= inv;
+      const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
+      if (DT == DT_BF16) {
+        const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
+                         ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
+      } else {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
+      }
+      if (seg == 0 && a.lse != nullptr)
+        a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (rm + log2f(rl)) * 0.6931471805599453f;
+    }
+    if (n + 1 < NQ) __syncthreads();
+  }
+  if (alone) return;
+
+  // Parts: write-through stores are done before the arrival is counted; the last one joins.
+  ar::wait_all_mem();
+  __syncthreads();
+  const int job_slot = job.slot - job.chunk;
+  if (tid == 0) {
+    const uint32_t before = __hip_atomic_fetch_add(args.arrived + job_slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = before + 1 == static_cast<uint32_t>(parts);
+    if (last) __hip_atomic_store(args.arrived + job_slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int x = tid; x < R * seg_per; x += kAttnThreads) {
+    const int r = x / seg_per, seg = x - r * seg_per, row = row0 + r;
+    if (row >= rows) continue;
+    const uint32_t at0 = static_cast<uint32_t>(job_slot * R + r);
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p)
+      top = fmaxf(top, __uint_as_float(ar::ld8<ar::kCoh>(part, args.stats_at + (at0 + p * R) * 8).x));
+    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+    float rl = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const uint32_t at = at0 + p * R;
+      const u32x2 st = ar::ld8<ar::kCoh>(part, args.stats_at + at * 8);
+      const f32x4 v0 = __builtin_bit_cast(f32x4, ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4));
+      const f32x4 v1 = __builtin_bit_cast(f32x4, ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4));
+      const float f = top == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st.x) - top);
+      rl += __uint_as_float(st.y) * f;
+      o0 += v0 * f, o1 += v1 * f;
+    }
+    const int i = row / group, head = job.head * group + row - i * group;
+    const int64_t token = me.q0 + i;
+    const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
+    o0 *= inv, o1 *= inv;
+    const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
+    if (DT == DT_BF16) {
+      const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
+                       ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
+    }
+    if (seg == 0 && a.lse != nullptr)
+      a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace ard

@@ -1,0 +1,365 @@
+// Row operators of the decode path: per-head RMS norm and position rotation of q and k, rows into
+// the 4-bit paged cache and rows out of it.
+//
+// A row (one head of one token, 64..256 elements) belongs to 8, 16 or 32 neighbouring lanes, eight
+// elements a lane, so everything a row needs (its sum of squares, the largest element of each 32)
+// is a few cross-lane steps and each byte of HBM moves once.
+//
+// Arithmetic of the norm and the rotation is 64-bit: gfx950's binary64 rate is that of unpacked
+// binary32, the kernel is bound by bytes (or by its launch), and what is rounded to bfloat16 and
+// then to 4 bits no longer depends on the order of the sum of squares.
+
+#include "ar_decode.h"
+
+namespace ard {
+
+constexpr int kRowThreads = 256;
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DT_F32> {
+  typedef float T;
+  __device__ static void load4(const void* base, int64_t at, float* x) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v[i];
+  }
+  __device__ static void store4(void* base, int64_t at, const float* x) {
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[i];
+    *reinterpret_cast<f32x4*>(static_cast<float*>(base) + at) = v;
+  }
+  __device__ static float round(double y) { return static_cast<float>(y); }
+};
+template <>
+struct Elem<DT_BF16> {
+  typedef uint16_t T;
+  __device__ static void load4(const void* base, int64_t at, float* x) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + at);
+    x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+  }
+  __device__ static void store4(void* base, int64_t at, const float* x) {
+    u32x2 v;
+    v.x = ar::bf16x2_rne(x[0], x[1]), v.y = ar::bf16x2_rne(x[2], x[3]);
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(base) + at) = v;
+  }
+  __device__ static float round(double y) {
+    return bf16_lo(ar::bf16x2_rne(static_cast<float>(y), 0.0f));
+  }
+};
+
+// Writes eight consecutive elements x of a row, elements 8u .. 8u+7, as codes; the four lanes of a
+// group of 32 share its scale. K rows are plain, V rows interleaved by four tokens.
+__device__ __forceinline__ void put_row(const Cache& c, int64_t slot, int head, bool value, int d,
+                                        int u, const float* x) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 1)));
+  most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 2)));
+  // most = m 2^E with 1 <= m < 2; the smallest scale with m 2^E <= 6 scale is 2^(E-2) while
+  // m <= 1.5, 2^(E-1) beyond.
+  const int e = static_cast<int>(most >> 23) - 2 + ((most & 0x7FFFFFu) > 0x400000u);
+  const uint32_t byte = most >= 0x7F800000u ? 255u : static_cast<uint32_t>(min(max(e, 1), kMaxScale));
+  const float scale = __uint_as_float(byte << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
+  if (byte == 255u) w = 0;
+  const int page = 1 << c.page_shift, off = static_cast<int>(slot) & (page - 1);
+  const int64_t part = ((slot >> c.page_shift) * c.heads + head) * 2 + value;
+  uint8_t* data = c.data + part * (page * (d / 2));
+  const int at = value ? (off >> 2) * (d * 2) + u * 16 + (off & 3) * 4 : off * (d / 2) + u * 4;
+  *reinterpret_cast<uint32_t*>(data + at) = w;
+  if ((u & 3) == 0) c.scales[part * (page * (d / 32)) + (u >> 2) * page + off] = static_cast<uint8_t>(byte);
+}
+
+struct RowArgs {
+  ar_qk_norm_rope_args a;
+  Cache cache;
+  int values;  // rows of v a token (kv_heads with a cache, else 0)
+};
+
+// G lanes a row. CACHE: keys and values go into the cache, else keys to k_out.
+template <int DT, int G, bool CACHE>
+__global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
+  const ar_qk_norm_rope_args& a = r.a;
+  // A rotated row's elements pass through LDS on their way to the cache: the rotation pairs
+  // elements half a row apart, the cache's groups are consecutive.
+  __shared__ float stage[CACHE ? kRowThreads * 8 : 1];
+  const int d = a.head_dim, rot = a.rot;
+  const int per_token = a.q_heads + a.kv_heads + r.values;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
+  const int u = threadIdx.x % G;
+  const int t = static_cast<int>(row / per_token);
+  const int h = static_cast<int>(row - static_cast<int64_t>(t) * per_token);
+  if (t >= a.ntokens) return;
+  const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
+  const int head = is_q ? h : is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
+  const int32_t pos = a.positions != nullptr ? a.positions[t] : 0;
+  int64_t slot = -1;
+  if (CACHE && !is_q) slot = a.slots[t];
+  if (pos < 0) return;
+  if (CACHE && !is_q && (slot < 0 || (slot >> r.cache.page_shift) >= r.cache.num_pages)) return;
+  const void* src = is_q ? a.q : is_v ? a.v : a.k;
+  const int64_t from = is_q ? t * a.q_token + head * a.q_head
+                     : is_v ? t * a.v_token + head * a.v_head
+                            : t * a.k_token + head * a.k_head;
+  const bool live = u * 8 < d;
+  const bool turned = !is_v && u * 8 < rot;
+  // A lane's two runs of four elements: both ends of its pairs.
+  const bool halves = turned && !a.interleaved;
+  const int lo = halves ? 4 * u : 8 * u, hi = halves ? rot / 2 + 4 * u : 8 * u + 4;
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  if (live) {
+    Elem<DT>::load4(src, from + lo, x);
+    Elem<DT>::load4(src, from + hi, x + 4);
+  }
+  if (!is_v) {
+    double y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    const void* weight = is_q ? a.q_weight : a.k_weight;
+    if (weight != nullptr) {
+      float w[8] = {};
+      if (live) {
+        Elem<DT>::load4(weight, lo, w);
+        Elem<DT>::load4(weight, hi, w + 4);
+      }
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fma(y[i], y[i], sum);
+#pragma unroll
+      for (int s = 1; s < G; s <<= 1) sum += __shfl_xor(sum, s);
+      const double inv = 1.0 / sqrt(sum / d + a.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * w[i];
+    }
+    if (turned) {
+      float c[4], s[4];
+      if (pos < a.rows) {
+        Elem<DT_F32>::load4(a.cos_sin, static_cast<int64_t>(pos) * rot + 4 * u, c);
+        Elem<DT_F32>::load4(a.cos_sin, static_cast<int64_t>(pos) * rot + rot / 2 + 4 * u, s);
+      }
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double p = y[2 * i], q = y[2 * i + 1];
+          y[2 * i] = p * c[i] - q * s[i];
+          y[2 * i + 1] = q * c[i] + p * s[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double p = y[i], q = y[4 + i];
+          y[i] = p * c[i] - q * s[i];
+          y[4 + i] = q * c[i] + p * s[i];
+        }
+      }
+    }
+    const bool beyond = rot > 0 && pos >= a.rows;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = beyond ? __uint_as_float(0x7FC00000u) : Elem<DT>::round(y[i]);
+  }
+  if (CACHE && !is_q) {
+    if (!is_v && live) {
+      float* mine = stage + (threadIdx.x / G) * (G * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine[lo + i] = x[i], mine[hi + i] = x[4 + i];
+      // the row's lanes are one wave's, whose LDS accesses are in order
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = mine[8 * u + i];
+    }
+    if (live) put_row(r.cache, slot, head, is_v, d, u, x);
+    return;
+  }
+  if (live) {
+    void* dst = is_q ? a.q_out : a.k_out;
+    const int64_t to = is_q ? t * a.qo_token + head * a.qo_head : t * a.ko_token + head * a.ko_head;
+    Elem<DT>::store4(dst, to + lo, x);
+    Elem<DT>::store4(dst, to + hi, x + 4);
+  }
+}
+
+struct ReadArgs {
+  ar_kv4_rows_args a;
+  Cache cache;
+  int head_dim;
+};
+
+template <int DT, int G>
+__global__ __launch_bounds__(kRowThreads) void read_rows(ReadArgs r) {
+  const ar_kv4_rows_args& a = r.a;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
+  const int u = threadIdx.x % G, d = r.head_dim, per_token = 2 * r.cache.heads;
+  const int t = static_cast<int>(row / per_token);
+  if (t >= a.ntokens || u * 8 >= d) return;
+  const int h = static_cast<int>(row - static_cast<int64_t>(t) * per_token);
+  const bool value = h >= r.cache.heads;
+  const int head = value ? h - r.cache.heads : h;
+  const int64_t slot = a.slots[t];
+  float x[8] = {};
+  if (slot >= 0 && (slot >> r.cache.page_shift) < r.cache.num_pages) {
+    const int page = 1 << r.cache.page_shift, off = static_cast<int>(slot) & (page - 1);
+    const int64_t part = ((slot >> r.cache.page_shift) * r.cache.heads + head) * 2 + value;
+    const int at = value ? (off >> 2) * (d * 2) + u * 16 + (off & 3) * 4 : off * (d / 2) + u * 4;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(r.cache.data + part * (page * (d / 2)) + at);
+    const float scale = scale_of(r.cache.scales[part * (page * (d / 32)) + (u >> 2) * page + off]);
+    const uint32_t p[4] = {
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(p[i]), x[2 * i + 1] = bf16_hi(p[i]);
+  }
+  void* dst = value ? a.v : a.k;
+  const int64_t to = (value ? t * a.v_token + head * a.v_head : t * a.k_token + head * a.k_head) + 8 * u;
+  Elem<DT>::store4(dst, to, x);
+  Elem<DT>::store4(dst, to + 4, x + 4);
+}
+
+inline int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+
+template <bool CACHE>
+int launch_norm_rope(const RowArgs& r, hipStream_t stream) {
+  const int g = lanes_of(r.a.head_dim);
+  const int64_t rows = static_cast<int64_t>(r.a.ntokens) * (r.a.q_heads + r.a.kv_heads + r.values);
+  if (rows == 0) return AR_OK;
+  const int64_t blocks = (rows + kRowThreads / g - 1) / (kRowThreads / g);
+  if (blocks > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kRowThreads);
+#define ARD_LAUNCH(DT, G) hipLaunchKernelGGL((norm_rope<DT, G, CACHE>), grid, block, 0, stream, r)
+  if (r.a.dtype == AR_BFLOAT16) {
+    if (g == 8) ARD_LAUNCH(DT_BF16, 8); else if (g == 16) ARD_LAUNCH(DT_BF16, 16); else ARD_LAUNCH(DT_BF16, 32);
+  } else {
+    if (g == 8) ARD_LAUNCH(DT_F32, 8); else if (g == 16) ARD_LAUNCH(DT_F32, 16); else ARD_LAUNCH(DT_F32, 32);
+  }
+#undef ARD_LAUNCH
+  AR_HIP(hipGetLastError());
+  return AR_OK;
+}
+
+// Base address and strides of a [tokens][heads][head_dim] tensor in units of four elements.
+int check_rows(const char* name, const void* p, int64_t token, int64_t head, int heads, int dtype) {
+  if (heads == 0) return AR_OK;
+  if (p == nullptr) return ar_fail(AR_EINVAL, "null %s", name);
+  if (!aligned(p, dtype == AR_BFLOAT16 ? 8 : 16) || token % 4 != 0 || head % 4 != 0)
+    return ar_fail(AR_EINVAL, "%s: address and strides must be multiples of 4 elements", name);
+  if (token < 0 || head < 0) return ar_fail(AR_EINVAL, "%s: negative stride", name);
+  return AR_OK;
+}
+
+int check_norm_rope(const ar_qk_norm_rope_args* a) {
+  if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
+  if (int rc = check_dtype(a->dtype)) return rc;
+  if (a->ntokens < 0 || a->q_heads < 0 || a->kv_heads < 0) return ar_fail(AR_EINVAL, "negative size");
+  if (a->q_heads > 65536 || a->kv_heads > 65536) return ar_fail(AR_ETOOBIG, "too many heads");
+  if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8 != 0)
+    return ar_fail(AR_EINVAL, "head_dim must be a multiple of 8 in [8, 256], got %d", a->head_dim);
+  if (a->rot < 0 || a->rot > a->head_dim || a->rot % 8 != 0)
+    return ar_fail(AR_EINVAL, "rot must be a multiple of 8 in [0, head_dim], got %d", a->rot);
+  if (!(a->eps >= 0)) return ar_fail(AR_EINVAL, "eps must not be negative");
+  if (a->ntokens == 0) return AR_OK;
+  if (a->rot > 0 && (a->positions == nullptr || a->cos_sin == nullptr || a->rows < 1))
+    return ar_fail(AR_EINVAL, "a rotation needs positions and cos_sin");
+  if (a->rot > 0 && !aligned(a->cos_sin, 16)) return ar_fail(AR_EINVAL, "cos_sin is not 16-byte aligned");
+  const uintptr_t w = a->dtype == AR_BFLOAT16 ? 8 : 16;
+  if (!aligned(a->q_weight, w) || !aligned(a->k_weight, w))
+    return ar_fail(AR_EINVAL, "a weight's address must be a multiple of 4 elements");
+  if (int rc = check_rows("q", a->q, a->q_token, a->q_head, a->q_heads, a->dtype)) return rc;
+  if (int rc = check_rows("k", a->k, a->k_token, a->k_head, a->kv_heads, a->dtype)) return rc;
+  if (int rc = check_rows("q_out", a->q_out, a->qo_token, a->qo_head, a->q_heads, a->dtype)) return rc;
+  if (a->q_heads > 0 && a->q == a->q_out && (a->q_token != a->qo_token || a->q_head != a->qo_head))
+    return ar_fail(AR_EINVAL, "q in place needs equal strides");
+  return AR_OK;
+}
+
+Cache cache_of(const ar_kv4* h, uint8_t* data, uint8_t* scales, int64_t num_pages) {
+  return Cache{data, scales, num_pages, h->heads, h->page_shift};
+}
+
+int check_kv_rows(const ar_kv4* h, const ar_kv4_rows_args* a) {
+  if (int rc = check_handle(h)) return rc;
+  if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
+  if (int rc = check_dtype(a->dtype)) return rc;
+  if (a->ntokens < 0) return ar_fail(AR_EINVAL, "negative size");
+  if (int rc = check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (a->ntokens == 0) return AR_OK;
+  if (a->slots == nullptr) return ar_fail(AR_EINVAL, "null slots");
+  if (int rc = check_rows("k", a->k, a->k_token, a->k_head, h->heads, a->dtype)) return rc;
+  return check_rows("v", a->v, a->v_token, a->v_head, h->heads, a->dtype);
+}
+
+}  // namespace ard
+
+extern "C" {
+
+int ar_qk_norm_rope(const ar_qk_norm_rope_args* a, void* stream) {
+  if (int rc = ard::check_norm_rope(a)) return rc;
+  if (a->ntokens > 0) {
+    if (int rc = ard::check_rows("k_out", a->k_out, a->ko_token, a->ko_head, a->kv_heads, a->dtype)) return rc;
+    if (a->kv_heads > 0 && a->k == a->k_out && (a->k_token != a->ko_token || a->k_head != a->ko_head))
+      return ar_fail(AR_EINVAL, "k in place needs equal strides");
+  }
+  ard::RowArgs r{*a, {}, 0};
+  return ard::launch_norm_rope<false>(r, static_cast<hipStream_t>(stream));
+}
+
+int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stream) {
+  if (int rc = ard::check_handle(h)) return rc;
+  if (int rc = ard::check_norm_rope(a)) return rc;
+  if (a->kv_heads != h->heads || a->head_dim != h->head_dim)
+    return ar_fail(AR_EINVAL, "the handle is for %d kv heads of %d, got %d of %d", h->heads, h->head_dim,
+                   a->kv_heads, a->head_dim);
+  if (int rc = ard::check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (a->ntokens > 0) {
+    if (a->slots == nullptr) return ar_fail(AR_EINVAL, "null slots");
+    if (int rc = ard::check_rows("v", a->v, a->v_token, a->v_head, a->kv_heads, a->dtype)) return rc;
+  }
+  ard::RowArgs r{*a, ard::cache_of(h, a->data, a->scales, a->num_pages), a->kv_heads};
+  return ard::launch_norm_rope<true>(r, static_cast<hipStream_t>(stream));
+}
+
+int ar_kv4_append(ar_kv4* h, const ar_kv4_rows_args* a, void* stream) {
+  if (int rc = ard::check_kv_rows(h, a)) return rc;
+  ard::RowArgs r{};
+  r.a.k = a->k, r.a.v = a->v, r.a.slots = a->slots;
+  r.a.k_token = a->k_token, r.a.k_head = a->k_head, r.a.v_token = a->v_token, r.a.v_head = a->v_head;
+  r.a.dtype = a->dtype, r.a.ntokens = a->ntokens, r.a.kv_heads = h->heads, r.a.head_dim = h->head_dim;
+  r.cache = ard::cache_of(h, a->data, a->scales, a->num_pages);
+  r.values = h->heads;
+  return ard::launch_norm_rope<true>(r, static_cast<hipStream_t>(stream));
+}
+
+int ar_kv4_read(ar_kv4* h, const ar_kv4_rows_args* a, void* stream) {
+  if (int rc = ard::check_kv_rows(h, a)) return rc;
+  const int g = ard::lanes_of(h->head_dim);
+  const int64_t rows = static_cast<int64_t>(a->ntokens) * 2 * h->heads;
+  if (rows == 0) return AR_OK;
+  const int64_t blocks = (rows + ard::kRowThreads / g - 1) / (ard::kRowThreads / g);
+  if (blocks > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  const dim3 grid(static_cast<unsigned>(blocks)), block(ard::kRowThreads);
+  const ard::ReadArgs r{*a, ard::cache_of(h, a->data, a->scales, a->num_pages), h->head_dim};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+#define ARD_LAUNCH(DT, G) hipLaunchKernelGGL((ard::read_rows<ard::DT, G>), grid, block, 0, s, r)
+  if (a->dtype == AR_BFLOAT16) {
+    if (g == 8) ARD_LAUNCH(DT_BF16, 8); else if (g == 16) ARD_LAUNCH(DT_BF16, 16); else ARD_LAUNCH(DT_BF16, 32);
+  } else {
+    if (g == 8) ARD_LAUNCH(DT_F32, 8); else if (g == 16) ARD_LAUNCH(DT_F32, 16); else ARD_LAUNCH(DT_F32, 32);
+  }
+#undef ARD_LAUNCH
+  AR_HIP(hipGetLastError());
+  return AR_OK;
+}
+
+}  // extern "C"
