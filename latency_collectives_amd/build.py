@@ -2,7 +2,8 @@
 
     python -m latency_collectives_amd.build
 
-compiles every ``csrc/*.hip`` file with hipcc into ``latency_collectives_amd/libar.so``.
+compiles every ``csrc/*.hip`` (collectives) and ``csrc_decode/*.hip`` (decode operators) file with
+hipcc into ``latency_collectives_amd/libar.so``.
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_DECODE = os.path.join(PKG, "csrc_decode")
 LIB = os.path.join(PKG, "libar.so")
 ARCH = os.environ.get("AR_OFFLOAD_ARCH", "gfx950")
 
@@ -31,7 +33,7 @@ HIPCC_FLAGS = [
 
 
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    return sorted(f for d in (CSRC, CSRC_DECODE) for f in glob.glob(os.path.join(d, "*.hip")))
 
 
 def build(verbose: bool = False) -> str:

@@ -6,8 +6,8 @@
 #include <stdint.h>
 
 #include "../../include/ar_decode.h"
-#include "ar_device.h"
-#include "ar_internal.h"
+#include "../csrc/ar_device.h"
+#include "../csrc/ar_internal.h"
 
 namespace ard {
 
