@@ -10,4 +10,13 @@ AllReduces of a decode step over its own heads (page tables, norm and rotation o
 
 from ._ar import *  # noqa: F401,F403
 from ._ar import ArError, lib  # noqa: F401
+from . import _decode
 from ._decode import *  # noqa: F401,F403
+
+
+def __getattr__(name):
+    # the compiled calls load with their first use
+    if name in _decode.DECODE_EXPORTS:
+        globals()[name] = getattr(_decode, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

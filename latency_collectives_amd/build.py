@@ -1,9 +1,10 @@
-"""Build the HIP library (libar.so) for gfx950 in-tree.
+"""Build the HIP library (libar.so) for gfx950 in-tree, and the binding of the decode operators.
 
     python -m latency_collectives_amd.build
 
 compiles every ``csrc/*.hip`` (collectives) and ``csrc_decode/*.hip`` (decode operators) file with
-hipcc into ``latency_collectives_amd/libar.so``.
+hipcc into ``latency_collectives_amd/libar.so``, and ``csrc_decode/ar_decode_bind.cpp`` (host code
+against torch's headers) with the C++ compiler into ``latency_collectives_amd/_decode_calls.so``.
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 CSRC_DECODE = os.path.join(PKG, "csrc_decode")
 LIB = os.path.join(PKG, "libar.so")
+CALLS = os.path.join(PKG, "_decode_calls.so")
 ARCH = os.environ.get("AR_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -66,13 +68,43 @@ def build(verbose: bool = False) -> str:
                         sys.stderr.write(q.stdout + q.stderr)
                 raise RuntimeError("hipcc failed to build libar.so")
     os.replace(tmp, LIB)
+    build_calls(verbose)
     return LIB
 
 
+def build_calls(verbose: bool = False) -> str:
+    """Compile the binding of the decode operators (libar.so must be there) and return its path."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    # -D: what the HIP headers and torch's ask of a plain C++ compiler
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", "/opt/rocm/include", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC_DECODE, "ar_decode_bind.cpp"), "-o", tmp, "-L", PKG, "-lar",
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the C++ compiler failed to build _decode_calls.so")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def ensure_built() -> str:
-    """Build only when no library exists yet (tests and tools call this)."""
+    """Build only what does not exist yet (tests and tools call this)."""
     if not os.path.exists(LIB):
         build()
+    elif not os.path.exists(CALLS):
+        build_calls()
     return LIB
 
 
