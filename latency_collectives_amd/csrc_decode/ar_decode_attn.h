@@ -9,24 +9,31 @@ struct AttnArgs {
   ar_kv4_attention_args a;
   Cache cache;
   int group;          // query heads of a kv head
-  int target_shift;   // the work is cut into about 2^target_shift items
+  int room;           // tokens that a row of the table holds
+  // The work split: units of `unit` tokens (32 << tile_shift), of which a row sees at most
+  // most_seen; at most `runs` runs.
+  uint32_t most_seen, unit, runs;
+  int unit_shift, tile_shift;
+  int job_units;      // what starting and ending a job costs, in units
   float scale_log2;   // scale * log2(e)
   uint8_t* part;      // partial sums [slot][row][head_dim], then {max, sum} [slot][row]
   uint32_t part_bytes;
   uint32_t stats_at;  // byte offset of the {max, sum} pairs in `part`
-  uint32_t* arrived;  // [slot of a job's first part]: parts done
+  uint32_t* arrived;  // [workgroup of a job's first part]: parts done
 };
 
 // Rows (tokens x heads of a group) of a query tile are 16 * columns.
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 
-typedef void (*attn_fn)(AttnArgs);
-attn_fn select_attn_bf16(int head_dim, int columns);
-attn_fn select_attn_f32(int head_dim, int columns);
+// A kernel and the workgroups of it that fill the device's 256 compute units.
+struct AttnKernel {
+  void (*fn)(AttnArgs);
+  int fill;
+};
+AttnKernel select_attn_bf16(int head_dim, int columns);
+AttnKernel select_attn_f32(int head_dim, int columns);
 
-// Items a launch is cut into (before rounding up per job), as a power of two: what fills the
-// device's 256 compute units at the occupancy of the variant.
-constexpr int target_shift(int columns) { return columns == 1 ? 10 : 9; }
+constexpr int kMostRuns = 1024;
 
 }  // namespace ard

@@ -25,13 +25,17 @@ int pick_columns(const ar_kv4* h, const ar_kv4_attention_args* a) {
   return n;
 }
 
-// Partial results of a launch: at most two slots an item of the split, each R rows of head_dim
-// sums and a {max, sum} pair.
+// Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each R
+// rows of head_dim sums and a {max, sum} pair.
 size_t part_bytes(int columns, int head_dim) {
-  return (size_t(2) << ard::target_shift(columns)) * 16 * columns * (head_dim + 2) * sizeof(float);
+  return size_t(2) * ard::kMostRuns * 16 * columns * (head_dim + 2) * sizeof(float);
 }
 
-constexpr size_t kArrivedBytes = (size_t(2) << 10) * sizeof(uint32_t);
+constexpr size_t kArrivedBytes = ard::kMostRuns * sizeof(uint32_t);
+
+// Finding a job, its queries and its end take about what eight units of 32 tokens take while the
+// whole device reads; without them in the split, a run of many short requests ended last.
+constexpr int kJobUnits = 8;
 
 }  // namespace
 
@@ -115,22 +119,35 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   args.cache = Cache{const_cast<uint8_t*>(a->data), const_cast<uint8_t*>(a->scales), a->num_pages,
                      h->heads, h->page_shift};
   args.group = a->q_heads / h->heads;
-  args.target_shift = target_shift(columns);
   args.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
   args.part = static_cast<uint8_t*>(h->work);
   args.part_bytes = static_cast<uint32_t>(part_bytes(columns, h->head_dim));
-  args.stats_at = (2u << args.target_shift) * 16 * columns * h->head_dim * 4;
+  args.stats_at = 2u * kMostRuns * 16 * columns * h->head_dim * 4;
   args.arrived = reinterpret_cast<uint32_t*>(args.part + h->work_bytes);
-  // Jobs: query tiles x kv heads. Cutting them into parts of equal length gives at most
-  // 2^target_shift parts more than that; workgroups beyond the parts that exist end at once.
-  const int64_t tiles = static_cast<int64_t>(a->ntokens) * args.group / (16 * columns) +
-                        std::min(a->nreq, a->ntokens);
-  const int64_t grid = tiles * h->heads + (int64_t(1) << args.target_shift);
-  if (grid > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  attn_fn fn = a->dtype == AR_BFLOAT16 ? select_attn_bf16(h->head_dim, columns)
-                                       : select_attn_f32(h->head_dim, columns);
-  if (fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
-  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0,
+  // As many workgroups as the device holds at once, of at least four units of 32 tokens each: fewer
+  // where the requests cannot have more. Larger units where 32-bit sums of them could overflow.
+  const int rows_per_tile = 16 * columns;
+  const int64_t room = std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FFFFFE0);
+  int64_t seen = room;
+  // what a tile's rows see with a window: their tokens and the start's rounding down to 32
+  if (a->window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(a->window) + rows_per_tile / args.group + 33);
+  const int64_t tiles = static_cast<int64_t>(a->ntokens) * args.group / rows_per_tile + std::min(a->nreq, a->ntokens);
+  if (tiles * rows_per_tile > 0x7FFFFFFF || tiles * h->heads > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  args.room = static_cast<int>(room);
+  args.most_seen = static_cast<uint32_t>(seen);
+  args.unit_shift = 5;
+  const auto span = [&] { return ((seen + (1 << args.unit_shift) - 1) >> args.unit_shift) + kJobUnits; };
+  while (span() * (tiles * h->heads) > 0x7FFFFFFF) ++args.unit_shift;
+  args.unit = 1u << args.unit_shift;
+  args.tile_shift = args.unit_shift - 5;
+  args.job_units = kJobUnits;
+  const int64_t runs = (tiles * h->heads * span() + kAttnWaves - 1) / kAttnWaves;
+  const AttnKernel k = a->dtype == AR_BFLOAT16 ? select_attn_bf16(h->head_dim, columns)
+                                               : select_attn_f32(h->head_dim, columns);
+  if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
+  const int64_t grid = std::min<int64_t>(std::min(k.fill, kMostRuns), runs);
+  args.runs = static_cast<uint32_t>(grid);
+  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0,
                      static_cast<hipStream_t>(stream), args);
   AR_HIP(hipGetLastError());
   return AR_OK;

@@ -4,16 +4,16 @@
 
 namespace ard {
 
-attn_fn select_attn_bf16(int head_dim, int columns) {
+AttnKernel select_attn_bf16(int head_dim, int columns) {
 #define ARD_CASE(D, NQ, OCC) \
-  if (head_dim == D && columns == NQ) return kv4_attention<DT_BF16, D, NQ, OCC>
-  ARD_CASE(64, 1, 4);
+  if (head_dim == D && columns == NQ) return {kv4_attention<DT_BF16, D, NQ, OCC>, 256 * OCC}
+  ARD_CASE(64, 1, 3);
   ARD_CASE(64, 2, 2);
   ARD_CASE(64, 4, 1);
-  ARD_CASE(96, 1, 4);
+  ARD_CASE(96, 1, 3);
   ARD_CASE(96, 2, 2);
   ARD_CASE(96, 4, 1);
-  ARD_CASE(128, 1, 4);
+  ARD_CASE(128, 1, 3);
   ARD_CASE(128, 2, 2);
   ARD_CASE(128, 4, 1);
   ARD_CASE(192, 1, 2);
@@ -21,7 +21,7 @@ attn_fn select_attn_bf16(int head_dim, int columns) {
   ARD_CASE(256, 1, 2);
   ARD_CASE(256, 2, 1);
 #undef ARD_CASE
-  return nullptr;
+  return {nullptr, 0};
 }
 
 }  // namespace ard

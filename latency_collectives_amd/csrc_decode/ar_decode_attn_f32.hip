@@ -5,19 +5,19 @@
 
 namespace ard {
 
-attn_fn select_attn_f32(int head_dim, int columns) {
+AttnKernel select_attn_f32(int head_dim, int columns) {
 #define ARD_CASE(D, NQ, OCC) \
-  if (head_dim == D && columns == NQ) return kv4_attention<DT_F32, D, NQ, OCC>
+  if (head_dim == D && columns == NQ) return {kv4_attention<DT_F32, D, NQ, OCC>, 256 * OCC}
   ARD_CASE(64, 1, 3);
   ARD_CASE(64, 2, 2);
-  ARD_CASE(96, 1, 3);
-  ARD_CASE(96, 2, 2);
+  ARD_CASE(96, 1, 2);
+  ARD_CASE(96, 2, 1);
   ARD_CASE(128, 1, 2);
   ARD_CASE(128, 2, 1);
   ARD_CASE(192, 1, 1);
   ARD_CASE(256, 1, 1);
 #undef ARD_CASE
-  return nullptr;
+  return {nullptr, 0};
 }
 
 }  // namespace ard

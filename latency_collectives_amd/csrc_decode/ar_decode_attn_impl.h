@@ -16,11 +16,14 @@
 // by the conversion, exactly; no LDS is used before the join.
 //
 // Work. A job is a tile of query rows (16 * NQ: tokens x heads of the group) of one request and kv
-// head. The tokens a job sees are cut into parts of equal length for all jobs, chosen by every
-// workgroup from the requests' lengths so that about 2^target_shift parts exist; a workgroup takes
-// one part, its four waves every fourth 32-token tile. A job of several parts leaves partial sums
-// in the workspace and the last workgroup to arrive joins them in the order of the tokens, so the
-// result does not depend on who came last. Nothing waits for another workgroup.
+// head; its tokens are 32-token units. All jobs' units in one row are cut into equal runs, one run a
+// workgroup, whose four waves take every fourth unit. A run may end one job, hold whole ones and
+// begin another, so every workgroup reads the same number of bytes whatever the requests' lengths
+// are (64 requests of up to 8192 tokens, 8 kv heads of 128, 285 MB: 85 us with one part of a job a
+// workgroup, which left a second, half-empty round of workgroups; 63 us so). A job
+// of several workgroups leaves partial sums in the workspace and the last one to arrive joins them
+// in the order of the tokens, so the result does not depend on who came last. Nothing waits for
+// another workgroup.
 #pragma once
 
 #include "ar_decode_attn.h"
@@ -86,13 +89,30 @@ __device__ __forceinline__ void split(const float* x, bf16x8* out) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-struct Job {
-  int request, tile, head, chunk;
-  int slot;      // workspace slot of this part, its job's first is slot - chunk
-  int per_part;  // 32-token tiles of a part
-};
+// Inclusive prefix sum over the wave's lanes, saturating.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+#define ARD_STEP(CTRL, ROWS)                  \
+  x = __builtin_elementwise_add_sat(          \
+      x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false)));
+  ARD_STEP(0x111, 0xF) ARD_STEP(0x112, 0xF) ARD_STEP(0x114, 0xF) ARD_STEP(0x118, 0xF)  // row_shr 1, 2, 4, 8
+  ARD_STEP(0x142, 0xA) ARD_STEP(0x143, 0xC)  // the last lane of a row of 16, of two rows
+#undef ARD_STEP
+  return x;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#define ARD_STEP(CTRL, ROWS) \
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false)));
+  ARD_STEP(0x111, 0xF) ARD_STEP(0x112, 0xF) ARD_STEP(0x114, 0xF) ARD_STEP(0x118, 0xF)
+  ARD_STEP(0x142, 0xA) ARD_STEP(0x143, 0xC)
+#undef ARD_STEP
+  return __builtin_amdgcn_readlane(static_cast<int>(x), 63);
+}
+__device__ __forceinline__ int lane_value(uint32_t x, int lane) {
+  return __builtin_amdgcn_readlane(static_cast<int>(x), lane);
+}
 
-// A request's cost as the work split sees it: tiles of rows, parts of a tile.
+// A request as the split sees it: tiles of rows, and their units: the tokens that a tile may see and,
+// after them, what starting and ending a job costs in units.
 struct Cost {
   int q0, m, kv;
   int tiles, span;
@@ -101,77 +121,92 @@ struct Cost {
 template <int R>
 __device__ __forceinline__ Cost cost_of(const AttnArgs& args, int b) {
   const ar_kv4_attention_args& a = args.a;
-  Cost c = {0, 0, 0, 0, 0};
+  Cost c = {0, 0, 0, 0, 1};
   if (b < a.nreq) {
-    c.q0 = min(max(a.q_start[b], 0), a.ntokens);
-    c.m = max(min(a.q_start[b + 1], a.ntokens) - c.q0, 0);
+    const int at = a.q_start[b], to = a.q_start[b + 1];
     c.kv = max(a.kv_len[b], 0);
-    c.tiles = static_cast<int>((static_cast<int64_t>(c.m) * args.group + R - 1) / R);
-    const int64_t most = static_cast<int64_t>(a.table_width) << args.cache.page_shift;
-    int64_t seen = c.kv < most ? c.kv : most;
-    if (a.window > 0) {
-      // a tile's rows are at most R / group + 1 tokens, its range starts at a multiple of 32
-      const int64_t far = static_cast<int64_t>(a.window) + R / args.group + 1 + 32;
-      seen = seen < far ? seen : far;
-    }
-    c.span = static_cast<int>((seen + 31) >> 5);
+    c.q0 = min(max(at, 0), a.ntokens);
+    c.m = max(min(to, a.ntokens) - c.q0, 0);
+    c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+    const uint32_t seen = min(static_cast<uint32_t>(c.kv), args.most_seen);
+    c.span = static_cast<int>((seen + args.unit - 1) >> args.unit_shift) + args.job_units;
   }
   return c;
 }
 
-// The part of the work that workgroup `item` does; false where there is none. Every wave computes
-// it alone (lanes are requests), with no barrier.
+// Where a workgroup is in its run: a job and the units of it.
+struct Run {
+  int request, tile, head;
+  int at;    // the job's first unit of this run
+  int left;  // units of the run from there on
+  int per;   // units of a run
+};
+
+// The run of workgroup `w`; false where there is none. Every wave computes it alone (lanes are
+// requests), with no barrier. This code runs once, from a cold instruction cache, before anything
+// else: it is kept short (32-bit sums; the host picks units large enough for them).
 template <int R>
-__device__ __forceinline__ bool find_job(const AttnArgs& args, int item, Job& job, Cost& mine) {
-  const int lane = threadIdx.x & 63, n = args.a.nreq, heads = args.cache.heads;
-  int64_t total = 0;
-  Cost c = cost_of<R>(args, lane);
-  for (int b = 0; b < n; b += 64) {
-    const Cost x = b == 0 ? c : cost_of<R>(args, b + lane);
-    total += static_cast<int64_t>(x.tiles) * x.span;
+__device__ __forceinline__ bool find_run(const AttnArgs& args, int w, Run& run, Cost& mine) {
+  const int lane = threadIdx.x & 63, heads = args.cache.heads;
+  uint32_t total = 0, longest = 0;
+  Cost c;
+  uint32_t upto;
+  for (int b = (args.a.nreq - 1) & ~63; b >= 0; b -= 64) {  // ends with the first requests at hand
+    c = cost_of<R>(args, b + lane);
+    upto = wave_scan(static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span));
+    total = __builtin_elementwise_add_sat(total, static_cast<uint32_t>(lane_value(upto, 63)));
+    longest = max(longest, wave_max(c.tiles > 0 ? c.span : 0));
   }
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
-  total *= heads;
-  const int64_t each = (total + (int64_t(1) << args.target_shift) - 1) >> args.target_shift;
-  // a tile of 32 tokens for each wave at least
-  const int per = static_cast<int>(max<int64_t>(kAttnWaves, (each + kAttnWaves - 1) / kAttnWaves * kAttnWaves));
-  int64_t items = 0, slots = 0;
-  for (int b = 0; b < n; b += 64) {
-    const Cost x = b == 0 ? c : cost_of<R>(args, b + lane);
-    const int parts = max(1, (x.span + per - 1) / per);
-    const int64_t jobs = static_cast<int64_t>(x.tiles) * heads;
-    const int64_t my_items = jobs * parts, my_slots = parts > 1 ? my_items : 0;
-    int64_t upto = my_items, slot_upto = my_slots;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int64_t y = __shfl_up(upto, s), z = __shfl_up(slot_upto, s);
-      if (lane >= s) upto += y, slot_upto += z;
-    }
-    const uint64_t hit = __ballot(items + upto > item);
-    if (hit != 0) {
-      const int who = __builtin_ctzll(hit);
-      const int at = item - static_cast<int>(items + __shfl(upto - my_items, who));
-      const int tiles = __shfl(x.tiles, who), count = __shfl(parts, who);
-      job.request = uniform(b + who);
-      // neighbouring workgroups (on the eight XCDs in turn) take neighbouring heads, and the
-      // tiles with the longest ranges come first
-      const int rest = at / heads;
-      job.head = uniform(at - rest * heads);
-      job.chunk = uniform(rest / tiles);
-      job.tile = uniform(tiles - 1 - (rest - rest / tiles * tiles));
-      job.slot = uniform(static_cast<int>(slots + __shfl(slot_upto - my_slots, who)) +
-                         (job.tile * heads + job.head) * count + job.chunk);
-      job.per_part = uniform(per);
-      mine.q0 = uniform(__shfl(x.q0, who));
-      mine.m = uniform(__shfl(x.m, who));
-      mine.kv = uniform(__shfl(x.kv, who));
-      return true;
-    }
-    items += __shfl(upto, 63);
-    slots += __shfl(slot_upto, 63);
+  // Only request starts that overlap reach this: nothing is done.
+  if (total > 0x7FFFFFFFu) return false;
+  // A unit for each wave at least, and no more parts of a job than units of a part: reading a part
+  // back costs about what a unit does where few jobs leave the device idle.
+  const int least = max((total + args.runs - 1) / args.runs,
+                        static_cast<uint32_t>(uniform(static_cast<int>(sqrtf(static_cast<float>(longest))))));
+  run.per = max(kAttnWaves, (least + kAttnWaves - 1) & ~(kAttnWaves - 1));
+  if (static_cast<uint64_t>(w) * run.per >= total) return false;
+  uint32_t from = w * run.per;
+  run.left = min(run.per, static_cast<int>(total - from));
+  int b = 0;
+  while (__ballot(upto > from) == 0) {
+    from -= lane_value(upto, 63);
+    b += 64;
+    c = cost_of<R>(args, b + lane);
+    upto = wave_scan(static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span));
   }
-  return false;
+  const int who = __builtin_ctzll(__ballot(upto > from));
+  run.request = b + who;
+  mine.q0 = lane_value(c.q0, who), mine.m = lane_value(c.m, who), mine.kv = lane_value(c.kv, who);
+  mine.tiles = lane_value(c.tiles, who), mine.span = lane_value(c.span, who);
+  from += static_cast<uint32_t>(mine.tiles * heads) * static_cast<uint32_t>(mine.span) - lane_value(upto, who);
+  // Jobs in the order of the heads, a head's tiles side by side: they share its keys.
+  const uint32_t job = from / static_cast<uint32_t>(mine.span);
+  run.at = uniform(from - job * mine.span);
+  run.head = uniform(job), run.tile = 0;
+  if (mine.tiles > 1) {
+    run.head = uniform(job / static_cast<uint32_t>(mine.tiles));
+    run.tile = uniform(job - run.head * mine.tiles);
+  }
+  return true;
+}
+
+// The next job of the run.
+template <int R>
+__device__ __forceinline__ void next_job(const AttnArgs& args, Run& run, Cost& mine) {
+  run.at = 0;
+  if (++run.tile < mine.tiles) return;
+  run.tile = 0;
+  if (++run.head < args.cache.heads) return;
+  run.head = 0;
+  do {
+    if (++run.request >= args.a.nreq) {  // only if lengths change under the call
+      run.left = 0;
+      return;
+    }
+    mine = cost_of<R>(args, run.request);
+    mine.tiles = uniform(mine.tiles);
+  } while (mine.tiles == 0);
+  mine.q0 = uniform(mine.q0), mine.m = uniform(mine.m), mine.kv = uniform(mine.kv), mine.span = uniform(mine.span);
 }
 
 // Any byte above kMaxScale (252) in a word of scale bytes.
@@ -217,54 +252,101 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   __shared__ int last;
 
   const ar_kv4_attention_args& a = args.a;
-  Job job;
+  const int w = blockIdx.x;
+  Run run;
   Cost me;
-  if (!find_job<R>(args, blockIdx.x, job, me)) return;
+  if (!find_run<R>(args, w, run, me)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int group = args.group, shift = args.cache.page_shift;
+  const float per_group = 1.0f / group;
 
+  // Per-lane offsets within a page's K and V.
+  const int page = 1 << shift;
+  const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
+  const int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
+  const int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
+  const int num_pages = static_cast<int>(args.cache.num_pages);
+  const int k_group = (g * kDw) >> 2;  // 32-group of a lane's first K dword
+  const int k_off = c * (D / 2) + g * (D / 8);
+  int v_off[kSets], vs_off[kSets];
+#pragma unroll
+  for (int e = 0; e < kSets; ++e) {
+    const int chunk = min(e * 16 + c, NC - 1);  // lanes beyond the row repeat its last chunk
+    v_off[e] = k_bytes + g * (D * 2) + chunk * 16;
+    vs_off[e] = s_bytes + (chunk >> 2) * page + g * 4;
+  }
+
+  for (;;) {
   // Rows of this tile and what each sees.
   const int rows = me.m * group;
-  const int row0 = job.tile * R;
-  const int i0 = row0 / group, i1 = (min(row0 + R, rows) - 1) / group;
-  const int64_t room = static_cast<int64_t>(a.table_width) << shift;
-  const int kv_end = static_cast<int>(min<int64_t>(me.kv, room));
+  const int row0 = run.tile * R;
+  int i0 = 0;
+  if (run.tile > 0) i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group));
+  const int rem0 = row0 - i0 * group;
+  // token and head in the group of row row0 + r: rem0 + r is below 2^17, exact in binary32
+  auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * per_group); };
+  const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
+  const int kv_end = min(me.kv, args.room);
   const int first_pos = me.kv - me.m;  // position of the request's first new token
   const int end = min(max(first_pos + i1 + 1, 0), kv_end);
   int begin = 0;
   if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
   const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
-  const int parts = max(1, (ntiles + job.per_part - 1) / job.per_part);
-  if (job.chunk >= parts) return;
-  const int t_first = job.chunk * job.per_part, t_last = min(t_first + job.per_part, ntiles);
+  const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
+  const int taken = min(run.left, me.span - run.at);  // units of the run in this job
+  const int t_first = run.at << args.tile_shift;
+  const int t_last = min((run.at + taken) << args.tile_shift, ntiles);
+  run.left -= taken;
+  // Parts of the job: part 0 is the workgroup that holds its first unit, slot 2 * (that) + 1; the
+  // others hold nothing before it in their runs, slot 2 * (theirs).
+  int before = 0, first_units = taken;  // parts before this one, units of part 0
+  if (run.at > 0) {
+    before = uniform(static_cast<uint32_t>(run.at + run.per - 1) / static_cast<uint32_t>(run.per));
+    first_units = run.at - (before - 1) * run.per;
+  }
+  const int first_wg = w - before;
+  int parts = 1;
+  if (nunits > first_units)
+    parts = 1 + uniform(static_cast<uint32_t>(nunits - first_units + run.per - 1) / static_cast<uint32_t>(run.per));
+  if (run.at == 0 || t_first < ntiles) {
+  const uint8_t* data = args.cache.data + static_cast<int64_t>(run.head) * 2 * k_bytes;
+  const uint8_t* scales = args.cache.scales + static_cast<int64_t>(run.head) * 2 * s_bytes;
+  const int32_t* table = a.table + run.request * a.table_stride;
+
+  // Pages of this wave's next 32 tiles, lane 2 k + u the u-th half of the k-th; -1 where there is
+  // nothing to see. One load a tile would make the wave wait for its keys and values with it.
+  auto pages = [&](int tile) {
+    const int mine = tile + (lane >> 1) * kAttnWaves, t = begin + mine * 32 + (lane & 1) * 16;
+    int p = -1;
+    if (mine < t_last && t < end) p = table[t >> shift];
+    return p < num_pages ? p : -1;
+  };
+  int ids = pages(t_first + wave);  // under way with the queries
 
   int hi[NQ], lo[NQ];
   bf16x8 q[NQ][PARTS][kDw];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int row = row0 + n * 16 + c;
-    const bool real = row < rows;
-    const int i = real ? row / group : 0;
+    const bool real = row < rows;  // others repeat the last row, with nothing to see
+    const int r = min(n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
     const int pos = first_pos + i;
     hi[n] = real ? min(pos + 1, kv_end) : 0;
     lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
     const int64_t at = static_cast<int64_t>(me.q0 + i) * a.q_token +
-                       static_cast<int64_t>(job.head * group + (real ? row - i * group : 0)) * a.q_head + g * (D / 4);
+                       static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head + g * (D / 4);
 #pragma unroll
     for (int s = 0; s < kDw; ++s) {
       if (DT == DT_BF16) {
-        u32x4 w = {0, 0, 0, 0};
-        if (real) w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at + s * 8);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at + s * 8);
         q[n][0][s] = __builtin_bit_cast(bf16x8, w);
       } else {
-        float x[8] = {};
-        if (real) {
-          const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at + s * 8);
-          const f32x4 v0 = p[0], v1 = p[1];
+        float x[8];
+        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at + s * 8);
+        const f32x4 v0 = p[0], v1 = p[1];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = v0[j], x[4 + j] = v1[j];
-        }
+        for (int j = 0; j < 4; ++j) x[j] = v0[j], x[4 + j] = v1[j];
         bf16x8 w[PARTS];
         split<PARTS>(x, w);
 #pragma unroll
@@ -288,41 +370,11 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
   }
 
-  // Per-lane offsets within a page's K and V.
-  const int page = 1 << shift;
-  const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
-  int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
-  int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
-  const uint8_t* data = args.cache.data + static_cast<int64_t>(job.head) * 2 * k_bytes;
-  const uint8_t* scales = args.cache.scales + static_cast<int64_t>(job.head) * 2 * s_bytes;
-  const int32_t* table = a.table + job.request * a.table_stride;
-  const int num_pages = static_cast<int>(args.cache.num_pages);
-  const int k_group = (g * kDw) >> 2;  // 32-group of a lane's first K dword
-  int k_off = c * (D / 2) + g * (D / 8);
-  int v_off[kSets], vs_off[kSets];
-#pragma unroll
-  for (int e = 0; e < kSets; ++e) {
-    const int chunk = min(e * 16 + c, NC - 1);  // lanes beyond the row repeat its last chunk
-    v_off[e] = k_bytes + g * (D * 2) + chunk * 16;
-    vs_off[e] = s_bytes + (chunk >> 2) * page + g * 4;
-  }
-
-  // Pages of a tile's two halves; -1: nothing to see there.
-  auto pages = [&](int tile, int* id) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int t = begin + tile * 32 + u * 16;
-      int p = -1;
-      if (tile < t_last && t < end) p = table[t >> shift];
-      p = uniform(p);
-      id[u] = p >= 0 && p < num_pages ? p : -1;
-    }
-  };
   auto load = [&](int tile, const int* id, Tile& x) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int off = (begin + tile * 32 + u * 16) & (page - 1);
-      const int64_t p = max(id[u], 0);
+      const int64_t p = max(id[u], 0);  // a valid place, for loads that nothing uses
       const uint8_t* kd = data + p * page_bytes + off * (D / 2);
       const uint8_t* sd = scales + p * page_scales + off;
       load_dwords<kDw>(kd + k_off, x.k[u]);
@@ -337,17 +389,21 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
     }
   };
 
-  int id[2], id_next[2];
+  // The first round only loads: one copy of this code.
+  int id[2] = {-1, -1}, id_next[2];
   Tile now, next;
-  int tile = t_first + wave;
-  pages(tile, id);
-  load(tile, id, now);
-  pages(tile + kAttnWaves, id_next);
-
+  int tile = t_first + wave - kAttnWaves;
+  int ids_after = -1, turn = 0;
   for (; tile < t_last; tile += kAttnWaves) {
+    if ((turn & 31) == 0) {
+      if (turn > 0) ids = ids_after;
+      ids_after = pages(tile + 33 * kAttnWaves);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) id_next[u] = __builtin_amdgcn_readlane(ids, 2 * (turn & 31) + u);
+    ++turn;
     load(tile + kAttnWaves, id_next, next);
-    int id_after[2];
-    pages(tile + 2 * kAttnWaves, id_after);
+    if (tile >= t_first) {
 
     const int t0 = begin + tile * 32;
     // Scores.
@@ -470,9 +526,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       ARD_PAIR(0) ARD_PAIR(1) ARD_PAIR(2) ARD_PAIR(3)
 #undef ARD_PAIR
     }
+    }
     now = next;
     id[0] = id_next[0], id[1] = id_next[1];
-    id_next[0] = id_after[0], id_next[1] = id_after[1];
   }
 
   // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
@@ -485,6 +541,24 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   __syncthreads();
   const int seg_per = NC;  // eight elements a thread
   const bool alone = parts == 1;
+  // Eight elements of row r from its sums, and its logarithm.
+  auto finish = [&](int r, int seg, f32x4 o0, f32x4 o1, float top, float rl) {
+    const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
+    const int64_t token = me.q0 + i;
+    const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
+    o0 *= inv, o1 *= inv;
+    const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
+    if (DT == DT_BF16) {
+      const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
+                       ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
+    }
+    if (seg == 0 && a.lse != nullptr)
+      a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+  };
   const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -492,6 +566,16 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
 #pragma unroll
     for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][n * 16 + c]);
     const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
+    if (__any(nan_groups[n] != 0)) {
+#pragma unroll
+      for (int e = 0; e < kSets; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (nan_groups[n] >> ((e * 16 + g * 4 + i) >> 2) & 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[n][e][j][i] = __uint_as_float(0x7FC00000u);
+          }
+    }
     float* mine = join + (wave * 16 + c) * kPitch;
 #pragma unroll
     for (int e = 0; e < kSets; ++e)
@@ -499,12 +583,11 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       for (int i = 0; i < 4; ++i) {
         const int chunk = e * 16 + g * 4 + i;
         if (chunk < NC) {
-          const float nan = nan_groups[n] >> (chunk >> 2) & 1 ? __uint_as_float(0x7FC00000u) : 0.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             f32x4 v;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = acc[n][e][4 * h + j][i] * f + nan;
+            for (int j = 0; j < 4; ++j) v[j] = acc[n][e][4 * h + j][i] * f;
             *reinterpret_cast<f32x4*>(mine + chunk * 8 + 4 * h) = v;
           }
         }
@@ -525,79 +608,95 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       }
       if (row >= rows) continue;
       if (!alone) {
-        const uint32_t at = static_cast<uint32_t>(job.slot * R + n * 16 + r);
+        const uint32_t at = static_cast<uint32_t>((2 * w + (before == 0)) * R + n * 16 + r);
         ar::st16<ar::kCoh>(part, (at * D + seg * 8) * 4, __builtin_bit_cast(u32x4, o0));
         ar::st16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4, __builtin_bit_cast(u32x4, o1));
         if (seg == 0)
           ar::st8<ar::kCoh>(part, args.stats_at + at * 8, u32x2{__float_as_uint(rm), __float_as_uint(rl)});
         continue;
       }
-      const int i = row / group, head = job.head * group + row - i * group;
-      const int64_t token = me.q0 + i;
-      const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
-      o0 *= inv, o1 *= inv;
-      const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
-      if (DT == DT_BF16) {
-        const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
-                         ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
-      } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
-      }
-      if (seg == 0 && a.lse != nullptr)
-        a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (rm + log2f(rl)) * 0.6931471805599453f;
+      finish(n * 16 + r, seg, o0, o1, rm, rl);
     }
     if (n + 1 < NQ) __syncthreads();
   }
-  if (alone) return;
-
+  if (!alone) {
   // Parts: write-through stores are done before the arrival is counted; the last one joins.
   ar::wait_all_mem();
   __syncthreads();
-  const int job_slot = job.slot - job.chunk;
   if (tid == 0) {
-    const uint32_t before = __hip_atomic_fetch_add(args.arrived + job_slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = __hip_atomic_fetch_add(args.arrived + first_wg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     last = before + 1 == static_cast<uint32_t>(parts);
-    if (last) __hip_atomic_store(args.arrived + job_slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (last) __hip_atomic_store(args.arrived + first_wg, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!last) return;
-  for (int x = tid; x < R * seg_per; x += kAttnThreads) {
-    const int r = x / seg_per, seg = x - r * seg_per, row = row0 + r;
-    if (row >= rows) continue;
-    const uint32_t at0 = static_cast<uint32_t>(job_slot * R + r);
-    float top = -INFINITY;
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p)
-      top = fmaxf(top, __uint_as_float(ar::ld8<ar::kCoh>(part, args.stats_at + (at0 + p * R) * 8).x));
-    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
-    float rl = 0.0f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const uint32_t at = at0 + p * R;
-      const u32x2 st = ar::ld8<ar::kCoh>(part, args.stats_at + at * 8);
-      const f32x4 v0 = __builtin_bit_cast(f32x4, ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4));
-      const f32x4 v1 = __builtin_bit_cast(f32x4, ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4));
-      const float f = top == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st.x) - top);
-      rl += __uint_as_float(st.y) * f;
-      o0 += v0 * f, o1 += v1 * f;
+  if (last) {
+    // A thread reads eight elements of a row from every part, or from every `groups`-th where
+    // threads are left over; eight parts are under way at once.
+    const int items = min(R, rows - row0) * seg_per;
+    int groups = 1;
+    while (groups * 2 * items <= kAttnThreads && groups * 8 < parts) groups *= 2;
+    for (int x0 = 0; x0 < items * groups; x0 += kAttnThreads) {
+      const int x = x0 + tid, mine = x / items, y = x - mine * items;
+      const int r = y / seg_per, seg = y - r * seg_per;
+      float top = -INFINITY, rl = 0.0f;
+      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+      for (int p0 = mine; p0 < parts && mine < groups; p0 += 8 * groups) {
+        constexpr int N = 8;
+        u32x2 st[N];
+        u32x4 v0[N], v1[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int p = min(p0 + k * groups, parts - 1);
+          // slot of part p > 0 is 2 * (first_wg + p), of part 0 one more than 2 * first_wg
+          const uint32_t at = static_cast<uint32_t>((2 * (first_wg + p) + (p == 0)) * R + r);
+          st[k] = ar::ld8<ar::kCoh>(part, args.stats_at + at * 8);
+          v0[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4);
+          v1[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4);
+        }
+        float to = top;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (p0 + k * groups >= parts) st[k].x = 0xFF800000u;  // -infinity
+          to = fmaxf(to, __uint_as_float(st[k].x));
+        }
+        const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
+        o0 *= f0, o1 *= f0, rl *= f0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float f = to == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[k].x) - to);
+          rl += __uint_as_float(st[k].y) * f;
+          o0 += __builtin_bit_cast(f32x4, v0[k]) * f, o1 += __builtin_bit_cast(f32x4, v1[k]) * f;
+        }
+        top = to;
+      }
+      if (groups > 1) {  // one round of the outer loop: the groups' sums meet in LDS
+        if (x < items * groups) {
+          float* p = join + x * 12;
+          *reinterpret_cast<f32x4*>(p) = o0;
+          *reinterpret_cast<f32x4*>(p + 4) = o1;
+          p[8] = top, p[9] = rl;
+        }
+        __syncthreads();
+        if (x < items)
+          for (int k = 1; k < groups; ++k) {
+            const float* p = join + (k * items + x) * 12;
+            const float to = fmaxf(top, p[8]);
+            const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
+            const float f1 = to == -INFINITY ? 0.0f : exp2_fast(p[8] - to);
+            o0 = o0 * f0 + *reinterpret_cast<const f32x4*>(p) * f1;
+            o1 = o1 * f0 + *reinterpret_cast<const f32x4*>(p + 4) * f1;
+            rl = rl * f0 + p[9] * f1, top = to;
+          }
+      }
+      if (x < items) finish(r, seg, o0, o1, top, rl);
     }
-    const int i = row / group, head = job.head * group + row - i * group;
-    const int64_t token = me.q0 + i;
-    const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
-    o0 *= inv, o1 *= inv;
-    const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
-    if (DT == DT_BF16) {
-      const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
-                       ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
-    } else {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
-    }
-    if (seg == 0 && a.lse != nullptr)
-      a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+  }
+  }
+  }
+  if (run.left <= 0) return;
+  next_job<R>(args, run, me);
+  if (run.left <= 0) return;
+  __syncthreads();  // the next job's joins use the same LDS
   }
 }
 
