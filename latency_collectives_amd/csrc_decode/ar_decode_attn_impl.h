@@ -89,16 +89,6 @@ __device__ __forceinline__ void split(const float* x, bf16x8* out) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Inclusive prefix sum over the wave's lanes, saturating.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
-#define ARD_STEP(CTRL, ROWS)                  \
-  x = __builtin_elementwise_add_sat(          \
-      x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false)));
-  ARD_STEP(0x111, 0xF) ARD_STEP(0x112, 0xF) ARD_STEP(0x114, 0xF) ARD_STEP(0x118, 0xF)  // row_shr 1, 2, 4, 8
-  ARD_STEP(0x142, 0xA) ARD_STEP(0x143, 0xC)  // the last lane of a row of 16, of two rows
-#undef ARD_STEP
-  return x;
-}
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 #define ARD_STEP(CTRL, ROWS) \
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false)));
