@@ -33,9 +33,9 @@ size_t part_bytes(int columns, int head_dim) {
 
 constexpr size_t kArrivedBytes = ard::kMostRuns * sizeof(uint32_t);
 
-// Finding a job, its queries and its end take about what eight units of 32 tokens take while the
+// Finding a job, its queries and its end take about what twelve units of 32 tokens take while the
 // whole device reads; without them in the split, a run of many short requests ended last.
-constexpr int kJobUnits = 8;
+constexpr int kJobUnits = 12;
 
 }  // namespace
 

@@ -3,17 +3,27 @@
 //
 // A row (one head of one token, 64..256 elements) belongs to 8, 16 or 32 neighbouring lanes, eight
 // elements a lane, so everything a row needs (its sum of squares, the largest element of each 32)
-// is a few cross-lane steps and each byte of HBM moves once.
+// is a few cross-lane steps and each byte of HBM moves once. A group of lanes takes `run`
+// neighbouring heads of one token, four rows' loads under way at once; the token's cosines and the
+// weights are read and widened once for them.
 //
 // Arithmetic of the norm and the rotation is 64-bit: gfx950's binary64 rate is that of unpacked
 // binary32, the kernel is bound by bytes (or by its launch), and what is rounded to bfloat16 and
 // then to 4 bits no longer depends on the order of the sum of squares.
+//
+// Measured, 8191 tokens of 32 + 8 heads of 128 in bfloat16 (172 MB): 41 us, 4.2 TB/s; one row a group
+// with a 64-bit division for its place and a library square root and reciprocal was bound by its
+// instructions (56 us).
+
+#include <type_traits>
 
 #include "ar_decode.h"
 
 namespace ard {
 
 constexpr int kRowThreads = 256;
+// Workgroups below which rows are spread over more of them.
+constexpr int kFewBlocks = 2048;
 
 template <int DT>
 struct Elem;
@@ -78,115 +88,154 @@ __device__ __forceinline__ void put_row(const Cache& c, int64_t slot, int head, 
   if ((u & 3) == 0) c.scales[part * (page * (d / 32)) + (u >> 2) * page + off] = static_cast<uint8_t>(byte);
 }
 
+// Sum over the G lanes of a row, the same in each.
+template <int G>
+__device__ __forceinline__ double row_total(double x) {
+  auto step = [&](auto ctrl) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), decltype(ctrl)::value, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), decltype(ctrl)::value, 0xF, 0xF, false);
+    x += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+  };
+  step(std::integral_constant<int, 0xB1>());   // lane ^ 1
+  step(std::integral_constant<int, 0x4E>());   // lane ^ 2
+  step(std::integral_constant<int, 0x141>());  // mirrored within 8
+  if (G >= 16) step(std::integral_constant<int, 0x140>());  // mirrored within 16
+  if (G >= 32) x += __shfl_xor(x, 16);
+  return x;
+}
+
+// 1 / sqrt(a): the instruction's estimate and two Newton steps, each squaring its error.
+__device__ __forceinline__ double inverse_root(double a) {
+  double y = __builtin_amdgcn_rsq(a);
+  if (y > 0.0) {  // not for an infinity, whose inverse root is 0, nor for NaN
+    y = fma(y, fma(-0.5 * a * y, y, 0.5), y);
+    y = fma(y, fma(-0.5 * a * y, y, 0.5), y);
+  }
+  return y;
+}
+
 struct RowArgs {
   ar_qk_norm_rope_args a;
   Cache cache;
-  int values;  // rows of v a token (kv_heads with a cache, else 0)
+  double per_dim;  // 1 / head_dim
+  int values;      // rows of v a token (kv_heads with a cache, else 0)
+  int run;         // rows that a group of lanes takes
+  int q_runs, k_runs;  // blocks in y: q's runs of heads, then k's, then v's
 };
 
 // G lanes a row. CACHE: keys and values go into the cache, else keys to k_out.
 template <int DT, int G, bool CACHE>
 __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
+  constexpr int B = 4;  // rows whose loads are under way at once
   const ar_qk_norm_rope_args& a = r.a;
   // A rotated row's elements pass through LDS on their way to the cache: the rotation pairs
   // elements half a row apart, the cache's groups are consecutive.
   __shared__ float stage[CACHE ? kRowThreads * 8 : 1];
   const int d = a.head_dim, rot = a.rot;
-  const int per_token = a.q_heads + a.kv_heads + r.values;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
+  const int by = blockIdx.y;
+  const bool is_q = by < r.q_runs, is_v = by >= r.q_runs + r.k_runs;
+  const int head0 = (is_q ? by : is_v ? by - r.q_runs - r.k_runs : by - r.q_runs) * r.run;
+  const int head1 = min(head0 + r.run, is_q ? a.q_heads : is_v ? r.values : a.kv_heads);
   const int u = threadIdx.x % G;
-  const int t = static_cast<int>(row / per_token);
-  const int h = static_cast<int>(row - static_cast<int64_t>(t) * per_token);
+  const int t = static_cast<int>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
   if (t >= a.ntokens) return;
-  const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
-  const int head = is_q ? h : is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
   const int32_t pos = a.positions != nullptr ? a.positions[t] : 0;
   int64_t slot = -1;
   if (CACHE && !is_q) slot = a.slots[t];
-  if (pos < 0) return;
-  if (CACHE && !is_q && (slot < 0 || (slot >> r.cache.page_shift) >= r.cache.num_pages)) return;
   const void* src = is_q ? a.q : is_v ? a.v : a.k;
-  const int64_t from = is_q ? t * a.q_token + head * a.q_head
-                     : is_v ? t * a.v_token + head * a.v_head
-                            : t * a.k_token + head * a.k_head;
+  const int64_t head_step = is_q ? a.q_head : is_v ? a.v_head : a.k_head;
+  int64_t from = t * (is_q ? a.q_token : is_v ? a.v_token : a.k_token) + head0 * head_step;
+  void* dst = is_q ? a.q_out : a.k_out;
+  const int64_t to_step = is_q ? a.qo_head : a.ko_head;
+  int64_t to = t * (is_q ? a.qo_token : a.ko_token) + head0 * to_step;
   const bool live = u * 8 < d;
   const bool turned = !is_v && u * 8 < rot;
   // A lane's two runs of four elements: both ends of its pairs.
   const bool halves = turned && !a.interleaved;
-  const int lo = halves ? 4 * u : 8 * u, hi = halves ? rot / 2 + 4 * u : 8 * u + 4;
-  float x[8];
+  const int lo = !live ? 0 : halves ? 4 * u : 8 * u, hi = !live ? 4 : halves ? rot / 2 + 4 * u : 8 * u + 4;
+  float x[B][8];
+  auto load = [&](int n) {  // rows from `from` on; places past the last repeat it
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-  if (live) {
-    Elem<DT>::load4(src, from + lo, x);
-    Elem<DT>::load4(src, from + hi, x + 4);
-  }
-  if (!is_v) {
-    double y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-    const void* weight = is_q ? a.q_weight : a.k_weight;
-    if (weight != nullptr) {
-      float w[8] = {};
-      if (live) {
-        Elem<DT>::load4(weight, lo, w);
-        Elem<DT>::load4(weight, hi, w + 4);
-      }
-      double sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma(y[i], y[i], sum);
-#pragma unroll
-      for (int s = 1; s < G; s <<= 1) sum += __shfl_xor(sum, s);
-      const double inv = 1.0 / sqrt(sum / d + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * w[i];
+    for (int i = 0; i < B; ++i) {
+      const int64_t at = from + min(i, n - 1) * head_step;
+      Elem<DT>::load4(src, at + lo, x[i]);
+      Elem<DT>::load4(src, at + hi, x[i] + 4);
     }
-    if (turned) {
-      float c[4], s[4];
-      if (pos < a.rows) {
-        Elem<DT_F32>::load4(a.cos_sin, static_cast<int64_t>(pos) * rot + 4 * u, c);
-        Elem<DT_F32>::load4(a.cos_sin, static_cast<int64_t>(pos) * rot + rot / 2 + 4 * u, s);
-      }
-      if (a.interleaved) {
+  };
+  load(head1 - head0);
+  if (pos < 0) return;
+  if (CACHE && !is_q && (slot < 0 || (slot >> r.cache.page_shift) >= r.cache.num_pages)) return;
+  const void* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+  const bool beyond = !is_v && rot > 0 && pos >= a.rows;
+  double w[8], c[4], s[4];
+  if (weight != nullptr) {
+    float f[8];
+    Elem<DT>::load4(weight, lo, f);
+    Elem<DT>::load4(weight, hi, f + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const double p = y[2 * i], q = y[2 * i + 1];
-          y[2 * i] = p * c[i] - q * s[i];
-          y[2 * i + 1] = q * c[i] + p * s[i];
+    for (int i = 0; i < 8; ++i) w[i] = f[i];
+  }
+  if (turned) {
+    float f[8];
+    const int64_t at = static_cast<int64_t>(beyond ? 0 : pos) * rot + 4 * u;
+    Elem<DT_F32>::load4(a.cos_sin, at, f);
+    Elem<DT_F32>::load4(a.cos_sin, at + rot / 2, f + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f[i], s[i] = f[4 + i];
+  }
+  for (int head = head0;;) {
+    const int n = min(B, head1 - head);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (i >= n) break;
+      if (!is_v && (weight != nullptr || turned || beyond)) {
+        double y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = x[i][j];
+        if (weight != nullptr) {
+          double sum = 0.0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum = fma(y[j], y[j], sum);
+          const double inv = inverse_root(fma(row_total<G>(live ? sum : 0.0), r.per_dim, a.eps));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = y[j] * inv * w[j];
         }
-      } else {
+        if (turned) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const double p = y[i], q = y[4 + i];
-          y[i] = p * c[i] - q * s[i];
-          y[4 + i] = q * c[i] + p * s[i];
+          for (int j = 0; j < 4; ++j) {
+            const double p = a.interleaved ? y[2 * j] : y[j], q = a.interleaved ? y[2 * j + 1] : y[4 + j];
+            const double yp = p * c[j] - q * s[j], yq = q * c[j] + p * s[j];
+            // what follows takes the pairs side by side or apart, as they were loaded
+            if (a.interleaved) y[2 * j] = yp, y[2 * j + 1] = yq;
+            else y[j] = yp, y[4 + j] = yq;
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = beyond ? __uint_as_float(0x7FC00000u) : Elem<DT>::round(y[j]);
+      }
+      if (CACHE && !is_q) {
+        if (halves) {
+          float* mine = stage + (threadIdx.x / G) * (G * 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mine[lo + j] = x[i][j], mine[hi + j] = x[i][4 + j];
+          // the row's lanes are one wave's, whose LDS accesses are in order
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[i][j] = mine[8 * u + j];
+        }
+        if (live) put_row(r.cache, slot, head + i, is_v, d, u, x[i]);
+      } else if (live) {
+        Elem<DT>::store4(dst, to + i * to_step + lo, x[i]);
+        Elem<DT>::store4(dst, to + i * to_step + hi, x[i] + 4);
       }
     }
-    const bool beyond = rot > 0 && pos >= a.rows;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = beyond ? __uint_as_float(0x7FC00000u) : Elem<DT>::round(y[i]);
-  }
-  if (CACHE && !is_q) {
-    if (!is_v && live) {
-      float* mine = stage + (threadIdx.x / G) * (G * 8);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mine[lo + i] = x[i], mine[hi + i] = x[4 + i];
-      // the row's lanes are one wave's, whose LDS accesses are in order
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = mine[8 * u + i];
-    }
-    if (live) put_row(r.cache, slot, head, is_v, d, u, x);
-    return;
-  }
-  if (live) {
-    void* dst = is_q ? a.q_out : a.k_out;
-    const int64_t to = is_q ? t * a.qo_token + head * a.qo_head : t * a.ko_token + head * a.ko_head;
-    Elem<DT>::store4(dst, to + lo, x);
-    Elem<DT>::store4(dst, to + hi, x + 4);
+    head += B;
+    if (head >= head1) return;
+    from += B * head_step, to += B * to_step;
+    load(head1 - head);
   }
 }
 
@@ -199,13 +248,11 @@ struct ReadArgs {
 template <int DT, int G>
 __global__ __launch_bounds__(kRowThreads) void read_rows(ReadArgs r) {
   const ar_kv4_rows_args& a = r.a;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
-  const int u = threadIdx.x % G, d = r.head_dim, per_token = 2 * r.cache.heads;
-  const int t = static_cast<int>(row / per_token);
+  const int u = threadIdx.x % G, d = r.head_dim;
+  const int t = static_cast<int>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
   if (t >= a.ntokens || u * 8 >= d) return;
-  const int h = static_cast<int>(row - static_cast<int64_t>(t) * per_token);
-  const bool value = h >= r.cache.heads;
-  const int head = value ? h - r.cache.heads : h;
+  const bool value = blockIdx.y >= r.cache.heads;
+  const int head = value ? blockIdx.y - r.cache.heads : blockIdx.y;
   const int64_t slot = a.slots[t];
   float x[8] = {};
   if (slot >= 0 && (slot >> r.cache.page_shift) < r.cache.num_pages) {
@@ -230,14 +277,28 @@ __global__ __launch_bounds__(kRowThreads) void read_rows(ReadArgs r) {
 
 inline int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
 
+// Heads that a group of lanes takes, of `heads`: eight, half as many while the launch would not give
+// every compute unit a few workgroups (then one row a group: latency counts).
+int pick_run(int64_t tokens, int rows, int g) {
+  const int64_t blocks = (tokens * g + kRowThreads - 1) / kRowThreads;
+  int run = 8;
+  while (run > 1 && blocks * ((rows + run - 1) / run) < kFewBlocks) run /= 2;
+  return run;
+}
+
 template <bool CACHE>
-int launch_norm_rope(const RowArgs& r, hipStream_t stream) {
+int launch_norm_rope(RowArgs& r, hipStream_t stream) {
   const int g = lanes_of(r.a.head_dim);
-  const int64_t rows = static_cast<int64_t>(r.a.ntokens) * (r.a.q_heads + r.a.kv_heads + r.values);
-  if (rows == 0) return AR_OK;
-  const int64_t blocks = (rows + kRowThreads / g - 1) / (kRowThreads / g);
-  if (blocks > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kRowThreads);
+  const int rows = r.a.q_heads + r.a.kv_heads + r.values;
+  if (r.a.ntokens == 0 || rows == 0) return AR_OK;
+  r.per_dim = 1.0 / r.a.head_dim;
+  r.run = pick_run(r.a.ntokens, rows, g);
+  const auto runs = [&](int heads) { return (heads + r.run - 1) / r.run; };
+  r.q_runs = runs(r.a.q_heads), r.k_runs = runs(r.a.kv_heads);
+  const int in_y = r.q_runs + r.k_runs + runs(r.values);
+  if (in_y > 65535) return ar_fail(AR_ETOOBIG, "too many heads");
+  const int each = kRowThreads / g;
+  const dim3 grid((r.a.ntokens + each - 1) / each, in_y), block(kRowThreads);
 #define ARD_LAUNCH(DT, G) hipLaunchKernelGGL((norm_rope<DT, G, CACHE>), grid, block, 0, stream, r)
   if (r.a.dtype == AR_BFLOAT16) {
     if (g == 8) ARD_LAUNCH(DT_BF16, 8); else if (g == 16) ARD_LAUNCH(DT_BF16, 16); else ARD_LAUNCH(DT_BF16, 32);
@@ -311,7 +372,7 @@ int ar_qk_norm_rope(const ar_qk_norm_rope_args* a, void* stream) {
     if (a->kv_heads > 0 && a->k == a->k_out && (a->k_token != a->ko_token || a->k_head != a->ko_head))
       return ar_fail(AR_EINVAL, "k in place needs equal strides");
   }
-  ard::RowArgs r{*a, {}, 0};
+  ard::RowArgs r{*a, {}, 0.0, 0, 0, 0, 0};
   return ard::launch_norm_rope<false>(r, static_cast<hipStream_t>(stream));
 }
 
@@ -326,7 +387,7 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
     if (a->slots == nullptr) return ar_fail(AR_EINVAL, "null slots");
     if (int rc = ard::check_rows("v", a->v, a->v_token, a->v_head, a->kv_heads, a->dtype)) return rc;
   }
-  ard::RowArgs r{*a, ard::cache_of(h, a->data, a->scales, a->num_pages), a->kv_heads};
+  ard::RowArgs r{*a, ard::cache_of(h, a->data, a->scales, a->num_pages), 0.0, a->kv_heads, 0, 0, 0};
   return ard::launch_norm_rope<true>(r, static_cast<hipStream_t>(stream));
 }
 
@@ -344,11 +405,9 @@ int ar_kv4_append(ar_kv4* h, const ar_kv4_rows_args* a, void* stream) {
 int ar_kv4_read(ar_kv4* h, const ar_kv4_rows_args* a, void* stream) {
   if (int rc = ard::check_kv_rows(h, a)) return rc;
   const int g = ard::lanes_of(h->head_dim);
-  const int64_t rows = static_cast<int64_t>(a->ntokens) * 2 * h->heads;
-  if (rows == 0) return AR_OK;
-  const int64_t blocks = (rows + ard::kRowThreads / g - 1) / (ard::kRowThreads / g);
-  if (blocks > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  const dim3 grid(static_cast<unsigned>(blocks)), block(ard::kRowThreads);
+  if (a->ntokens == 0) return AR_OK;
+  const int each = ard::kRowThreads / g;
+  const dim3 grid((a->ntokens + each - 1) / each, 2 * h->heads), block(ard::kRowThreads);
   const ard::ReadArgs r{*a, ard::cache_of(h, a->data, a->scales, a->num_pages), h->head_dim};
   hipStream_t s = static_cast<hipStream_t>(stream);
 #define ARD_LAUNCH(DT, G) hipLaunchKernelGGL((ard::read_rows<ard::DT, G>), grid, block, 0, s, r)
