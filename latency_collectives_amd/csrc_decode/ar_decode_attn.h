@@ -15,7 +15,9 @@ struct AttnArgs {
   uint32_t most_seen, unit, runs;
   int unit_shift, tile_shift;
   int job_units;      // what starting and ending a job costs, in units
-  float scale_log2;   // scale * log2(e)
+  float scale_log2;   // scale * log2(e); its absolute value for the kernel of many rows
+  uint32_t q_sign;    // there: its sign, over two bfloat16
+  int tile_tokens;    // there: tokens that a tile of rows may touch
   uint8_t* part;      // partial sums [slot][row][head_dim], then {max, sum} [slot][row]
   uint32_t part_bytes;
   uint32_t stats_at;  // byte offset of the {max, sum} pairs in `part`
@@ -33,7 +35,8 @@ struct AttnKernel {
 };
 AttnKernel select_attn_bf16(int head_dim, int columns);
 AttnKernel select_attn_f32(int head_dim, int columns);
-
-constexpr int kMostRuns = 1024;
+// Many rows a request: tiles of 16 * columns rows for each of a workgroup's waves.
+AttnKernel select_attn_rows(int head_dim);
+int rows_columns(int head_dim);
 
 }  // namespace ard

@@ -8,30 +8,36 @@
 
 namespace {
 
-// Query columns (16 rows each) of a tile: as many as the rows of an average request fill, up to
-// what the registers hold. More columns read the cache for more rows at once; columns that stay
-// empty cost their matrix instructions.
-int max_columns(int dtype, int head_dim) {
-  if (dtype == AR_BFLOAT16) return head_dim <= 128 ? 4 : 2;
-  return head_dim <= 128 ? 2 : 1;
-}
+// Rows a request above which tiles of 128 rows are faster than tiles of 32.
+constexpr int kFewRows = 32;
 
-int pick_columns(const ar_kv4* h, const ar_kv4_attention_args* a) {
+// The kernel for a call: a tile of 16 or 32 rows where a request brings that many on average, its
+// four waves on different tokens; tiles of 128 rows beyond, its waves on different rows
+// (bfloat16; binary32, three products for one, stays with the small tiles).
+struct Choice {
+  ard::AttnKernel k;
+  int rows;  // of a tile
+  bool many;
+};
+
+Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
-  const int most = max_columns(a->dtype, h->head_dim);
-  int n = 1;
-  while (n < most && each > 16 * n) n *= 2;
-  return n;
+  const bool bf16 = a->dtype == AR_BFLOAT16;
+  if (bf16 && each > kFewRows) return {ard::select_attn_rows(h->head_dim), 64 * ard::rows_columns(h->head_dim), true};
+  const int columns = each > 16 && (bf16 || h->head_dim <= 128) ? 2 : 1;
+  return {bf16 ? ard::select_attn_bf16(h->head_dim, columns) : ard::select_attn_f32(h->head_dim, columns), 16 * columns,
+          false};
 }
 
-// Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each R
-// rows of head_dim sums and a {max, sum} pair.
-size_t part_bytes(int columns, int head_dim) {
-  return size_t(2) * ard::kMostRuns * 16 * columns * (head_dim + 2) * sizeof(float);
+// Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each
+// `rows` rows of head_dim sums and a {max, sum} pair.
+size_t part_bytes(int runs, int rows, int head_dim) {
+  return size_t(2) * runs * rows * (head_dim + 2) * sizeof(float);
 }
 
-constexpr size_t kArrivedBytes = ard::kMostRuns * sizeof(uint32_t);
+constexpr int kMostRuns = 1024;  // at least every kernel's `fill`
+constexpr size_t kArrivedBytes = kMostRuns * sizeof(uint32_t);
 
 // Finding a job, its queries and its end take about what twelve units of 32 tokens take while the
 // whole device reads; without them in the split, a run of many short requests ended last.
@@ -60,8 +66,11 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
     return nullptr;
   }
   *h = ar_kv4{kv_heads, head_dim, page_size, __builtin_ctz(page_size), nullptr, 0};
-  for (int n = 1; n <= max_columns(AR_BFLOAT16, head_dim); n *= 2)
-    h->work_bytes = std::max(h->work_bytes, part_bytes(n, head_dim));
+  for (int n = 1; n <= 2; ++n)
+    for (const ard::AttnKernel& k : {ard::select_attn_bf16(head_dim, n), ard::select_attn_f32(head_dim, n)})
+      h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
+  h->work_bytes = std::max(h->work_bytes, part_bytes(ard::select_attn_rows(head_dim).fill,
+                                                     64 * ard::rows_columns(head_dim), head_dim));
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -113,21 +122,30 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
     return ar_fail(AR_EINVAL, "negative stride");
   if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
 
-  const int columns = pick_columns(h, a);
+  const Choice choice = choose(h, a);
+  const AttnKernel& k = choice.k;
+  if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
   AttnArgs args;
   args.a = *a;
   args.cache = Cache{const_cast<uint8_t*>(a->data), const_cast<uint8_t*>(a->scales), a->num_pages,
                      h->heads, h->page_shift};
   args.group = a->q_heads / h->heads;
   args.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  args.q_sign = 0;
+  if (choice.many) {
+    if (a->scale < 0) args.q_sign = 0x80008000u;
+    // not zero: a masked score's infinity times it has to stay one
+    args.scale_log2 = std::max(std::fabs(args.scale_log2), 1e-38f);
+  }
   args.part = static_cast<uint8_t*>(h->work);
-  args.part_bytes = static_cast<uint32_t>(part_bytes(columns, h->head_dim));
-  args.stats_at = 2u * kMostRuns * 16 * columns * h->head_dim * 4;
+  args.part_bytes = static_cast<uint32_t>(part_bytes(k.fill, choice.rows, h->head_dim));
+  args.stats_at = 2u * k.fill * choice.rows * h->head_dim * 4;
   args.arrived = reinterpret_cast<uint32_t*>(args.part + h->work_bytes);
   // As many workgroups as the device holds at once, of at least four units of 32 tokens each: fewer
   // where the requests cannot have more. Larger units where 32-bit sums of them could overflow.
-  const int rows_per_tile = 16 * columns;
-  const int64_t room = std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FFFFFE0);
+  const int rows_per_tile = choice.rows;
+  // (below 2^31 by more than a wave looks ahead)
+  const int64_t room = std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
   int64_t seen = room;
   // what a tile's rows see with a window: their tokens and the start's rounding down to 32
   if (a->window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(a->window) + rows_per_tile / args.group + 33);
@@ -140,12 +158,11 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   while (span() * (tiles * h->heads) > 0x7FFFFFFF) ++args.unit_shift;
   args.unit = 1u << args.unit_shift;
   args.tile_shift = args.unit_shift - 5;
+  args.tile_tokens = (rows_per_tile - 1) / args.group + 1;
   args.job_units = kJobUnits;
   const int64_t runs = (tiles * h->heads * span() + kAttnWaves - 1) / kAttnWaves;
-  const AttnKernel k = a->dtype == AR_BFLOAT16 ? select_attn_bf16(h->head_dim, columns)
-                                               : select_attn_f32(h->head_dim, columns);
-  if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
-  const int64_t grid = std::min<int64_t>(std::min(k.fill, kMostRuns), runs);
+  int64_t grid = std::min<int64_t>(k.fill, runs);
+  if (choice.many) grid = (grid + 7) & ~7;  // the same number for every XCD
   args.runs = static_cast<uint32_t>(grid);
   hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0,
                      static_cast<hipStream_t>(stream), args);

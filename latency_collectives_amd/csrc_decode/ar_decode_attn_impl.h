@@ -229,6 +229,104 @@ struct Tile32 {  // a lane's share of 32 tokens, as loaded
   uint32_t vs[2][kSets];
 };
 
+// Eight elements of a row of `out` from its sums, and its logarithm.
+template <int DT>
+__device__ __forceinline__ void finish_row(const ar_kv4_attention_args& a, int64_t token, int head, int seg,
+                                           f32x4 o0, f32x4 o1, float top, float rl) {
+  const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
+  o0 *= inv, o1 *= inv;
+  const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
+  if (DT == DT_BF16) {
+    const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
+                     ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
+  }
+  if (seg == 0 && a.lse != nullptr)
+    a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+}
+
+// Counts this workgroup's part of a job as done; true in the last of `parts`. Write-through stores
+// are done before the arrival is counted.
+__device__ __forceinline__ bool arrive(uint32_t* arrived, int parts, int* last) {
+  ar::wait_all_mem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t before = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *last = before + 1 == static_cast<uint32_t>(parts);
+    if (*last) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *last;
+}
+
+// Joins a job's parts, in the order of the tokens. A thread reads eight elements of a row from
+// every part, or from every `groups`-th where threads are left over; N parts are under way at once.
+template <int D, int R, int N, class F>
+__device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, int first_wg, int parts, int rows,
+                                           float* lds, F finish) {
+  constexpr int NC = D / 8;
+  const int tid = threadIdx.x, items = rows * NC;
+  int groups = 1;
+  while (groups * 2 * items <= kAttnThreads && groups * N < parts) groups *= 2;
+  for (int x0 = 0; x0 < items * groups; x0 += kAttnThreads) {
+    const int x = x0 + tid, mine = x / items, y = x - mine * items;
+    const int r = y / NC, seg = y - r * NC;
+    float top = -INFINITY, rl = 0.0f;
+    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+    for (int p0 = mine; p0 < parts && mine < groups; p0 += 8 * groups) {
+      u32x2 st[N];
+      u32x4 v0[N], v1[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int p = min(p0 + k * groups, parts - 1);
+        // slot of part p > 0 is 2 * (first_wg + p), of part 0 one more than 2 * first_wg
+        const uint32_t at = static_cast<uint32_t>((2 * (first_wg + p) + (p == 0)) * R + r);
+        st[k] = ar::ld8<ar::kCoh>(part, stats_at + at * 8);
+        v0[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4);
+        v1[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4);
+      }
+      float to = top;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (p0 + k * groups >= parts) st[k].x = 0xFF800000u;  // -infinity
+        to = fmaxf(to, __uint_as_float(st[k].x));
+      }
+      const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
+      o0 *= f0, o1 *= f0, rl *= f0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float f = to == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[k].x) - to);
+        rl += __uint_as_float(st[k].y) * f;
+        o0 += __builtin_bit_cast(f32x4, v0[k]) * f, o1 += __builtin_bit_cast(f32x4, v1[k]) * f;
+      }
+      top = to;
+    }
+    if (groups > 1) {  // one round of the outer loop: the groups' sums meet in LDS
+      if (x < items * groups) {
+        float* p = lds + x * 12;
+        *reinterpret_cast<f32x4*>(p) = o0;
+        *reinterpret_cast<f32x4*>(p + 4) = o1;
+        p[8] = top, p[9] = rl;
+      }
+      __syncthreads();
+      if (x < items)
+        for (int k = 1; k < groups; ++k) {
+          const float* p = lds + (k * items + x) * 12;
+          const float to = fmaxf(top, p[8]);
+          const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
+          const float f1 = to == -INFINITY ? 0.0f : exp2_fast(p[8] - to);
+          o0 = o0 * f0 + *reinterpret_cast<const f32x4*>(p) * f1;
+          o1 = o1 * f0 + *reinterpret_cast<const f32x4*>(p + 4) * f1;
+          rl = rl * f0 + p[9] * f1, top = to;
+        }
+    }
+    if (x < items) finish(r, seg, o0, o1, top, rl);
+  }
+}
+
 template <int DT, int D, int NQ, int OCC>
 __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args) {
   constexpr int R = 16 * NQ;
@@ -531,23 +629,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   __syncthreads();
   const int seg_per = NC;  // eight elements a thread
   const bool alone = parts == 1;
-  // Eight elements of row r from its sums, and its logarithm.
   auto finish = [&](int r, int seg, f32x4 o0, f32x4 o1, float top, float rl) {
     const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
-    const int64_t token = me.q0 + i;
-    const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
-    o0 *= inv, o1 *= inv;
-    const int64_t to = token * a.o_token + head * a.o_head + seg * 8;
-    if (DT == DT_BF16) {
-      const u32x4 w = {ar::bf16x2_rne(o0[0], o0[1]), ar::bf16x2_rne(o0[2], o0[3]),
-                       ar::bf16x2_rne(o1[0], o1[1]), ar::bf16x2_rne(o1[2], o1[3])};
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to) = w;
-    } else {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = o0;
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + 4) = o1;
-    }
-    if (seg == 0 && a.lse != nullptr)
-      a.lse[token * a.q_heads + head] = rl == 0.0f ? -INFINITY : (top + log2f(rl)) * 0.6931471805599453f;
+    finish_row<DT>(a, me.q0 + i, head, seg, o0, o1, top, rl);
   };
   const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
 #pragma unroll
@@ -609,79 +693,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
     }
     if (n + 1 < NQ) __syncthreads();
   }
-  if (!alone) {
-  // Parts: write-through stores are done before the arrival is counted; the last one joins.
-  ar::wait_all_mem();
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t before = __hip_atomic_fetch_add(args.arrived + first_wg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = before + 1 == static_cast<uint32_t>(parts);
-    if (last) __hip_atomic_store(args.arrived + first_wg, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (last) {
-    // A thread reads eight elements of a row from every part, or from every `groups`-th where
-    // threads are left over; eight parts are under way at once.
-    const int items = min(R, rows - row0) * seg_per;
-    int groups = 1;
-    while (groups * 2 * items <= kAttnThreads && groups * 8 < parts) groups *= 2;
-    for (int x0 = 0; x0 < items * groups; x0 += kAttnThreads) {
-      const int x = x0 + tid, mine = x / items, y = x - mine * items;
-      const int r = y / seg_per, seg = y - r * seg_per;
-      float top = -INFINITY, rl = 0.0f;
-      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
-      for (int p0 = mine; p0 < parts && mine < groups; p0 += 8 * groups) {
-        constexpr int N = 8;
-        u32x2 st[N];
-        u32x4 v0[N], v1[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int p = min(p0 + k * groups, parts - 1);
-          // slot of part p > 0 is 2 * (first_wg + p), of part 0 one more than 2 * first_wg
-          const uint32_t at = static_cast<uint32_t>((2 * (first_wg + p) + (p == 0)) * R + r);
-          st[k] = ar::ld8<ar::kCoh>(part, args.stats_at + at * 8);
-          v0[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4);
-          v1[k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4);
-        }
-        float to = top;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          if (p0 + k * groups >= parts) st[k].x = 0xFF800000u;  // -infinity
-          to = fmaxf(to, __uint_as_float(st[k].x));
-        }
-        const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
-        o0 *= f0, o1 *= f0, rl *= f0;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float f = to == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[k].x) - to);
-          rl += __uint_as_float(st[k].y) * f;
-          o0 += __builtin_bit_cast(f32x4, v0[k]) * f, o1 += __builtin_bit_cast(f32x4, v1[k]) * f;
-        }
-        top = to;
-      }
-      if (groups > 1) {  // one round of the outer loop: the groups' sums meet in LDS
-        if (x < items * groups) {
-          float* p = join + x * 12;
-          *reinterpret_cast<f32x4*>(p) = o0;
-          *reinterpret_cast<f32x4*>(p + 4) = o1;
-          p[8] = top, p[9] = rl;
-        }
-        __syncthreads();
-        if (x < items)
-          for (int k = 1; k < groups; ++k) {
-            const float* p = join + (k * items + x) * 12;
-            const float to = fmaxf(top, p[8]);
-            const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
-            const float f1 = to == -INFINITY ? 0.0f : exp2_fast(p[8] - to);
-            o0 = o0 * f0 + *reinterpret_cast<const f32x4*>(p) * f1;
-            o1 = o1 * f0 + *reinterpret_cast<const f32x4*>(p + 4) * f1;
-            rl = rl * f0 + p[9] * f1, top = to;
-          }
-      }
-      if (x < items) finish(r, seg, o0, o1, top, rl);
-    }
-  }
-  }
+  if (!alone && arrive(args.arrived + first_wg, parts, &last))
+    join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0), join, finish);
   }
   if (run.left <= 0) return;
   next_job<R>(args, run, me);

@@ -1,0 +1,536 @@
+// Attention over the 4-bit paged cache for many query rows a request (prompt chunks), bfloat16.
+//
+// Mathematics as in ar_decode_attn_impl.h; the products are shared out the other way round: a
+// workgroup's four waves hold 16 * NQ rows each and go through the same tokens together.
+//
+//   S^T = K Q^T   by the scaled 16x16x128 product with K in its 4 bits as stored, the cache's scale
+//                 bytes as the product's own. A query is two e4m3 values, one for its upper four
+//                 significant bits, one for its lower four, each with a scale for 32 elements: all of a
+//                 bfloat16, to 2^-22 of the largest of its 32 for those far below it. Keys need
+//                 no conversion and no LDS.
+//   O^T += V^T P^T  by 16x16x32 products in bfloat16. The scales of V run along the wrong axis
+//                 for the scaled product, so V becomes bfloat16 (exactly), once a workgroup: each
+//                 wave converts a quarter of a round's tokens into LDS in the order of the
+//                 product's operand, for the next round while this one is computed. One barrier a
+//                 round.
+//
+// Work. As there, equal runs of units for as many workgroups as the device holds; the units of a
+// request's tiles grow with the tile (each sees the tokens before it), so they are summed as an
+// arithmetic series. Consecutive runs lie on one XCD: they share keys and values in its L2.
+#pragma once
+
+#include "ar_decode_attn_impl.h"
+
+namespace ard {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// A request as the split sees it: units of tile r (of one head) are below(r + 1) - below(r).
+struct Series {
+  int q0, m, kv, tiles;
+  uint32_t first;     // units of tile 0
+  double half_slope;  // half of what a tile has more than the one before
+  __device__ uint32_t below(int r) const { return static_cast<uint32_t>(r * (first + (r - 1) * half_slope)); }
+};
+
+template <int R>
+__device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
+  const ar_kv4_attention_args& a = args.a;
+  Series c = {0, 0, 0, 0, 1, 0.0};
+  if (b < a.nreq) {
+    const int at = a.q_start[b], to = a.q_start[b + 1];
+    c.kv = max(a.kv_len[b], 0);
+    c.q0 = min(max(at, 0), a.ntokens);
+    c.m = max(min(to, a.ntokens) - c.q0, 0);
+    c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+    const int end = min(c.kv, args.room);
+    const int low = min(max(c.kv - c.m + min(args.tile_tokens, c.m), 0), end);
+    auto units = [&](int seen) {
+      return ((min(static_cast<uint32_t>(seen), args.most_seen) + args.unit - 1) >> args.unit_shift) + args.job_units;
+    };
+    c.first = units(low);
+    if (c.tiles > 1) c.half_slope = static_cast<double>(units(end) - c.first) / (2 * (c.tiles - 1));
+  }
+  return c;
+}
+
+// As find_run, with a job's units in `span`.
+template <int R>
+__device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run, Series& mine, int& span) {
+  const int lane = threadIdx.x & 63, heads = args.cache.heads;
+  uint32_t total = 0;
+  Series c;
+  uint32_t upto;
+  for (int b = (args.a.nreq - 1) & ~63; b >= 0; b -= 64) {
+    c = series_of<R>(args, b + lane);
+    upto = wave_scan(c.below(c.tiles) * heads);
+    total = __builtin_elementwise_add_sat(total, static_cast<uint32_t>(lane_value(upto, 63)));
+  }
+  if (total > 0x7FFFFFFFu) return false;  // request starts that overlap
+  // four units at least: a round of the workgroup
+  run.per = max(4u, (total + args.runs - 1) / args.runs);
+  if (static_cast<uint64_t>(w) * run.per >= total) return false;
+  uint32_t from = w * run.per;
+  run.left = min(run.per, static_cast<int>(total - from));
+  int b = 0;
+  while (__ballot(upto > from) == 0) {
+    from -= lane_value(upto, 63);
+    b += 64;
+    c = series_of<R>(args, b + lane);
+    upto = wave_scan(c.below(c.tiles) * heads);
+  }
+  const int who = __builtin_ctzll(__ballot(upto > from));
+  run.request = b + who;
+  const uint32_t before = who > 0 ? lane_value(upto, who - 1) : 0;
+  mine = series_of<R>(args, run.request);
+  mine.tiles = uniform(mine.tiles);
+  from -= before;
+  const uint32_t head_units = uniform(mine.below(mine.tiles));
+  run.head = uniform(from / head_units);
+  from -= run.head * head_units;
+  // the tile: the root of the series, then to the whole number around it
+  int r = 0;
+  if (mine.tiles > 1) {
+    const double h = mine.half_slope, f = mine.first - h;
+    const double root = h > 0 ? (sqrt(f * f + 4 * h * from) - f) / (2 * h) : from / f;
+    r = min(max(static_cast<int>(root), 0), mine.tiles - 1);
+    while (r > 0 && mine.below(r) > from) --r;
+    while (r + 1 < mine.tiles && mine.below(r + 1) <= from) ++r;
+  }
+  run.tile = uniform(r);
+  run.at = uniform(from - mine.below(r));
+  span = uniform(mine.below(r + 1) - mine.below(r));
+  return true;
+}
+
+// A lane's share of a block of scores' keys: rows of 16 tokens, 32 elements each.
+template <int D>
+struct Keys16 {
+  static constexpr int NB = D / 32;              // groups of 32
+  static constexpr int NM = (2 * NB + 3) / 4;    // products: four groups each, of both parts of q
+  static constexpr int NL = NB % 4 == 0 ? NB / 4 : NM;  // different loads for them
+  u32x4 k[NL];
+  uint32_t s[NL];
+};
+
+template <int D, int NQ, int OCC>
+__global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs args) {
+  constexpr int RW = 16 * NQ, R = RW * kAttnWaves;
+  constexpr int NC = D / 8, kSets = (NC + 15) / 16;
+  constexpr int SUB = kAttnWaves / kSets;  // units of 32 tokens of a round
+  typedef Keys16<D> Keys;
+  constexpr int NB = Keys::NB, NM = Keys::NM, NL = Keys::NL;
+  __shared__ u32x4 values[2][kAttnWaves][8][64];      // [buffer][unit, set][element][lane]
+  __shared__ uint32_t nan_token[2][kAttnWaves][32];   // groups of 32 elements that are NaN
+  __shared__ uint32_t any_nan[2][kAttnWaves];
+  __shared__ int last;
+
+  const ar_kv4_attention_args& a = args.a;
+  // consecutive runs on one XCD: workgroups go to the eight in turn
+  const int w = (blockIdx.x & 7) * (args.runs >> 3) + (blockIdx.x >> 3);
+  Run run;
+  Series me;
+  int span;
+  if (!find_rows<R>(args, w, run, me, span)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int group = args.group, shift = args.cache.page_shift;
+  const float per_group = 1.0f / group;
+  const int page = 1 << shift;
+  const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
+  const int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
+  const int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
+  const int num_pages = static_cast<int>(args.cache.num_pages);
+  // This lane's groups of a key for every load, its values for this wave's share of a round.
+  int k_off[NL], ks_off[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int kb = (4 * i + g) % NB;
+    k_off[i] = c * (D / 2) + kb * 16;
+    ks_off[i] = kb * page + c;
+  }
+  const int my_set = wave % kSets, my_unit = wave / kSets;
+  const int chunk = min(my_set * 16 + c, NC - 1);
+  const int v_off = k_bytes + g * (D * 2) + chunk * 16;
+  const int vs_off = s_bytes + (chunk >> 2) * page + g * 4;
+  const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
+
+  for (;;) {
+    const int rows = me.m * group;
+    const int row0 = run.tile * R;
+    const int i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group)), rem0 = row0 - i0 * group;
+    // token of row row0 + r: rem0 + r is below 2^17, exact in binary32
+    auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * per_group); };
+    const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
+    const int kv_end = min(me.kv, args.room);
+    const int first_pos = me.kv - me.m;
+    const int end = min(max(first_pos + i1 + 1, 0), kv_end);
+    int begin = 0;
+    if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
+    const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
+    const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
+    const int taken = min(run.left, span - run.at);
+    const bool ends = run.at + taken == span;  // the last part takes what the series left out
+    const int t_first = run.at << args.tile_shift;
+    const int t_last = ends ? ntiles : min((run.at + taken) << args.tile_shift, ntiles);
+    run.left -= taken;
+    int before = 0, first_units = taken;
+    if (run.at > 0) {
+      before = uniform(static_cast<uint32_t>(run.at + run.per - 1) / static_cast<uint32_t>(run.per));
+      first_units = run.at - (before - 1) * run.per;
+    }
+    const int first_wg = w - before;
+    int parts = 1;
+    if (min(nunits, span) > first_units)
+      parts = 1 + uniform(static_cast<uint32_t>(min(nunits, span) - first_units + run.per - 1) /
+                          static_cast<uint32_t>(run.per));
+    if (run.at == 0 || t_first < ntiles) {
+      const uint8_t* data = args.cache.data + static_cast<int64_t>(run.head) * 2 * k_bytes;
+      const uint8_t* scales = args.cache.scales + static_cast<int64_t>(run.head) * 2 * s_bytes;
+      const int32_t* table = a.table + run.request * a.table_stride;
+      const int t_begin = begin + t_first * 32, t_end = min(begin + t_last * 32, end);
+
+      // Pages of 64 halves (16 tokens) from half `h` of this part on, one a lane.
+      auto pages = [&](int h) {
+        const int t = t_begin + (h + lane) * 16;
+        int p = -1;
+        if (t < t_end) p = table[t >> shift];
+        return p < num_pages ? p : -1;
+      };
+      int ids = pages(0), ids_next = pages(64), batch = 0;
+      auto page_of = [&](int half) {
+        return __builtin_amdgcn_readlane(half >> 6 == batch ? ids : ids_next, half & 63);
+      };
+
+      // This wave's rows.
+      const int mine0 = row0 + wave * RW;
+      int hi[NQ], lo[NQ];
+      i32x8 q[NQ][NM];
+      int qs[NQ][NM];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        // rows past the last repeat it
+        const int r = min(wave * RW + n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
+        const int pos = first_pos + i;
+        hi[n] = min(pos + 1, kv_end);
+        lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+        const uint16_t* x = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(me.q0 + i) * a.q_token +
+                            static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head;
+#pragma unroll
+        for (int mm = 0; mm < NM; ++mm) {
+          int bytes[2];  // scale bytes of the two groups that this lane holds halves of
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // group 4 mm + 2 h + g / 2 of the upper parts' groups, then the lower parts'
+            const int idx = 4 * mm + 2 * h + (g >> 1);
+            const bool low = idx >= NB;
+            const int kb = idx >= NB ? idx - NB : idx;
+            const u32x4* p = reinterpret_cast<const u32x4*>(x + min(kb, NB - 1) * 32 + (g & 1) * 16);
+            const u32x4 v0 = p[0], v1 = p[1];
+            float f[16];
+            uint32_t most = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t word = (j < 4 ? v0[j & 3] : v1[j & 3]) ^ args.q_sign;
+              f[2 * j] = bf16_lo(word), f[2 * j + 1] = bf16_hi(word);
+              most = max(most, max(word << 16 & 0x7FFFFFFFu, word & 0x7FFF0000u));
+            }
+            most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 16)));
+            // the largest is below 2^8 of the scale (e4m3 ends at 448), what is left over below
+            // 2^3, below 2^8 of a scale 2^5 smaller
+            const int up = max(static_cast<int>(most >> 23) - 7, 6);
+            const float s_up = __uint_as_float(static_cast<uint32_t>(up) << 23);
+            const float s_low = __uint_as_float(static_cast<uint32_t>(up - 5) << 23);
+            const bool wild = most >= 0x7F800000u;  // an infinity or NaN: NaN for the whole row
+            bytes[h] = wild ? 255 : low ? up - 5 : up;
+            if (wild || idx >= 2 * NB) {
+              if (!wild) bytes[h] = 127;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+            }
+            typedef short s16x2 __attribute__((ext_vector_type(2)));
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s16x2 code = {0, 0};
+              code = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(code, f[4 * j], f[4 * j + 1], s_up, false);
+              code = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(code, f[4 * j + 2], f[4 * j + 3], s_up, true);
+              uint32_t word = __builtin_bit_cast(uint32_t, code);
+              const f32x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, s_up, false);
+              const f32x2 b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, s_up, true);
+              s16x2 rest = {0, 0};
+              rest = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(rest, f[4 * j] - b0[0], f[4 * j + 1] - b0[1], s_low, false);
+              rest = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(rest, f[4 * j + 2] - b1[0], f[4 * j + 3] - b1[1], s_low, true);
+              if (low) word = __builtin_bit_cast(uint32_t, rest);
+              q[n][mm][4 * h + j] = static_cast<int>(word);
+            }
+          }
+          // The scale that this lane supplies is group 4 mm + g's: lanes 2 g and 2 g + 1 hold the
+          // first two groups, their second bytes the others.
+          const int from = c + 16 * ((2 * g) & 3);
+          const int b0 = __shfl(bytes[0], from), b1 = __shfl(bytes[1], from);
+          qs[n][mm] = g < 2 ? b0 : b1;
+        }
+      }
+      const int mine_end = mine0 < rows ? min(max(first_pos + i0 + token_of(min(wave * RW + RW, rows - row0) - 1) + 1, 0), kv_end) : 0;
+      const int my_end = uniform(min(mine_end, t_end));
+      // Units from here on need masks: the first row's end, the last row's window.
+      const int i_first = i0 + token_of(min(wave * RW, rows - 1 - row0));
+      const int whole_end = uniform(min(first_pos + i_first + 1, kv_end));
+      const int whole_begin =
+          uniform(a.window > 0 ? first_pos + i0 + token_of(min(wave * RW + RW, rows - row0) - 1) - a.window + 1 : 0);
+      const int my_begin = uniform(a.window > 0 ? max(first_pos + i_first - a.window + 1, 0) : 0);
+
+      f32x4 acc[NQ][kSets][8];
+      float m[NQ], l[NQ];
+      int nan_groups[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
+      }
+
+      // Half `h` of the part: where its keys and scales start (a valid place if it has no page).
+      auto place = [&](int h, const uint8_t*& kd, const uint8_t*& sd) {
+        const int64_t p = max(page_of(h), 0);
+        const int off = (t_begin + h * 16) & (page - 1);
+        kd = data + p * page_bytes + off * (D / 2);
+        sd = scales + p * page_scales + off;
+      };
+      auto load_keys = [&](int half, Keys* x) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t *kd, *sd;
+          place(half + u, kd, sd);
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            x[u].k[i] = *reinterpret_cast<const u32x4*>(kd + k_off[i]);
+            x[u].s[i] = sd[ks_off[i]];
+          }
+        }
+      };
+      u32x4 v[2];
+      uint32_t vs[2];
+      auto load_values = [&](int half) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t *kd, *sd;
+          place(half + u, kd, sd);
+          v[u] = *reinterpret_cast<const u32x4*>(kd + v_off);
+          vs[u] = *reinterpret_cast<const uint32_t*>(sd + vs_off);
+        }
+      };
+      auto convert = [&](int buf) {
+        uint32_t bad[2] = {nan_bytes(vs[0]), nan_bytes(vs[1])};
+        const bool some = __any((bad[0] | bad[1]) != 0);
+        if (lane == 0) any_nan[buf][wave] = some;
+        if (some) {  // read as finite; the rows that see them are noted from nan_token
+          if (lane < 32) nan_token[buf][wave][lane] = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if ((c & 3) == 0 && my_set * 16 + c < NC)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (bad[u] >> (8 * i + 7) & 1) atomicOr(&nan_token[buf][wave][u * 16 + g * 4 + i], 1u << (chunk >> 2));
+            bad[u] |= bad[u] >> 1, bad[u] |= bad[u] >> 2, bad[u] |= bad[u] >> 4;
+            vs[u] &= ~bad[u];
+          }
+        }
+        float sc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = __uint_as_float((vs[i >> 2] >> (8 * (i & 3)) & 0xFFu) << 23);
+#define ARD_PAIR(B)                                                                               \
+  {                                                                                               \
+    uint32_t x[8];                                                                                \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) x[i] = codes<B>(v[i >> 2][i & 3], sc[i]);       \
+    values[buf][wave][2 * B][lane] =                                                              \
+        u32x4{pair_lo(x[0], x[1]), pair_lo(x[2], x[3]), pair_lo(x[4], x[5]), pair_lo(x[6], x[7])}; \
+    values[buf][wave][2 * B + 1][lane] =                                                          \
+        u32x4{pair_hi(x[0], x[1]), pair_hi(x[2], x[3]), pair_hi(x[4], x[5]), pair_hi(x[6], x[7])}; \
+  }
+        ARD_PAIR(0) ARD_PAIR(1) ARD_PAIR(2) ARD_PAIR(3)
+#undef ARD_PAIR
+      };
+
+      const int halves = t_end > t_begin ? (t_end - t_begin + 15) >> 4 : 0;
+      int buf = 0;
+      Keys now[2], next[2];
+      if (halves > 0) {
+        load_values(my_unit * 2);
+        load_keys(0, now);
+        convert(0);
+      }
+      __syncthreads();
+      for (int h0 = 0; h0 < halves; h0 += 2 * SUB) {
+        const bool more = h0 + 2 * SUB < halves;
+        if (more) load_values(h0 + 2 * SUB + my_unit * 2);
+#pragma unroll 1
+        for (int sub = 0; sub < SUB; ++sub) {
+          const int h = h0 + 2 * sub;
+          load_keys(h + 2, next);
+          const int t0 = t_begin + h * 16;
+          if (t0 < my_end && t0 + 32 > my_begin) {
+            // Scores.
+            f32x4 s[NQ][2];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int mm = 0; mm < NM; ++mm) {
+                const u32x4 k = now[u].k[mm % NL];
+                const uint32_t ks = now[u].s[mm % NL];
+                const i32x8 kk = {static_cast<int>(k[0]), static_cast<int>(k[1]), static_cast<int>(k[2]),
+                                  static_cast<int>(k[3]), 0, 0, 0, 0};
+                const int scale = ks > kMaxScale ? 255 : static_cast<int>(ks);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)  // formats: 4 e2m1, 0 e4m3
+                  s[n][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kk, q[n][mm], s[n][u], 4, 0, 0, scale, 0, qs[n][mm]);
+              }
+            const int id0 = page_of(h), id1 = page_of(h + 1);
+            if (t0 + 32 > whole_end || t0 < whole_begin || id0 < 0 || id1 < 0) {
+#pragma unroll
+              for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int t = t0 + u * 16 + g * 4 + i;
+                    if (t >= hi[n] || t < lo[n] || (u == 0 ? id0 : id1) < 0) s[n][u][i] = -INFINITY;
+                  }
+            }
+#pragma unroll
+            for (int e = 0; e < kSets; ++e)
+              if (any_nan[buf][sub * kSets + e] != 0) {
+#pragma unroll 1
+                for (int x = 0; x < 32; ++x) {
+                  const uint32_t groups = nan_token[buf][sub * kSets + e][x];
+                  const int t = t0 + x;
+                  if (groups == 0 || (x < 16 ? id0 : id1) < 0) continue;
+#pragma unroll
+                  for (int n = 0; n < NQ; ++n)
+                    if (t < hi[n] && t >= lo[n]) nan_groups[n] |= groups;
+                }
+              }
+            // Probabilities.
+            bf16x8 pr[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              float top = s[n][0][0];
+#pragma unroll
+              for (int i = 1; i < 8; ++i) top = fmaxf(top, s[n][i >> 2][i & 3]);
+              top *= args.scale_log2;
+              if (__any(top > m[n] + 8.0f)) {
+                const float to = fmaxf(m[n], row_max(top));
+                const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
+                m[n] = to;
+                l[n] *= f;
+#pragma unroll
+                for (int e = 0; e < kSets; ++e)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
+              }
+              const float ref = m[n] == -INFINITY ? 0.0f : m[n];
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[i] = exp2_fast(fmaf(s[n][i >> 2][i & 3], args.scale_log2, -ref));
+                l[n] += x[i];
+              }
+              split<1>(x, &pr[n]);
+            }
+            // Values.
+#pragma unroll
+            for (int e = 0; e < kSets; ++e)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const bf16x8 x = __builtin_bit_cast(bf16x8, values[buf][sub * kSets + e][j][lane]);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) acc[n][e][j] = mfma(x, pr[n], acc[n][e][j]);
+              }
+          }
+          now[0] = next[0], now[1] = next[1];
+        }
+        if (more) convert(buf ^ 1);
+        buf ^= 1;
+        if ((h0 + 2 * SUB) >> 6 != batch) {
+          ids = ids_next, ++batch;
+          ids_next = pages((batch + 1) * 64);
+        }
+        __syncthreads();
+      }
+
+      // This wave's rows are its own: out, or into the workspace.
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        l[n] = row_sum(l[n]);
+        const int r = wave * RW + n * 16 + c;
+        if (row0 + r < rows) {
+          const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
+          const int64_t token = me.q0 + i;
+          const float f = parts > 1 ? 1.0f : l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+          const uint32_t at = static_cast<uint32_t>((2 * w + (before == 0)) * R + r);
+#pragma unroll
+          for (int e = 0; e < kSets; ++e) {
+            const bool nan = nan_groups[n] >> (e * 4 + g) & 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int to_chunk = e * 16 + g * 4 + k;
+              if (to_chunk >= NC) continue;
+              float o[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] = nan ? __uint_as_float(0x7FC00000u) : acc[n][e][j][k] * f;
+              if (parts > 1) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  ar::st16<ar::kCoh>(part, (at * D + to_chunk * 8 + 4 * j) * 4,
+                                     u32x4{__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                                           __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3])});
+              } else {
+                *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + token * a.o_token + head * a.o_head + to_chunk * 8) =
+                    u32x4{ar::bf16x2_rne(o[0], o[1]), ar::bf16x2_rne(o[2], o[3]), ar::bf16x2_rne(o[4], o[5]),
+                          ar::bf16x2_rne(o[6], o[7])};
+              }
+            }
+          }
+          if (g == 0) {
+            if (parts > 1)
+              ar::st8<ar::kCoh>(part, args.stats_at + at * 8, u32x2{__float_as_uint(m[n]), __float_as_uint(l[n])});
+            else if (a.lse != nullptr)
+              a.lse[token * a.q_heads + head] = l[n] == 0.0f ? -INFINITY : (m[n] + log2f(l[n])) * 0.6931471805599453f;
+          }
+        }
+      }
+      if (parts > 1) {
+        auto finish = [&](int r, int seg, f32x4 o0, f32x4 o1, float top, float rl) {
+          const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
+          finish_row<DT_BF16>(a, me.q0 + i, head, seg, o0, o1, top, rl);
+        };
+        if (arrive(args.arrived + first_wg, parts, &last))
+          join_parts<D, R, 4>(part, args.stats_at, first_wg, parts, min(R, rows - row0),
+                              reinterpret_cast<float*>(values), finish);
+      }
+    }
+    if (run.left <= 0) return;
+    // The next job of the run.
+    run.at = 0;
+    if (++run.tile == me.tiles) {
+      run.tile = 0;
+      if (++run.head == args.cache.heads) {
+        run.head = 0;
+        do {
+          if (++run.request >= a.nreq) return;  // only if lengths change under the call
+          me = series_of<R>(args, run.request);
+          me.tiles = uniform(me.tiles);
+        } while (me.tiles == 0);
+      }
+    }
+    span = uniform(me.below(run.tile + 1) - me.below(run.tile));
+    __syncthreads();  // the next job uses the same LDS
+  }
+}
+
+}  // namespace ard
