@@ -106,7 +106,8 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run,
 // A lane's share of a block of scores' keys: rows of 16 tokens, 32 elements each.
 template <int D>
 struct Keys16 {
-  static constexpr int NB = D / 32;              // groups of 32
+  // groups of 32, three with a fourth that stays empty: both parts of q then meet the same loads
+  static constexpr int NB = D == 96 ? 4 : D / 32;
   static constexpr int NM = (2 * NB + 3) / 4;    // products: four groups each, of both parts of q
   static constexpr int NL = NB % 4 == 0 ? NB / 4 : NM;  // different loads for them
   u32x4 k[NL];
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   constexpr int NB = Keys::NB, NM = Keys::NM, NL = Keys::NL;
   __shared__ u32x4 values[2][kAttnWaves][8][64];      // [buffer][unit, set][element][lane]
   __shared__ uint32_t nan_token[2][kAttnWaves][32];   // groups of 32 elements that are NaN
-  __shared__ uint32_t any_nan[2][kAttnWaves];
+  __shared__ u32x4 any_nan[2];  // a word a wave
   __shared__ int last;
 
   const ar_kv4_attention_args& a = args.a;
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   int k_off[NL], ks_off[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    const int kb = (4 * i + g) % NB;
+    const int kb = min((4 * i + g) % NB, D / 32 - 1);
     k_off[i] = c * (D / 2) + kb * 16;
     ks_off[i] = kb * page + c;
   }
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
             const int idx = 4 * mm + 2 * h + (g >> 1);
             const bool low = idx >= NB;
             const int kb = idx >= NB ? idx - NB : idx;
-            const u32x4* p = reinterpret_cast<const u32x4*>(x + min(kb, NB - 1) * 32 + (g & 1) * 16);
+            const u32x4* p = reinterpret_cast<const u32x4*>(x + min(kb, D / 32 - 1) * 32 + (g & 1) * 16);
             const u32x4 v0 = p[0], v1 = p[1];
             float f[16];
             uint32_t most = 0;
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
             const float s_low = __uint_as_float(static_cast<uint32_t>(up - 5) << 23);
             const bool wild = most >= 0x7F800000u;  // an infinity or NaN: NaN for the whole row
             bytes[h] = wild ? 255 : low ? up - 5 : up;
-            if (wild || idx >= 2 * NB) {
+            if (wild || idx >= 2 * NB || kb >= D / 32) {
               if (!wild) bytes[h] = 127;
 #pragma unroll
               for (int j = 0; j < 16; ++j) f[j] = 0.0f;
@@ -326,9 +327,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       auto convert = [&](int buf) {
         uint32_t bad[2] = {nan_bytes(vs[0]), nan_bytes(vs[1])};
         const bool some = __any((bad[0] | bad[1]) != 0);
-        if (lane == 0) any_nan[buf][wave] = some;
+        if (lane == 0) reinterpret_cast<uint32_t*>(&any_nan[buf])[wave] = some;
+        if (lane < 32) nan_token[buf][wave][lane] = 0;
         if (some) {  // read as finite; the rows that see them are noted from nan_token
-          if (lane < 32) nan_token[buf][wave][lane] = 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             if ((c & 3) == 0 && my_set * 16 + c < NC)
@@ -366,6 +367,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       __syncthreads();
       for (int h0 = 0; h0 < halves; h0 += 2 * SUB) {
         const bool more = h0 + 2 * SUB < halves;
+        const u32x4 some_nan = any_nan[buf];
+        const bool round_nan = uniform(some_nan[0] | some_nan[1] | some_nan[2] | some_nan[3]) != 0;
         if (more) load_values(h0 + 2 * SUB + my_unit * 2);
 #pragma unroll 1
         for (int sub = 0; sub < SUB; ++sub) {
@@ -402,19 +405,26 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
                     if (t >= hi[n] || t < lo[n] || (u == 0 ? id0 : id1) < 0) s[n][u][i] = -INFINITY;
                   }
             }
+            // The first operands of the second product, under way with the probabilities.
+            constexpr int AHEAD = 4;
+            bf16x8 vv[AHEAD];
+            auto operand_of = [&](int j) {
+              return __builtin_bit_cast(bf16x8, values[buf][sub * kSets + (j >> 3)][j & 7][lane]);
+            };
 #pragma unroll
-            for (int e = 0; e < kSets; ++e)
-              if (any_nan[buf][sub * kSets + e] != 0) {
+            for (int j = 0; j < AHEAD; ++j) vv[j] = operand_of(j);
+            __builtin_amdgcn_sched_barrier(0);
+            if (round_nan) {
 #pragma unroll 1
-                for (int x = 0; x < 32; ++x) {
-                  const uint32_t groups = nan_token[buf][sub * kSets + e][x];
-                  const int t = t0 + x;
-                  if (groups == 0 || (x < 16 ? id0 : id1) < 0) continue;
+              for (int x = 0; x < 32 * kSets; ++x) {
+                const uint32_t groups = nan_token[buf][sub * kSets + (x >> 5)][x & 31];
+                const int t = t0 + (x & 31);
+                if (groups == 0 || ((x & 16) == 0 ? id0 : id1) < 0) continue;
 #pragma unroll
-                  for (int n = 0; n < NQ; ++n)
-                    if (t < hi[n] && t >= lo[n]) nan_groups[n] |= groups;
-                }
+                for (int n = 0; n < NQ; ++n)
+                  if (t < hi[n] && t >= lo[n]) nan_groups[n] |= groups;
               }
+            }
             // Probabilities.
             bf16x8 pr[NQ];
 #pragma unroll
@@ -444,13 +454,12 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
             }
             // Values.
 #pragma unroll
-            for (int e = 0; e < kSets; ++e)
+            for (int j = 0; j < 8 * kSets; ++j) {
+              const bf16x8 x = vv[j % AHEAD];
+              if (j + AHEAD < 8 * kSets) vv[j % AHEAD] = operand_of(j + AHEAD);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, values[buf][sub * kSets + e][j][lane]);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[n][e][j] = mfma(x, pr[n], acc[n][e][j]);
-              }
+              for (int n = 0; n < NQ; ++n) acc[n][j >> 3][j & 7] = mfma(x, pr[n], acc[n][j >> 3][j & 7]);
+            }
           }
           now[0] = next[0], now[1] = next[1];
         }
