@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   const int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
   const int num_pages = static_cast<int>(args.cache.num_pages);
   // This lane's groups of a key for every load, its values for this wave's share of a round.
-  int k_off[NL], ks_off[NL];
+  uint32_t k_off[NL], ks_off[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int kb = min((4 * i + g) % NB, D / 32 - 1);
@@ -152,8 +152,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   }
   const int my_set = wave % kSets, my_unit = wave / kSets;
   const int chunk = min(my_set * 16 + c, NC - 1);
-  const int v_off = k_bytes + g * (D * 2) + chunk * 16;
-  const int vs_off = s_bytes + (chunk >> 2) * page + g * 4;
+  const uint32_t v_off = k_bytes + g * (D * 2) + chunk * 16;
+  const uint32_t vs_off = s_bytes + (chunk >> 2) * page + g * 4;
   const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
 
   for (;;) {
@@ -191,17 +191,31 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       const int32_t* table = a.table + run.request * a.table_stride;
       const int t_begin = begin + t_first * 32, t_end = min(begin + t_last * 32, end);
 
-      // Pages of 64 halves (16 tokens) from half `h` of this part on, one a lane.
+      // Where the keys of a half (16 tokens) and its scales start, one half a lane, from half
+      // `base` of this part on; a valid place where there is nothing to see. Wide address
+      // arithmetic for every half in turn was a third of the loop's instructions.
+      constexpr int STEP = 48;  // halves between two bases: a round looks up to 15 ahead
       auto pages = [&](int h) {
         const int t = t_begin + (h + lane) * 16;
-        int p = -1;
-        if (t < t_end) p = table[t >> shift];
-        return p < num_pages ? p : -1;
+        return t < t_end ? table[t >> shift] : -1;
       };
-      int ids = pages(0), ids_next = pages(64), batch = 0;
-      auto page_of = [&](int half) {
-        return __builtin_amdgcn_readlane(half >> 6 == batch ? ids : ids_next, half & 63);
+      int base = 0;
+      uint64_t k_at, s_at, seen;
+      auto settle = [&](int p) {
+        const bool some = p >= 0 && p < num_pages;
+        const int64_t at = some ? p : 0;
+        const int off = (t_begin + (base + lane) * 16) & (page - 1);
+        k_at = reinterpret_cast<uint64_t>(data) + at * page_bytes + off * (D / 2);
+        s_at = reinterpret_cast<uint64_t>(scales) + at * page_scales + off;
+        seen = __ballot(some);
       };
+      auto lane_address = [&](uint64_t x, int l) {
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(x), l);
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), l);
+        return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+      };
+      const int pages0 = pages(0);
+      int pages_next = pages(STEP);
 
       // This wave's rows.
       const int mine0 = row0 + wave * RW;
@@ -294,18 +308,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
           for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
       }
 
-      // Half `h` of the part: where its keys and scales start (a valid place if it has no page).
-      auto place = [&](int h, const uint8_t*& kd, const uint8_t*& sd) {
-        const int64_t p = max(page_of(h), 0);
-        const int off = (t_begin + h * 16) & (page - 1);
-        kd = data + p * page_bytes + off * (D / 2);
-        sd = scales + p * page_scales + off;
-      };
-      auto load_keys = [&](int half, Keys* x) {
+      auto load_keys = [&](int h, Keys* x) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t *kd, *sd;
-          place(half + u, kd, sd);
+          const uint8_t *kd = lane_address(k_at, h + u - base), *sd = lane_address(s_at, h + u - base);
 #pragma unroll
           for (int i = 0; i < NL; ++i) {
             x[u].k[i] = *reinterpret_cast<const u32x4*>(kd + k_off[i]);
@@ -315,11 +321,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       };
       u32x4 v[2];
       uint32_t vs[2];
-      auto load_values = [&](int half) {
+      auto load_values = [&](int h) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t *kd, *sd;
-          place(half + u, kd, sd);
+          const uint8_t *kd = lane_address(k_at, h + u - base), *sd = lane_address(s_at, h + u - base);
           v[u] = *reinterpret_cast<const u32x4*>(kd + v_off);
           vs[u] = *reinterpret_cast<const uint32_t*>(sd + vs_off);
         }
@@ -359,6 +364,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       const int halves = t_end > t_begin ? (t_end - t_begin + 15) >> 4 : 0;
       int buf = 0;
       Keys now[2], next[2];
+      settle(pages0);
       if (halves > 0) {
         load_values(my_unit * 2);
         load_keys(0, now);
@@ -393,8 +399,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
                 for (int n = 0; n < NQ; ++n)  // formats: 4 e2m1, 0 e4m3
                   s[n][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kk, q[n][mm], s[n][u], 4, 0, 0, scale, 0, qs[n][mm]);
               }
-            const int id0 = page_of(h), id1 = page_of(h + 1);
-            if (t0 + 32 > whole_end || t0 < whole_begin || id0 < 0 || id1 < 0) {
+            const int both = static_cast<int>(seen >> (h - base)) & 3;  // the halves that have a page
+            if (t0 + 32 > whole_end || t0 < whole_begin || both != 3) {
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
 #pragma unroll
                   for (int i = 0; i < 4; ++i) {
                     const int t = t0 + u * 16 + g * 4 + i;
-                    if (t >= hi[n] || t < lo[n] || (u == 0 ? id0 : id1) < 0) s[n][u][i] = -INFINITY;
+                    if (t >= hi[n] || t < lo[n] || (both >> u & 1) == 0) s[n][u][i] = -INFINITY;
                   }
             }
             // The first operands of the second product, under way with the probabilities.
@@ -419,7 +425,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
               for (int x = 0; x < 32 * kSets; ++x) {
                 const uint32_t groups = nan_token[buf][sub * kSets + (x >> 5)][x & 31];
                 const int t = t0 + (x & 31);
-                if (groups == 0 || ((x & 16) == 0 ? id0 : id1) < 0) continue;
+                if (groups == 0 || (both >> (x >> 4 & 1) & 1) == 0) continue;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
                   if (t < hi[n] && t >= lo[n]) nan_groups[n] |= groups;
@@ -465,9 +471,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         }
         if (more) convert(buf ^ 1);
         buf ^= 1;
-        if ((h0 + 2 * SUB) >> 6 != batch) {
-          ids = ids_next, ++batch;
-          ids_next = pages((batch + 1) * 64);
+        if (h0 + 2 * SUB - base == STEP) {
+          base += STEP;
+          settle(pages_next);
+          pages_next = pages(base + STEP);
         }
         __syncthreads();
       }
