@@ -25,6 +25,15 @@ namespace ard {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// Memory that a computed address is known to lie in: a load of unknown place counts as one from
+// LDS too, and every wait for LDS would wait for it.
+#define ARD_GLOBAL __attribute__((address_space(1)))
+typedef const ARD_GLOBAL uint8_t* global_bytes;
+template <class T>
+__device__ __forceinline__ T load_at(global_bytes base, uint32_t off) {
+  return *reinterpret_cast<const ARD_GLOBAL T*>(base + off);
+}
+
 // A request as the split sees it: units of tile r (of one head) are below(r + 1) - below(r).
 struct Series {
   int q0, m, kv, tiles;
@@ -212,7 +221,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       auto lane_address = [&](uint64_t x, int l) {
         const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(x), l);
         const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), l);
-        return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+        return reinterpret_cast<global_bytes>(static_cast<uint64_t>(hi) << 32 | lo);
       };
       const int pages0 = pages(0);
       int pages_next = pages(STEP);
@@ -311,11 +320,11 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       auto load_keys = [&](int h, Keys* x) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t *kd = lane_address(k_at, h + u - base), *sd = lane_address(s_at, h + u - base);
+          const global_bytes kd = lane_address(k_at, h + u - base), sd = lane_address(s_at, h + u - base);
 #pragma unroll
           for (int i = 0; i < NL; ++i) {
-            x[u].k[i] = *reinterpret_cast<const u32x4*>(kd + k_off[i]);
-            x[u].s[i] = sd[ks_off[i]];
+            x[u].k[i] = load_at<u32x4>(kd, k_off[i]);
+            x[u].s[i] = load_at<uint8_t>(sd, ks_off[i]);
           }
         }
       };
@@ -324,9 +333,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       auto load_values = [&](int h) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t *kd = lane_address(k_at, h + u - base), *sd = lane_address(s_at, h + u - base);
-          v[u] = *reinterpret_cast<const u32x4*>(kd + v_off);
-          vs[u] = *reinterpret_cast<const uint32_t*>(sd + vs_off);
+          const global_bytes kd = lane_address(k_at, h + u - base), sd = lane_address(s_at, h + u - base);
+          v[u] = load_at<u32x4>(kd, v_off);
+          vs[u] = load_at<uint32_t>(sd, vs_off);
         }
       };
       auto convert = [&](int buf) {
