@@ -31,8 +31,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef const ARD_GLOBAL uint8_t* global_bytes;
 template <class T>
 __device__ __forceinline__ T load_at(global_bytes base, uint32_t off) {
+  asm("" : "+v"(off));  // stays a 32-bit offset beside a scalar base
   return *reinterpret_cast<const ARD_GLOBAL T*>(base + off);
 }
+
+// A running maximum that no score has reached yet: finite, so that a masked score less it is minus
+// infinity without a test.
+constexpr float kLowest = -3.0e38f;
 
 // A request as the split sees it: units of tile r (of one head) are below(r + 1) - below(r).
 struct Series {
@@ -128,6 +133,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   constexpr int RW = 16 * NQ, R = RW * kAttnWaves;
   constexpr int NC = D / 8, kSets = (NC + 15) / 16;
   constexpr int SUB = kAttnWaves / kSets;  // units of 32 tokens of a round
+  constexpr int TURNS = kSets == 1 ? 2 : 1;  // units in the loop's body: with two, keys stay where they are
   typedef Keys16<D> Keys;
   constexpr int NB = Keys::NB, NM = Keys::NM, NL = Keys::NL;
   __shared__ u32x4 values[2][kAttnWaves][8][64];      // [buffer][unit, set][element][lane]
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       int nan_groups[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
+        m[n] = kLowest, l[n] = 0.0f, nan_groups[n] = 0;
 #pragma unroll
         for (int e = 0; e < kSets; ++e)
 #pragma unroll
@@ -372,11 +378,11 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
 
       const int halves = t_end > t_begin ? (t_end - t_begin + 15) >> 4 : 0;
       int buf = 0;
-      Keys now[2], next[2];
+      Keys keys[2][2];  // of this unit and the next, in turn
       settle(pages0);
       if (halves > 0) {
         load_values(my_unit * 2);
-        load_keys(0, now);
+        load_keys(0, keys[0]);
         convert(0);
       }
       __syncthreads();
@@ -386,9 +392,12 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         const bool round_nan = uniform(some_nan[0] | some_nan[1] | some_nan[2] | some_nan[3]) != 0;
         if (more) load_values(h0 + 2 * SUB + my_unit * 2);
 #pragma unroll 1
-        for (int sub = 0; sub < SUB; ++sub) {
-          const int h = h0 + 2 * sub;
-          load_keys(h + 2, next);
+        for (int sub0 = 0; sub0 < SUB; sub0 += TURNS)
+#pragma unroll
+        for (int turn = 0; turn < TURNS; ++turn) {
+          const int sub = sub0 + turn, h = h0 + 2 * sub;
+          const Keys* now = keys[turn];
+          load_keys(h + 2, keys[turn ^ 1]);
           const int t0 = t_begin + h * 16;
           if (t0 < my_end && t0 + 32 > my_begin) {
             // Scores.
@@ -450,7 +459,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
               top *= args.scale_log2;
               if (__any(top > m[n] + 8.0f)) {
                 const float to = fmaxf(m[n], row_max(top));
-                const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
+                const float f = exp2_fast(m[n] - to);
                 m[n] = to;
                 l[n] *= f;
 #pragma unroll
@@ -458,11 +467,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
 #pragma unroll
                   for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
               }
-              const float ref = m[n] == -INFINITY ? 0.0f : m[n];
               float x[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                x[i] = exp2_fast(fmaf(s[n][i >> 2][i & 3], args.scale_log2, -ref));
+                x[i] = exp2_fast(fmaf(s[n][i >> 2][i & 3], args.scale_log2, -m[n]));
                 l[n] += x[i];
               }
               split<1>(x, &pr[n]);
@@ -476,7 +484,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
               for (int n = 0; n < NQ; ++n) acc[n][j >> 3][j & 7] = mfma(x, pr[n], acc[n][j >> 3][j & 7]);
             }
           }
-          now[0] = next[0], now[1] = next[1];
+          if (TURNS == 1) keys[0][0] = keys[1][0], keys[0][1] = keys[1][1];
         }
         if (more) convert(buf ^ 1);
         buf ^= 1;
