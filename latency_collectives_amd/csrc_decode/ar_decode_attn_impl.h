@@ -276,7 +276,7 @@ __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, i
     const int r = y / NC, seg = y - r * NC;
     float top = -INFINITY, rl = 0.0f;
     f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
-    for (int p0 = mine; p0 < parts && mine < groups; p0 += 8 * groups) {
+    for (int p0 = mine; p0 < parts && mine < groups; p0 += N * groups) {
       u32x2 st[N];
       u32x4 v0[N], v1[N];
 #pragma unroll
