@@ -8,12 +8,16 @@
 
 namespace {
 
-// Rows a request above which tiles of 128 rows are faster than tiles of 32.
-constexpr int kFewRows = 32;
+// The kernel for a call. Tiles of 16 or 32 rows (by what a request brings on average), four waves on
+// different tokens: short jobs, whose parts join quickly. Tiles of 128 rows, waves on different
+// rows: values are converted once for all of them, but a job is four times as long and so is its
+// join, so they pay where the tiles alone fill the device's 512 places, or the tokens behind them
+// (their bound, the tables' width) do. Measured, head_dim 128, 4 kv heads of 8 query heads, small
+// tiles against large: 8 requests of 256 rows, 4096 tokens 43 and 67 us; of 1024 rows 106 and 122;
+// of 2048 rows (512 tiles) 206 and 193; of 8192 rows 810 and 540; one of 4096 rows and 16384 tokens
+// (128 tiles) 199 and 183. Binary32, three products for one, stays with the small tiles.
+constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16;
 
-// The kernel for a call: a tile of 16 or 32 rows where a request brings that many on average, its
-// four waves on different tokens; tiles of 128 rows beyond, its waves on different rows
-// (bfloat16; binary32, three products for one, stays with the small tiles).
 struct Choice {
   ard::AttnKernel k;
   int rows;  // of a tile
@@ -24,7 +28,13 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
-  if (bf16 && each > kFewRows) return {ard::select_attn_rows(h->head_dim), 64 * ard::rows_columns(h->head_dim), true};
+  if (bf16 && each > 128) {
+    const int large = 64 * ard::rows_columns(h->head_dim);
+    const int64_t tiles = (each + large - 1) / large * std::min(a->nreq, a->ntokens) * h->heads;
+    const int64_t tokens = static_cast<int64_t>(a->table_width) << h->page_shift;
+    const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
+    if (tiles >= kManyTiles || tiles * units >= kManyUnits) return {ard::select_attn_rows(h->head_dim), large, true};
+  }
   const int columns = each > 16 && (bf16 || h->head_dim <= 128) ? 2 : 1;
   return {bf16 ? ard::select_attn_bf16(h->head_dim, columns) : ard::select_attn_f32(h->head_dim, columns), 16 * columns,
           false};

@@ -77,17 +77,21 @@ __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
 template <int R>
 __device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run, Series& mine, int& span) {
   const int lane = threadIdx.x & 63, heads = args.cache.heads;
-  uint32_t total = 0;
+  uint32_t total = 0, longest = 0;
   Series c;
   uint32_t upto;
   for (int b = (args.a.nreq - 1) & ~63; b >= 0; b -= 64) {
     c = series_of<R>(args, b + lane);
     upto = wave_scan(c.below(c.tiles) * heads);
+    longest = max(longest, wave_max(c.tiles > 0 ? c.below(c.tiles) - c.below(c.tiles - 1) : 0));
     total = __builtin_elementwise_add_sat(total, static_cast<uint32_t>(lane_value(upto, 63)));
   }
   if (total > 0x7FFFFFFFu) return false;  // request starts that overlap
-  // four units at least: a round of the workgroup
-  run.per = max(4u, (total + args.runs - 1) / args.runs);
+  // Four units at least, a round of the workgroup; and parts of a job no shorter than makes reading
+  // them back (one after the other, about 1.5 units each) as long as computing one.
+  const int least = max((total + args.runs - 1) / args.runs,
+                        static_cast<uint32_t>(uniform(static_cast<int>(sqrtf(1.5f * static_cast<float>(longest))))));
+  run.per = max(4, least);
   if (static_cast<uint64_t>(w) * run.per >= total) return false;
   uint32_t from = w * run.per;
   run.left = min(run.per, static_cast<int>(total - from));
@@ -551,7 +555,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
           finish_row<DT_BF16>(a, me.q0 + i, head, seg, o0, o1, top, rl);
         };
         if (arrive(args.arrived + first_wg, parts, &last))
-          join_parts<D, R, 4>(part, args.stats_at, first_wg, parts, min(R, rows - row0),
+          join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0),
                               reinterpret_cast<float*>(values), finish);
       }
     }
