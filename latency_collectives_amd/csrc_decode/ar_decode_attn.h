@@ -8,7 +8,9 @@ namespace ard {
 struct AttnArgs {
   ar_kv4_attention_args a;
   Cache cache;
+  int64_t page_bytes, page_scales;  // of a page's heads, in data and scales
   int group;          // query heads of a kv head
+  float per_group;    // 1 / group
   int room;           // tokens that a row of the table holds
   // The work split: units of `unit` tokens (32 << tile_shift), of which a row sees at most
   // most_seen; at most `runs` runs.

@@ -8,15 +8,14 @@
 
 namespace {
 
-// The kernel for a call. Tiles of 16 or 32 rows (by what a request brings on average), four waves on
-// different tokens: short jobs, whose parts join quickly. Tiles of 128 rows, waves on different
+// The kernel for a call. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose parts join quickly. Tiles of 128 rows, waves on different
 // rows: values are converted once for all of them, but a job is four times as long and so is its
 // join, so they pay where the tiles alone fill the device's 512 places, or the tokens behind them
 // (their bound, the tables' width) do. Measured, head_dim 128, 4 kv heads of 8 query heads, small
 // tiles against large: 8 requests of 256 rows, 4096 tokens 43 and 67 us; of 1024 rows 106 and 122;
 // of 2048 rows (512 tiles) 206 and 193; of 8192 rows 810 and 540; one of 4096 rows and 16384 tokens
 // (128 tiles) 199 and 183. Binary32, three products for one, stays with the small tiles.
-constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16;
+constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
 struct Choice {
   ard::AttnKernel k;
@@ -35,7 +34,11 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
     if (tiles >= kManyTiles || tiles * units >= kManyUnits) return {ard::select_attn_rows(h->head_dim), large, true};
   }
-  const int columns = each > 16 && (bf16 || h->head_dim <= 128) ? 2 : 1;
+  // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
+  // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and
+  // 30 us; one of 32 rows, 4096 tokens 11.8 and 15.7). Binary32 gains from it at head_dim 64 only.
+  const int64_t tiles = (each + 31) / 32 * std::min(a->nreq, a->ntokens) * h->heads;
+  const int columns = each > 16 && tiles >= kFewTiles && (bf16 || h->head_dim == 64) ? 2 : 1;
   return {bf16 ? ard::select_attn_bf16(h->head_dim, columns) : ard::select_attn_f32(h->head_dim, columns), 16 * columns,
           false};
 }
@@ -140,6 +143,9 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   args.cache = Cache{const_cast<uint8_t*>(a->data), const_cast<uint8_t*>(a->scales), a->num_pages,
                      h->heads, h->page_shift};
   args.group = a->q_heads / h->heads;
+  args.per_group = 1.0f / args.group;
+  args.page_bytes = static_cast<int64_t>(h->heads) * h->page_size * h->head_dim;
+  args.page_scales = static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32);
   args.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
   args.q_sign = 0;
   if (choice.many) {

@@ -11,9 +11,7 @@ AttnKernel select_attn_f32(int head_dim, int columns) {
   ARD_CASE(64, 1, 3);
   ARD_CASE(64, 2, 2);
   ARD_CASE(96, 1, 2);
-  ARD_CASE(96, 2, 1);
   ARD_CASE(128, 1, 2);
-  ARD_CASE(128, 2, 1);
   ARD_CASE(192, 1, 1);
   ARD_CASE(256, 1, 1);
 #undef ARD_CASE

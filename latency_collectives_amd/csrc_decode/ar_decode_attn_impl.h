@@ -199,6 +199,22 @@ __device__ __forceinline__ void next_job(const AttnArgs& args, Run& run, Cost& m
   mine.q0 = uniform(mine.q0), mine.m = uniform(mine.m), mine.kv = uniform(mine.kv), mine.span = uniform(mine.span);
 }
 
+// Memory that a computed address is known to lie in: a load of unknown place counts as one from
+// LDS too, and every wait for LDS would wait for it.
+#define ARD_GLOBAL __attribute__((address_space(1)))
+typedef const ARD_GLOBAL uint8_t* global_bytes;
+template <class T>
+__device__ __forceinline__ T load_at(global_bytes base, uint32_t off) {
+  asm("" : "+v"(off));  // stays a 32-bit offset beside a scalar base
+  return *reinterpret_cast<const ARD_GLOBAL T*>(base + off);
+}
+// The address that lane `l` holds.
+__device__ __forceinline__ global_bytes lane_address(uint64_t x, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(x), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), l);
+  return reinterpret_cast<global_bytes>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // Any byte above kMaxScale (252) in a word of scale bytes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x03030303u) & w & 0x80808080u;
@@ -207,12 +223,12 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // N consecutive dwords with the widest loads that their alignment allows (4 N bytes, N a divisor or
 // multiple of the width).
 template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* out) {
+__device__ __forceinline__ void load_dwords(global_bytes p, uint32_t off, uint32_t* out) {
   constexpr int W = N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1;
   typedef uint32_t vec __attribute__((ext_vector_type(W)));
 #pragma unroll
   for (int i = 0; i < N; i += W) {
-    const vec v = *reinterpret_cast<const vec*>(p + 4 * i);
+    const vec v = load_at<vec>(p, off + 4 * i);
 #pragma unroll
     for (int j = 0; j < W; ++j) out[i + j] = v[j];
   }
@@ -334,6 +350,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   constexpr int NC = D / 8;
   typedef Tile32<D> Tile;
   constexpr int kDw = Tile::kDw, kKs = Tile::kKs, kSets = Tile::kSets;
+  // Registers for two tiles of keys are not left: the next ones are loaded behind the scores.
+  constexpr bool kLate = kSets == 2 && NQ == 2;
   constexpr int kPitch = D + 4;  // LDS row: 16 rows' 16-byte accesses fall into different banks
   __shared__ float join[kAttnWaves * 16 * kPitch];
   __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
@@ -347,17 +365,13 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int group = args.group, shift = args.cache.page_shift;
-  const float per_group = 1.0f / group;
-
   // Per-lane offsets within a page's K and V.
   const int page = 1 << shift;
   const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
-  const int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
-  const int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
   const int num_pages = static_cast<int>(args.cache.num_pages);
   const int k_group = (g * kDw) >> 2;  // 32-group of a lane's first K dword
-  const int k_off = c * (D / 2) + g * (D / 8);
-  int v_off[kSets], vs_off[kSets];
+  const uint32_t k_off = c * (D / 2) + g * (D / 8);
+  uint32_t v_off[kSets], vs_off[kSets];
 #pragma unroll
   for (int e = 0; e < kSets; ++e) {
     const int chunk = min(e * 16 + c, NC - 1);  // lanes beyond the row repeat its last chunk
@@ -373,7 +387,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   if (run.tile > 0) i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group));
   const int rem0 = row0 - i0 * group;
   // token and head in the group of row row0 + r: rem0 + r is below 2^17, exact in binary32
-  auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * per_group); };
+  auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * args.per_group); };
   const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
   const int kv_end = min(me.kv, args.room);
   const int first_pos = me.kv - me.m;  // position of the request's first new token
@@ -402,13 +416,21 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   const uint8_t* scales = args.cache.scales + static_cast<int64_t>(run.head) * 2 * s_bytes;
   const int32_t* table = a.table + run.request * a.table_stride;
 
-  // Pages of this wave's next 32 tiles, lane 2 k + u the u-th half of the k-th; -1 where there is
-  // nothing to see. One load a tile would make the wave wait for its keys and values with it.
+  // Where the keys of this wave's next 32 tiles and their scales start: lane 2 k + u has the u-th
+  // half of the k-th, a valid place where there is nothing to see. One page id a tile would make
+  // the wave wait for its keys and values with it.
   auto pages = [&](int tile) {
     const int mine = tile + (lane >> 1) * kAttnWaves, t = begin + mine * 32 + (lane & 1) * 16;
-    int p = -1;
-    if (mine < t_last && t < end) p = table[t >> shift];
-    return p < num_pages ? p : -1;
+    return mine < t_last && t < end ? table[t >> shift] : -1;
+  };
+  uint64_t k_at, s_at, seen;
+  auto settle = [&](int p) {
+    const bool some = p >= 0 && p < num_pages;
+    const int64_t at = some ? p : 0;
+    const int off = (begin + (t_first + wave) * 32 + (lane & 1) * 16 + (lane >> 1) * (kAttnWaves * 32)) & (page - 1);
+    k_at = reinterpret_cast<uint64_t>(data) + at * args.page_bytes + off * (D / 2);
+    s_at = reinterpret_cast<uint64_t>(scales) + at * args.page_scales + off;
+    seen = __ballot(some);
   };
   int ids = pages(t_first + wave);  // under way with the queries
 
@@ -458,44 +480,45 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
   }
 
-  auto load = [&](int tile, const int* id, Tile& x) {
+  auto load_keys = [&](int k, Tile& x) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int off = (begin + tile * 32 + u * 16) & (page - 1);
-      const int64_t p = max(id[u], 0);  // a valid place, for loads that nothing uses
-      const uint8_t* kd = data + p * page_bytes + off * (D / 2);
-      const uint8_t* sd = scales + p * page_scales + off;
-      load_dwords<kDw>(kd + k_off, x.k[u]);
+      const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
+      load_dwords<kDw>(kd, k_off, x.k[u]);
 #pragma unroll
       for (int s = 0; s < kKs; ++s)
-        x.ks[u][s] = sd[min(k_group + s, D / 32 - 1) * page + c];
+        x.ks[u][s] = load_at<uint8_t>(sd, min(k_group + s, D / 32 - 1) * page + c);
+    }
+  };
+  auto load_values = [&](int k, Tile& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
 #pragma unroll
       for (int e = 0; e < kSets; ++e) {
-        x.v[u][e] = *reinterpret_cast<const u32x4*>(kd + v_off[e]);
-        x.vs[u][e] = *reinterpret_cast<const uint32_t*>(sd + vs_off[e]);
+        x.v[u][e] = load_at<u32x4>(kd, v_off[e]);
+        x.vs[u][e] = load_at<uint32_t>(sd, vs_off[e]);
       }
     }
   };
 
   // The first round only loads: one copy of this code.
-  int id[2] = {-1, -1}, id_next[2];
   Tile now, next;
-  int tile = t_first + wave - kAttnWaves;
-  int ids_after = -1, turn = 0;
+  int tile = t_first + wave - kAttnWaves, turn = 0;
+  int both = 0, both_next;  // the halves that have a page
   for (; tile < t_last; tile += kAttnWaves) {
     if ((turn & 31) == 0) {
-      if (turn > 0) ids = ids_after;
-      ids_after = pages(tile + 33 * kAttnWaves);
+      settle(ids);
+      ids = pages(tile + 33 * kAttnWaves);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) id_next[u] = __builtin_amdgcn_readlane(ids, 2 * (turn & 31) + u);
-    ++turn;
-    load(tile + kAttnWaves, id_next, next);
-    if (tile >= t_first) {
-
+    both_next = static_cast<int>(seen >> (2 * (turn & 31))) & 3;
+    const int k_next = turn++ & 31;
+    if (!kLate) load_keys(k_next, next);
+    load_values(k_next, next);
+    f32x4 s[NQ][2];
     const int t0 = begin + tile * 32;
     // Scores.
-    f32x4 s[NQ][2];
+    if (tile >= t_first) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -515,7 +538,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
           for (int p = 0; p < PARTS; ++p) s[n][u] = mfma(kk, q[n][p][i], s[n][u]);
       }
     }
-    const bool partial = t0 + 32 > whole_end || t0 < whole_begin || id[0] < 0 || id[1] < 0;
+    }
+    if (kLate) load_keys(k_next, now);
+    if (tile >= t_first) {
+    const bool partial = t0 + 32 > whole_end || t0 < whole_begin || both != 3;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
     if (partial) {
@@ -526,7 +552,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = t0 + u * 16 + g * 4 + i;
-            if (t >= hi[n] || t < lo[n] || id[u] < 0) s[n][u][i] = -INFINITY;
+            if (t >= hi[n] || t < lo[n] || (both >> u & 1) == 0) s[n][u][i] = -INFINITY;
           }
     }
 
@@ -553,7 +579,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int t = t0 + u * 16 + g * 4 + i;
-                if ((theirs >> (8 * i + 7) & 1) && t < hi[n] && t >= lo[n] && id[u] >= 0)
+                if ((theirs >> (8 * i + 7) & 1) && t < hi[n] && t >= lo[n] && (both >> u & 1) != 0)
                   nan_groups[n] |= 1 << group32;
               }
           }
@@ -615,8 +641,15 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
 #undef ARD_PAIR
     }
     }
-    now = next;
-    id[0] = id_next[0], id[1] = id_next[1];
+    if (kLate) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < kSets; ++e) now.v[u][e] = next.v[u][e], now.vs[u][e] = next.vs[u][e];
+    } else {
+      now = next;
+    }
+    both = both_next;
   }
 
   // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.

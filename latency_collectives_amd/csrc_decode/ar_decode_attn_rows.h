@@ -30,16 +30,6 @@ namespace ard {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// Memory that a computed address is known to lie in: a load of unknown place counts as one from
-// LDS too, and every wait for LDS would wait for it.
-#define ARD_GLOBAL __attribute__((address_space(1)))
-typedef const ARD_GLOBAL uint8_t* global_bytes;
-template <class T>
-__device__ __forceinline__ T load_at(global_bytes base, uint32_t off) {
-  asm("" : "+v"(off));  // stays a 32-bit offset beside a scalar base
-  return *reinterpret_cast<const ARD_GLOBAL T*>(base + off);
-}
-
 // A running maximum that no score has reached yet: finite, so that a masked score less it is minus
 // infinity without a test.
 constexpr float kLowest = -3.0e38f;
@@ -160,11 +150,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int group = args.group, shift = args.cache.page_shift;
-  const float per_group = 1.0f / group;
   const int page = 1 << shift;
   const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
-  const int64_t page_bytes = static_cast<int64_t>(args.cache.heads) * 2 * k_bytes;
-  const int64_t page_scales = static_cast<int64_t>(args.cache.heads) * 2 * s_bytes;
   const int num_pages = static_cast<int>(args.cache.num_pages);
   // This lane's groups of a key for every load, its values for this wave's share of a round.
   uint32_t k_off[NL], ks_off[NL];
@@ -185,7 +172,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
     const int row0 = run.tile * R;
     const int i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group)), rem0 = row0 - i0 * group;
     // token of row row0 + r: rem0 + r is below 2^17, exact in binary32
-    auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * per_group); };
+    auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * args.per_group); };
     const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
     const int kv_end = min(me.kv, args.room);
     const int first_pos = me.kv - me.m;
@@ -229,14 +216,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         const bool some = p >= 0 && p < num_pages;
         const int64_t at = some ? p : 0;
         const int off = (t_begin + (base + lane) * 16) & (page - 1);
-        k_at = reinterpret_cast<uint64_t>(data) + at * page_bytes + off * (D / 2);
-        s_at = reinterpret_cast<uint64_t>(scales) + at * page_scales + off;
+        k_at = reinterpret_cast<uint64_t>(data) + at * args.page_bytes + off * (D / 2);
+        s_at = reinterpret_cast<uint64_t>(scales) + at * args.page_scales + off;
         seen = __ballot(some);
-      };
-      auto lane_address = [&](uint64_t x, int l) {
-        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(x), l);
-        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(x >> 32), l);
-        return reinterpret_cast<global_bytes>(static_cast<uint64_t>(hi) << 32 | lo);
       };
       const int pages0 = pages(0);
       int pages_next = pages(STEP);
