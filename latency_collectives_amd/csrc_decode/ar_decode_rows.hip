@@ -11,7 +11,7 @@
 // binary32, the kernel is bound by bytes (or by its launch), and what is rounded to bfloat16 and
 // then to 4 bits no longer depends on the order of the sum of squares.
 //
-// Measured, 8191 tokens of 32 + 8 heads of 128 in bfloat16 (172 MB): 41 us, 4.2 TB/s; one row a group
+// Measured, 8191 tokens of 32 + 8 heads of 128 in bfloat16 (172 MB): 38.7 us, 4.4 TB/s; one row a group
 // with a 64-bit division for its place and a library square root and reciprocal was bound by its
 // instructions (56 us).
 
@@ -22,43 +22,53 @@
 namespace ard {
 
 constexpr int kRowThreads = 256;
-// Workgroups below which rows are spread over more of them.
-constexpr int kFewBlocks = 2048;
+// Workgroups below which rows are spread over more of them: 1000 tokens of 16 heads take 6.4 us in
+// runs of one to four heads, 8.2 us in runs of eight; 5001 tokens of 16 take 23 us in runs of one
+// and 18.6 us in runs of eight (into the cache and back), 8191 of 40 take 79 us and 42 us.
+constexpr int kFewBlocks = 512;
 
+// Four elements of either type: as they lie in memory, as binary32, and back.
 template <int DT>
 struct Elem;
 template <>
 struct Elem<DT_F32> {
-  typedef float T;
-  __device__ static void load4(const void* base, int64_t at, float* x) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
+  typedef f32x4 Raw;
+  __device__ static void widen(Raw v, float* x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = v[i];
   }
-  __device__ static void store4(void* base, int64_t at, const float* x) {
-    f32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = x[i];
-    *reinterpret_cast<f32x4*>(static_cast<float*>(base) + at) = v;
+  __device__ static Raw narrow(const float* x) { return Raw{x[0], x[1], x[2], x[3]}; }
+  __device__ static Raw* at(const void* base, int64_t i) {
+    return reinterpret_cast<Raw*>(static_cast<float*>(const_cast<void*>(base)) + i);
   }
   __device__ static float round(double y) { return static_cast<float>(y); }
 };
 template <>
 struct Elem<DT_BF16> {
-  typedef uint16_t T;
-  __device__ static void load4(const void* base, int64_t at, float* x) {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + at);
+  typedef u32x2 Raw;
+  __device__ static void widen(Raw v, float* x) {
     x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
   }
-  __device__ static void store4(void* base, int64_t at, const float* x) {
-    u32x2 v;
-    v.x = ar::bf16x2_rne(x[0], x[1]), v.y = ar::bf16x2_rne(x[2], x[3]);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(base) + at) = v;
+  __device__ static Raw narrow(const float* x) {
+    return Raw{ar::bf16x2_rne(x[0], x[1]), ar::bf16x2_rne(x[2], x[3])};
+  }
+  __device__ static Raw* at(const void* base, int64_t i) {
+    return reinterpret_cast<Raw*>(static_cast<uint16_t*>(const_cast<void*>(base)) + i);
   }
   __device__ static float round(double y) {
     return bf16_lo(ar::bf16x2_rne(static_cast<float>(y), 0.0f));
   }
 };
+template <int DT>
+__device__ __forceinline__ void load4(const void* base, int64_t i, float* x) {
+  Elem<DT>::widen(*Elem<DT>::at(base, i), x);
+}
+// PASS: past the caches.
+template <int DT, bool PASS>
+__device__ __forceinline__ void store4(void* base, int64_t i, const float* x) {
+  if constexpr (PASS) __builtin_nontemporal_store(Elem<DT>::narrow(x), Elem<DT>::at(base, i));
+  else *Elem<DT>::at(base, i) = Elem<DT>::narrow(x);
+}
 
 // Writes eight consecutive elements x of a row, elements 8u .. 8u+7, as codes; the four lanes of a
 // group of 32 share its scale. K rows are plain, V rows interleaved by four tokens.
@@ -124,10 +134,10 @@ struct RowArgs {
   int q_runs, k_runs;  // blocks in y: q's runs of heads, then k's, then v's
 };
 
-// G lanes a row. CACHE: keys and values go into the cache, else keys to k_out.
-template <int DT, int G, bool CACHE>
+// G lanes a row, B rows whose loads are under way at once. CACHE: keys and values go into the cache, else keys to k_out. PASS: outputs go past
+// the caches.
+template <int DT, int G, int B, bool CACHE, bool PASS>
 __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
-  constexpr int B = 4;  // rows whose loads are under way at once
   const ar_qk_norm_rope_args& a = r.a;
   // A rotated row's elements pass through LDS on their way to the cache: the rotation pairs
   // elements half a row apart, the cache's groups are consecutive.
@@ -154,13 +164,13 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
   // A lane's two runs of four elements: both ends of its pairs.
   const bool halves = turned && !a.interleaved;
   const int lo = !live ? 0 : halves ? 4 * u : 8 * u, hi = !live ? 4 : halves ? rot / 2 + 4 * u : 8 * u + 4;
-  float x[B][8];
+  typename Elem<DT>::Raw raw[B][2];
   auto load = [&](int n) {  // rows from `from` on; places past the last repeat it
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       const int64_t at = from + min(i, n - 1) * head_step;
-      Elem<DT>::load4(src, at + lo, x[i]);
-      Elem<DT>::load4(src, at + hi, x[i] + 4);
+      raw[i][0] = *Elem<DT>::at(src, at + lo);
+      raw[i][1] = *Elem<DT>::at(src, at + hi);
     }
   };
   load(head1 - head0);
@@ -171,21 +181,26 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
   double w[8], c[4], s[4];
   if (weight != nullptr) {
     float f[8];
-    Elem<DT>::load4(weight, lo, f);
-    Elem<DT>::load4(weight, hi, f + 4);
+    load4<DT>(weight, lo, f);
+    load4<DT>(weight, hi, f + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = f[i];
   }
   if (turned) {
     float f[8];
     const int64_t at = static_cast<int64_t>(beyond ? 0 : pos) * rot + 4 * u;
-    Elem<DT_F32>::load4(a.cos_sin, at, f);
-    Elem<DT_F32>::load4(a.cos_sin, at + rot / 2, f + 4);
+    load4<DT_F32>(a.cos_sin, at, f);
+    load4<DT_F32>(a.cos_sin, at + rot / 2, f + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = f[i], s[i] = f[4 + i];
   }
-  for (int head = head0;;) {
+  for (int head = head0; head < head1; head += B) {
     const int n = min(B, head1 - head);
+    float x[B][8];
+#pragma unroll
+    for (int i = 0; i < B; ++i) Elem<DT>::widen(raw[i][0], x[i]), Elem<DT>::widen(raw[i][1], x[i] + 4);
+    from += B * head_step;
+    if (B > 1 && head + B < head1) load(head1 - head - B);  // the next rows, under way with these
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       if (i >= n) break;
@@ -228,14 +243,11 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
         }
         if (live) put_row(r.cache, slot, head + i, is_v, d, u, x[i]);
       } else if (live) {
-        Elem<DT>::store4(dst, to + i * to_step + lo, x[i]);
-        Elem<DT>::store4(dst, to + i * to_step + hi, x[i] + 4);
+        store4<DT, PASS>(dst, to + i * to_step + lo, x[i]);
+        store4<DT, PASS>(dst, to + i * to_step + hi, x[i] + 4);
       }
     }
-    head += B;
-    if (head >= head1) return;
-    from += B * head_step, to += B * to_step;
-    load(head1 - head);
+    to += B * to_step;
   }
 }
 
@@ -271,8 +283,8 @@ __global__ __launch_bounds__(kRowThreads) void read_rows(ReadArgs r) {
   }
   void* dst = value ? a.v : a.k;
   const int64_t to = (value ? t * a.v_token + head * a.v_head : t * a.k_token + head * a.k_head) + 8 * u;
-  Elem<DT>::store4(dst, to, x);
-  Elem<DT>::store4(dst, to + 4, x + 4);
+  store4<DT, false>(dst, to, x);
+  store4<DT, false>(dst, to + 4, x + 4);
 }
 
 inline int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
@@ -293,19 +305,28 @@ int launch_norm_rope(RowArgs& r, hipStream_t stream) {
   if (r.a.ntokens == 0 || rows == 0) return AR_OK;
   r.per_dim = 1.0 / r.a.head_dim;
   r.run = pick_run(r.a.ntokens, rows, g);
+  // More than the XCDs' L2 hold is not read from there again: 8191 tokens of 40 heads 42 and 38 us.
+  const bool pass = !CACHE && static_cast<int64_t>(r.a.ntokens) * (r.a.q_heads + r.a.kv_heads) * r.a.head_dim *
+               (r.a.dtype == AR_BFLOAT16 ? 2 : 4) > (int64_t(32) << 20);
   const auto runs = [&](int heads) { return (heads + r.run - 1) / r.run; };
   r.q_runs = runs(r.a.q_heads), r.k_runs = runs(r.a.kv_heads);
   const int in_y = r.q_runs + r.k_runs + runs(r.values);
   if (in_y > 65535) return ar_fail(AR_ETOOBIG, "too many heads");
   const int each = kRowThreads / g;
   const dim3 grid((r.a.ntokens + each - 1) / each, in_y), block(kRowThreads);
-#define ARD_LAUNCH(DT, G) hipLaunchKernelGGL((norm_rope<DT, G, CACHE>), grid, block, 0, stream, r)
+  void (*fn)(RowArgs);
+  // One row a group has its own, shorter code: one token's 9 heads 2.7 us, 3.4 us with room for four.
+#define ARD_PICK(DT, G)                                  \
+  fn = r.run == 1 ? norm_rope<DT, G, 1, CACHE, false>    \
+       : pass     ? norm_rope<DT, G, 4, CACHE, !CACHE>   \
+                  : norm_rope<DT, G, 4, CACHE, false>
   if (r.a.dtype == AR_BFLOAT16) {
-    if (g == 8) ARD_LAUNCH(DT_BF16, 8); else if (g == 16) ARD_LAUNCH(DT_BF16, 16); else ARD_LAUNCH(DT_BF16, 32);
+    if (g == 8) ARD_PICK(DT_BF16, 8); else if (g == 16) ARD_PICK(DT_BF16, 16); else ARD_PICK(DT_BF16, 32);
   } else {
-    if (g == 8) ARD_LAUNCH(DT_F32, 8); else if (g == 16) ARD_LAUNCH(DT_F32, 16); else ARD_LAUNCH(DT_F32, 32);
+    if (g == 8) ARD_PICK(DT_F32, 8); else if (g == 16) ARD_PICK(DT_F32, 16); else ARD_PICK(DT_F32, 32);
   }
-#undef ARD_LAUNCH
+#undef ARD_PICK
+  hipLaunchKernelGGL(fn, grid, block, 0, stream, r);
   AR_HIP(hipGetLastError());
   return AR_OK;
 }
