@@ -9,8 +9,10 @@
 // code that runs once from a cold instruction cache, so the code is short: one copy of the scan,
 // sums in 32 bits that saturate (all that they are compared with is below 2^31), a division by the
 // page size as one binary64 product. In 64 bits with divisions, as first written, 32 requests of
-// one token took 6.6 us and 1000 requests of up to 64 took 14.9 us; they
-// take 4.0 us and 7.5 us so.
+// one token took 6.6 us and 1000 requests of up to 64 took 14.8 us; they
+// take 3.3 us and 7.0 us so.
+
+#include <algorithm>
 
 #include "ar_decode.h"
 
@@ -55,7 +57,8 @@ __device__ __forceinline__ uint32_t pages_for(uint32_t n, double per_page) {
   return n == 0 ? 0 : pages_below(n - 1, per_page) + 1;
 }
 
-__global__ __launch_bounds__(kTableThreads) void page_tables(ar_page_tables_args a, double per_page) {
+// Workgroups below `token_blocks` write the tokens' outputs, the others the tables' new entries.
+__global__ __launch_bounds__(kTableThreads) void page_tables(ar_page_tables_args a, double per_page, int token_blocks) {
   __shared__ uint32_t q_start[kMaxRequests + 1];
   __shared__ uint32_t page_at[kMaxRequests];  // pages taken by the requests before
   __shared__ int32_t held[kMaxRequests];      // tokens of a request, -1 where it is refused
@@ -109,8 +112,19 @@ __global__ __launch_bounds__(kTableThreads) void page_tables(ar_page_tables_args
     a.pool_out[1] = a.pool[1];
   }
 
-  const uint32_t stride = gridDim.x * kTableThreads;
-  for (uint32_t i = blockIdx.x * kTableThreads + tid; i < places; i += stride) {
+  const int block = blockIdx.x;
+  if (block >= token_blocks) {
+    // New pages: entries below a request's first new page are only read (below), those from it on
+    // only written here, so the two never meet.
+    const uint32_t stride = (gridDim.x - token_blocks) * kTableThreads;
+    for (uint32_t i = (block - token_blocks) * kTableThreads + tid; i < taken; i += stride) {
+      const int b = last_at_most(page_at, n, i);
+      a.table[b * a.table_stride + pages_for(held[b], per_page) + (i - page_at[b])] = a.free_pages[head + i];
+    }
+    return;
+  }
+  const uint32_t stride = token_blocks * kTableThreads;
+  for (uint32_t i = block * kTableThreads + tid; i < places; i += stride) {
     int64_t slot = -1;
     int32_t pos = -1;
     if (i < end) {
@@ -126,12 +140,6 @@ __global__ __launch_bounds__(kTableThreads) void page_tables(ar_page_tables_args
     }
     a.slots[i] = slot;
     a.positions[i] = pos;
-  }
-  // New pages: entries below a request's first new page are read above, those from it on are
-  // written here, so the two never meet.
-  for (uint32_t i = blockIdx.x * kTableThreads + tid; i < taken; i += stride) {
-    const int b = last_at_most(page_at, n, i);
-    a.table[b * a.table_stride + pages_for(held[b], per_page) + (i - page_at[b])] = a.free_pages[head + i];
   }
 }
 
@@ -155,10 +163,15 @@ extern "C" int ar_page_tables(const ar_page_tables_args* a, void* stream) {
   if (a->nfree > 0 && a->free_pages == nullptr) return ar_fail(AR_EINVAL, "null free list");
   if (a->pool_out == a->pool || (a->nreq > 0 && (a->kv_len == a->cached_len || a->kv_len == a->new_len)))
     return ar_fail(AR_EINVAL, "pool_out and kv_len must not be the buffers that the call reads");
-  // A token a thread: the sums that every workgroup repeats are short against a second round.
-  const int blocks = max(1, min(256, (a->ntokens + ard::kTableThreads - 1) / ard::kTableThreads));
-  hipLaunchKernelGGL(ard::page_tables, dim3(blocks), dim3(ard::kTableThreads), 0,
-                     static_cast<hipStream_t>(stream), *a, 1.0 / a->page_size);
+  // A token or a new page a thread: the sums that every workgroup repeats are short against a second
+  // round.
+  const auto blocks = [](int64_t n) {
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(256, (n + ard::kTableThreads - 1) / ard::kTableThreads)));
+  };
+  const int token_blocks = blocks(a->ntokens);
+  const int page_blocks = blocks(std::min<int64_t>(a->nfree, a->ntokens / a->page_size + a->nreq));
+  hipLaunchKernelGGL(ard::page_tables, dim3(token_blocks + page_blocks), dim3(ard::kTableThreads), 0,
+                     static_cast<hipStream_t>(stream), *a, 1.0 / a->page_size, token_blocks);
   AR_HIP(hipGetLastError());
   return AR_OK;
 }
