@@ -8,13 +8,15 @@
 
 namespace {
 
-// The kernel for a call. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose parts join quickly. Tiles of 128 rows, waves on different
-// rows: values are converted once for all of them, but a job is four times as long and so is its
-// join, so they pay where the tiles alone fill the device's 512 places, or the tokens behind them
-// (their bound, the tables' width) do. Measured, head_dim 128, 4 kv heads of 8 query heads, small
+// The kernel for a call. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose
+// parts join quickly. Tiles of 128 rows, waves on different rows: values are converted once for all
+// of them, but a job is four times as long and so is its join, so they pay where the tiles alone
+// fill the device's 512 places and have some tokens to read, or where the tokens behind them (their
+// bound, the tables' width) are many. Measured, head_dim 128, 4 kv heads of 8 query heads, small
 // tiles against large: 8 requests of 256 rows, 4096 tokens 43 and 67 us; of 1024 rows 106 and 122;
 // of 2048 rows (512 tiles) 206 and 193; of 8192 rows 810 and 540; one of 4096 rows and 16384 tokens
-// (128 tiles) 199 and 183. Binary32, three products for one, stays with the small tiles.
+// (128 tiles) 199 and 183; head_dim 64, 552 tiles of one prompt, 786 tokens 64 and 49; 528 tiles,
+// 355 tokens at most 37 and 56. Binary32, three products for one, stays with the small tiles.
 constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
 struct Choice {
@@ -32,7 +34,8 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
     const int64_t tiles = (each + large - 1) / large * std::min(a->nreq, a->ntokens) * h->heads;
     const int64_t tokens = static_cast<int64_t>(a->table_width) << h->page_shift;
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
-    if (tiles >= kManyTiles || tiles * units >= kManyUnits) return {ard::select_attn_rows(h->head_dim), large, true};
+    if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
+      return {ard::select_attn_rows(h->head_dim), large, true};
   }
   // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
   // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and

@@ -343,6 +343,47 @@ __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, i
   }
 }
 
+// The same for many rows and at most N parts: a thread has N parts of I segments under way at once.
+template <int D, int R, int N, int I, class F>
+__device__ __forceinline__ void join_few(ar::rsrc_t part, uint32_t stats_at, int first_wg, int parts, int rows,
+                                         F finish) {
+  constexpr int NC = D / 8;
+  const int items = rows * NC;
+  for (int x0 = threadIdx.x; x0 < items; x0 += I * kAttnThreads) {
+    u32x2 st[I][N];
+    u32x4 v0[I][N], v1[I][N];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int x = min(x0 + i * kAttnThreads, items - 1), r = x / NC, seg = x - r * NC;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int p = min(k, parts - 1);
+        const uint32_t at = static_cast<uint32_t>((2 * (first_wg + p) + (p == 0)) * R + r);
+        st[i][k] = ar::ld8<ar::kCoh>(part, stats_at + at * 8);
+        v0[i][k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8) * 4);
+        v1[i][k] = ar::ld16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int x = x0 + i * kAttnThreads, r = x / NC, seg = x - r * NC;
+      float top = -INFINITY, rl = 0.0f;
+      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < parts) top = fmaxf(top, __uint_as_float(st[i][k].x));
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (k >= parts) continue;
+        const float f = top == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[i][k].x) - top);
+        rl += __uint_as_float(st[i][k].y) * f;
+        o0 += __builtin_bit_cast(f32x4, v0[i][k]) * f, o1 += __builtin_bit_cast(f32x4, v1[i][k]) * f;
+      }
+      if (x < items) finish(r, seg, o0, o1, top, rl);
+    }
+  }
+}
+
 template <int DT, int D, int NQ, int OCC>
 __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args) {
   constexpr int R = 16 * NQ;

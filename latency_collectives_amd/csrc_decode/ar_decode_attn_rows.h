@@ -536,9 +536,12 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
           const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
           finish_row<DT_BF16>(a, me.q0 + i, head, seg, o0, o1, top, rl);
         };
-        if (arrive(args.arrived + first_wg, parts, &last))
-          join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0),
-                              reinterpret_cast<float*>(values), finish);
+        if (arrive(args.arrived + first_wg, parts, &last)) {
+          const int real = min(R, rows - row0);
+          if (parts == 2) join_few<D, R, 2, 4>(part, args.stats_at, first_wg, parts, real, finish);
+          else if (parts <= 4) join_few<D, R, 4, 2>(part, args.stats_at, first_wg, parts, real, finish);
+          else join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, real, reinterpret_cast<float*>(values), finish);
+        }
       }
     }
     if (run.left <= 0) return;
