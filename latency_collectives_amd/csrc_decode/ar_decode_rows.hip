@@ -306,8 +306,11 @@ int launch_norm_rope(RowArgs& r, hipStream_t stream) {
   r.per_dim = 1.0 / r.a.head_dim;
   r.run = pick_run(r.a.ntokens, rows, g);
   // More than the XCDs' L2 hold is not read from there again: 8191 tokens of 40 heads 42 and 38 us.
-  const bool pass = !CACHE && static_cast<int64_t>(r.a.ntokens) * (r.a.q_heads + r.a.kv_heads) * r.a.head_dim *
-               (r.a.dtype == AR_BFLOAT16 ? 2 : 4) > (int64_t(32) << 20);
+  // Only where every store is of neighbouring lanes' neighbouring elements: halves of lines that
+  // go past the L2 one by one took 29 us for 8000 tokens of 17 interleaved heads of 64 in binary32, 18 us through it.
+  const bool pass = !CACHE && !r.a.interleaved && r.a.rot == r.a.head_dim &&
+                    static_cast<int64_t>(r.a.ntokens) * (r.a.q_heads + r.a.kv_heads) * r.a.head_dim *
+                            (r.a.dtype == AR_BFLOAT16 ? 2 : 4) > (int64_t(32) << 20);
   const auto runs = [&](int heads) { return (heads + r.run - 1) / r.run; };
   r.q_runs = runs(r.a.q_heads), r.k_runs = runs(r.a.kv_heads);
   const int in_y = r.q_runs + r.k_runs + runs(r.values);
