@@ -421,250 +421,250 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
   }
 
   for (;;) {
-  // Rows of this tile and what each sees.
-  const int rows = me.m * group;
-  const int row0 = run.tile * R;
-  int i0 = 0;
-  if (run.tile > 0) i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group));
-  const int rem0 = row0 - i0 * group;
-  // token and head in the group of row row0 + r: rem0 + r is below 2^17, exact in binary32
-  auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * args.per_group); };
-  const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
-  const int kv_end = min(me.kv, args.room);
-  const int first_pos = me.kv - me.m;  // position of the request's first new token
-  const int end = min(max(first_pos + i1 + 1, 0), kv_end);
-  int begin = 0;
-  if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
-  const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
-  const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
-  const int taken = min(run.left, me.span - run.at);  // units of the run in this job
-  const int t_first = run.at << args.tile_shift;
-  const int t_last = min((run.at + taken) << args.tile_shift, ntiles);
-  run.left -= taken;
-  // Parts of the job: part 0 is the workgroup that holds its first unit, slot 2 * (that) + 1; the
-  // others hold nothing before it in their runs, slot 2 * (theirs).
-  int before = 0, first_units = taken;  // parts before this one, units of part 0
-  if (run.at > 0) {
-    before = uniform(static_cast<uint32_t>(run.at + run.per - 1) / static_cast<uint32_t>(run.per));
-    first_units = run.at - (before - 1) * run.per;
-  }
-  const int first_wg = w - before;
-  int parts = 1;
-  if (nunits > first_units)
-    parts = 1 + uniform(static_cast<uint32_t>(nunits - first_units + run.per - 1) / static_cast<uint32_t>(run.per));
-  if (run.at == 0 || t_first < ntiles) {
-  const uint8_t* data = args.cache.data + static_cast<int64_t>(run.head) * 2 * k_bytes;
-  const uint8_t* scales = args.cache.scales + static_cast<int64_t>(run.head) * 2 * s_bytes;
-  const int32_t* table = a.table + run.request * a.table_stride;
+    // Rows of this tile and what each sees.
+    const int rows = me.m * group;
+    const int row0 = run.tile * R;
+    int i0 = 0;
+    if (run.tile > 0) i0 = uniform(static_cast<uint32_t>(row0) / static_cast<uint32_t>(group));
+    const int rem0 = row0 - i0 * group;
+    // token and head in the group of row row0 + r: rem0 + r is below 2^17, exact in binary32
+    auto token_of = [&](int r) { return static_cast<int>((rem0 + r + 0.5f) * args.per_group); };
+    const int i1 = i0 + uniform(token_of(min(R, rows - row0) - 1));
+    const int kv_end = min(me.kv, args.room);
+    const int first_pos = me.kv - me.m;  // position of the request's first new token
+    const int end = min(max(first_pos + i1 + 1, 0), kv_end);
+    int begin = 0;
+    if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
+    const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
+    const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
+    const int taken = min(run.left, me.span - run.at);  // units of the run in this job
+    const int t_first = run.at << args.tile_shift;
+    const int t_last = min((run.at + taken) << args.tile_shift, ntiles);
+    run.left -= taken;
+    // Parts of the job: part 0 is the workgroup that holds its first unit, slot 2 * (that) + 1; the
+    // others hold nothing before it in their runs, slot 2 * (theirs).
+    int before = 0, first_units = taken;  // parts before this one, units of part 0
+    if (run.at > 0) {
+      before = uniform(static_cast<uint32_t>(run.at + run.per - 1) / static_cast<uint32_t>(run.per));
+      first_units = run.at - (before - 1) * run.per;
+    }
+    const int first_wg = w - before;
+    int parts = 1;
+    if (nunits > first_units)
+      parts = 1 + uniform(static_cast<uint32_t>(nunits - first_units + run.per - 1) / static_cast<uint32_t>(run.per));
+    if (run.at == 0 || t_first < ntiles) {
+      const uint8_t* data = args.cache.data + static_cast<int64_t>(run.head) * 2 * k_bytes;
+      const uint8_t* scales = args.cache.scales + static_cast<int64_t>(run.head) * 2 * s_bytes;
+      const int32_t* table = a.table + run.request * a.table_stride;
 
-  // Where the keys of this wave's next 32 tiles and their scales start: lane 2 k + u has the u-th
-  // half of the k-th, a valid place where there is nothing to see. One page id a tile would make
-  // the wave wait for its keys and values with it.
-  auto pages = [&](int tile) {
-    const int mine = tile + (lane >> 1) * kAttnWaves, t = begin + mine * 32 + (lane & 1) * 16;
-    return mine < t_last && t < end ? table[t >> shift] : -1;
-  };
-  uint64_t k_at, s_at, seen;
-  auto settle = [&](int p) {
-    const bool some = p >= 0 && p < num_pages;
-    const int64_t at = some ? p : 0;
-    const int off = (begin + (t_first + wave) * 32 + (lane & 1) * 16 + (lane >> 1) * (kAttnWaves * 32)) & (page - 1);
-    k_at = reinterpret_cast<uint64_t>(data) + at * args.page_bytes + off * (D / 2);
-    s_at = reinterpret_cast<uint64_t>(scales) + at * args.page_scales + off;
-    seen = __ballot(some);
-  };
-  int ids = pages(t_first + wave);  // under way with the queries
+      // Where the keys of this wave's next 32 tiles and their scales start: lane 2 k + u has the u-th
+      // half of the k-th, a valid place where there is nothing to see. One page id a tile would make
+      // the wave wait for its keys and values with it.
+      auto pages = [&](int tile) {
+        const int mine = tile + (lane >> 1) * kAttnWaves, t = begin + mine * 32 + (lane & 1) * 16;
+        return mine < t_last && t < end ? table[t >> shift] : -1;
+      };
+      uint64_t k_at, s_at, seen;
+      auto settle = [&](int p) {
+        const bool some = p >= 0 && p < num_pages;
+        const int64_t at = some ? p : 0;
+        const int off = (begin + (t_first + wave) * 32 + (lane & 1) * 16 + (lane >> 1) * (kAttnWaves * 32)) & (page - 1);
+        k_at = reinterpret_cast<uint64_t>(data) + at * args.page_bytes + off * (D / 2);
+        s_at = reinterpret_cast<uint64_t>(scales) + at * args.page_scales + off;
+        seen = __ballot(some);
+      };
+      int ids = pages(t_first + wave);  // under way with the queries
 
-  int hi[NQ], lo[NQ];
-  bf16x8 q[NQ][PARTS][kDw];
+      int hi[NQ], lo[NQ];
+      bf16x8 q[NQ][PARTS][kDw];
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int row = row0 + n * 16 + c;
-    const bool real = row < rows;  // others repeat the last row, with nothing to see
-    const int r = min(n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
-    const int pos = first_pos + i;
-    hi[n] = real ? min(pos + 1, kv_end) : 0;
-    lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
-    const int64_t at = static_cast<int64_t>(me.q0 + i) * a.q_token +
-                       static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head + g * (D / 4);
+      for (int n = 0; n < NQ; ++n) {
+        const int row = row0 + n * 16 + c;
+        const bool real = row < rows;  // others repeat the last row, with nothing to see
+        const int r = min(n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
+        const int pos = first_pos + i;
+        hi[n] = real ? min(pos + 1, kv_end) : 0;
+        lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+        const int64_t at = static_cast<int64_t>(me.q0 + i) * a.q_token +
+                           static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head + g * (D / 4);
 #pragma unroll
-    for (int s = 0; s < kDw; ++s) {
-      if (DT == DT_BF16) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at + s * 8);
-        q[n][0][s] = __builtin_bit_cast(bf16x8, w);
-      } else {
-        float x[8];
-        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at + s * 8);
-        const f32x4 v0 = p[0], v1 = p[1];
+        for (int s = 0; s < kDw; ++s) {
+          if (DT == DT_BF16) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at + s * 8);
+            q[n][0][s] = __builtin_bit_cast(bf16x8, w);
+          } else {
+            float x[8];
+            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at + s * 8);
+            const f32x4 v0 = p[0], v1 = p[1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = v0[j], x[4 + j] = v1[j];
-        bf16x8 w[PARTS];
-        split<PARTS>(x, w);
+            for (int j = 0; j < 4; ++j) x[j] = v0[j], x[4 + j] = v1[j];
+            bf16x8 w[PARTS];
+            split<PARTS>(x, w);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) q[n][p][s] = w[p];
-      }
-    }
-  }
-  // Tiles from here on need masks: the first row's end, the last row's window.
-  const int whole_end = min(first_pos + i0 + 1, kv_end);
-  const int whole_begin = a.window > 0 ? first_pos + i1 - a.window + 1 : 0;
-
-  f32x4 acc[NQ][kSets][8];
-  float m[NQ], l[NQ];
-  int nan_groups[NQ];  // groups of 32 elements in which a visible value is NaN
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
-#pragma unroll
-    for (int e = 0; e < kSets; ++e)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
-  }
-
-  auto load_keys = [&](int k, Tile& x) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
-      load_dwords<kDw>(kd, k_off, x.k[u]);
-#pragma unroll
-      for (int s = 0; s < kKs; ++s)
-        x.ks[u][s] = load_at<uint8_t>(sd, min(k_group + s, D / 32 - 1) * page + c);
-    }
-  };
-  auto load_values = [&](int k, Tile& x) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
-#pragma unroll
-      for (int e = 0; e < kSets; ++e) {
-        x.v[u][e] = load_at<u32x4>(kd, v_off[e]);
-        x.vs[u][e] = load_at<uint32_t>(sd, vs_off[e]);
-      }
-    }
-  };
-
-  // The first round only loads: one copy of this code.
-  Tile now, next;
-  int tile = t_first + wave - kAttnWaves, turn = 0;
-  int both = 0, both_next;  // the halves that have a page
-  for (; tile < t_last; tile += kAttnWaves) {
-    if ((turn & 31) == 0) {
-      settle(ids);
-      ids = pages(tile + 33 * kAttnWaves);
-    }
-    both_next = static_cast<int>(seen >> (2 * (turn & 31))) & 3;
-    const int k_next = turn++ & 31;
-    if (!kLate) load_keys(k_next, next);
-    load_values(k_next, next);
-    f32x4 s[NQ][2];
-    const int t0 = begin + tile * 32;
-    // Scores.
-    if (tile >= t_first) {
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float sc[kKs];
-#pragma unroll
-      for (int i = 0; i < kKs; ++i) sc[i] = scale_of(now.ks[u][i]);
-#pragma unroll
-      for (int i = 0; i < kDw; ++i) {
-        float x = sc[0];
-        if (kKs > 1) x = ((g * kDw + i) >> 2) == k_group ? sc[0] : sc[kKs - 1];
-        const uint32_t w = now.k[u][i];
-        const bf16x8 kk = operand(codes<0>(w, x), codes<1>(w, x), codes<2>(w, x), codes<3>(w, x));
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) s[n][u] = mfma(kk, q[n][p][i], s[n][u]);
-      }
-    }
-    }
-    if (kLate) load_keys(k_next, now);
-    if (tile >= t_first) {
-    const bool partial = t0 + 32 > whole_end || t0 < whole_begin || both != 3;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
-    if (partial) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + u * 16 + g * 4 + i;
-            if (t >= hi[n] || t < lo[n] || (both >> u & 1) == 0) s[n][u][i] = -INFINITY;
+            for (int p = 0; p < PARTS; ++p) q[n][p][s] = w[p];
           }
-    }
-
-    // Values that are NaN (or bytes that were never written) must not meet the zeros of rows that
-    // do not see them: such groups are read as finite and the rows that do see them noted.
-    uint32_t odd = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int e = 0; e < kSets; ++e) odd |= nan_bytes(now.vs[u][e]);
-    if (__any(odd != 0)) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < kSets; ++e) {
-          uint32_t bad = nan_bytes(now.vs[u][e]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // the groups of this set, held by lanes c = 4k
-            const int group32 = e * 4 + k;
-            if (group32 >= D / 32) break;
-            const uint32_t theirs = __shfl(static_cast<int>(bad), g * 16 + 4 * k);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = t0 + u * 16 + g * 4 + i;
-                if ((theirs >> (8 * i + 7) & 1) && t < hi[n] && t >= lo[n] && (both >> u & 1) != 0)
-                  nan_groups[n] |= 1 << group32;
-              }
-          }
-          bad |= bad >> 1, bad |= bad >> 2, bad |= bad >> 4;
-          now.vs[u][e] &= ~bad;  // 2^-127 or so: finite
         }
-    }
+      }
+      // Tiles from here on need masks: the first row's end, the last row's window.
+      const int whole_end = min(first_pos + i0 + 1, kv_end);
+      const int whole_begin = a.window > 0 ? first_pos + i1 - a.window + 1 : 0;
 
-    // Probabilities.
-    bf16x8 pr[NQ][PARTS];
+      f32x4 acc[NQ][kSets][8];
+      float m[NQ], l[NQ];
+      int nan_groups[NQ];  // groups of 32 elements in which a visible value is NaN
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3];
-      float top = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-      if (__any(top > m[n] + 8.0f)) {
-        const float to = fmaxf(m[n], row_max(top));
-        const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
-        m[n] = to;
-        l[n] *= f;
+      for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
 #pragma unroll
         for (int e = 0; e < kSets; ++e)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
+          for (int j = 0; j < 8; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
       }
-      const float ref = m[n] == -INFINITY ? 0.0f : m[n];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = exp2_fast(x[i] - ref);
-        l[n] += x[i];
-      }
-      split<PARTS>(x, pr[n]);
-    }
 
-    // Values.
+      auto load_keys = [&](int k, Tile& x) {
 #pragma unroll
-    for (int e = 0; e < kSets; ++e) {
-      float sc[8];
+        for (int u = 0; u < 2; ++u) {
+          const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
+          load_dwords<kDw>(kd, k_off, x.k[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sc[i] = __uint_as_float((now.vs[i >> 2][e] >> (8 * (i & 3)) & 0xFFu) << 23);
+          for (int s = 0; s < kKs; ++s)
+            x.ks[u][s] = load_at<uint8_t>(sd, min(k_group + s, D / 32 - 1) * page + c);
+        }
+      };
+      auto load_values = [&](int k, Tile& x) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const global_bytes kd = lane_address(k_at, 2 * k + u), sd = lane_address(s_at, 2 * k + u);
+#pragma unroll
+          for (int e = 0; e < kSets; ++e) {
+            x.v[u][e] = load_at<u32x4>(kd, v_off[e]);
+            x.vs[u][e] = load_at<uint32_t>(sd, vs_off[e]);
+          }
+        }
+      };
+
+      // The first round only loads: one copy of this code.
+      Tile now, next;
+      int tile = t_first + wave - kAttnWaves, turn = 0;
+      int both = 0, both_next;  // the halves that have a page
+      for (; tile < t_last; tile += kAttnWaves) {
+        if ((turn & 31) == 0) {
+          settle(ids);
+          ids = pages(tile + 33 * kAttnWaves);
+        }
+        both_next = static_cast<int>(seen >> (2 * (turn & 31))) & 3;
+        const int k_next = turn++ & 31;
+        if (!kLate) load_keys(k_next, next);
+        load_values(k_next, next);
+        f32x4 s[NQ][2];
+        const int t0 = begin + tile * 32;
+        // Scores.
+        if (tile >= t_first) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float sc[kKs];
+#pragma unroll
+            for (int i = 0; i < kKs; ++i) sc[i] = scale_of(now.ks[u][i]);
+#pragma unroll
+            for (int i = 0; i < kDw; ++i) {
+              float x = sc[0];
+              if (kKs > 1) x = ((g * kDw + i) >> 2) == k_group ? sc[0] : sc[kKs - 1];
+              const uint32_t w = now.k[u][i];
+              const bf16x8 kk = operand(codes<0>(w, x), codes<1>(w, x), codes<2>(w, x), codes<3>(w, x));
+#pragma unroll
+              for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) s[n][u] = mfma(kk, q[n][p][i], s[n][u]);
+            }
+          }
+        }
+        if (kLate) load_keys(k_next, now);
+        if (tile >= t_first) {
+          const bool partial = t0 + 32 > whole_end || t0 < whole_begin || both != 3;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
+          if (partial) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int t = t0 + u * 16 + g * 4 + i;
+                  if (t >= hi[n] || t < lo[n] || (both >> u & 1) == 0) s[n][u][i] = -INFINITY;
+                }
+          }
+
+          // Values that are NaN (or bytes that were never written) must not meet the zeros of rows that
+          // do not see them: such groups are read as finite and the rows that do see them noted.
+          uint32_t odd = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < kSets; ++e) odd |= nan_bytes(now.vs[u][e]);
+          if (__any(odd != 0)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int e = 0; e < kSets; ++e) {
+                uint32_t bad = nan_bytes(now.vs[u][e]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // the groups of this set, held by lanes c = 4k
+                  const int group32 = e * 4 + k;
+                  if (group32 >= D / 32) break;
+                  const uint32_t theirs = __shfl(static_cast<int>(bad), g * 16 + 4 * k);
+#pragma unroll
+                  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const int t = t0 + u * 16 + g * 4 + i;
+                      if ((theirs >> (8 * i + 7) & 1) && t < hi[n] && t >= lo[n] && (both >> u & 1) != 0)
+                        nan_groups[n] |= 1 << group32;
+                    }
+                }
+                bad |= bad >> 1, bad |= bad >> 2, bad |= bad >> 4;
+                now.vs[u][e] &= ~bad;  // 2^-127 or so: finite
+              }
+          }
+
+          // Probabilities.
+          bf16x8 pr[NQ][PARTS];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3];
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+            if (__any(top > m[n] + 8.0f)) {
+              const float to = fmaxf(m[n], row_max(top));
+              const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
+              m[n] = to;
+              l[n] *= f;
+#pragma unroll
+              for (int e = 0; e < kSets; ++e)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
+            }
+            const float ref = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              x[i] = exp2_fast(x[i] - ref);
+              l[n] += x[i];
+            }
+            split<PARTS>(x, pr[n]);
+          }
+
+          // Values.
+#pragma unroll
+          for (int e = 0; e < kSets; ++e) {
+            float sc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              sc[i] = __uint_as_float((now.vs[i >> 2][e] >> (8 * (i & 3)) & 0xFFu) << 23);
 #define ARD_PAIR(B)                                                                              \
   {                                                                                              \
     uint32_t w[8];                                                                               \
@@ -678,102 +678,102 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       acc[n][e][2 * B + 1] = mfma(v1, pr[n][p], acc[n][e][2 * B + 1]);                           \
     }                                                                                            \
   }
-      ARD_PAIR(0) ARD_PAIR(1) ARD_PAIR(2) ARD_PAIR(3)
+            ARD_PAIR(0) ARD_PAIR(1) ARD_PAIR(2) ARD_PAIR(3)
 #undef ARD_PAIR
-    }
-    }
-    if (kLate) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < kSets; ++e) now.v[u][e] = next.v[u][e], now.vs[u][e] = next.vs[u][e];
-    } else {
-      now = next;
-    }
-    both = both_next;
-  }
-
-  // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    l[n] = row_sum(l[n]);
-    nan_groups[n] = row_or(nan_groups[n]);
-    if (g == 0) stat_m[wave][n * 16 + c] = m[n], stat_l[wave][n * 16 + c] = l[n];
-  }
-  __syncthreads();
-  const int seg_per = NC;  // eight elements a thread
-  const bool alone = parts == 1;
-  auto finish = [&](int r, int seg, f32x4 o0, f32x4 o1, float top, float rl) {
-    const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
-    finish_row<DT>(a, me.q0 + i, head, seg, o0, o1, top, rl);
-  };
-  const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float top = stat_m[0][n * 16 + c];
-#pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][n * 16 + c]);
-    const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
-    if (__any(nan_groups[n] != 0)) {
-#pragma unroll
-      for (int e = 0; e < kSets; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (nan_groups[n] >> ((e * 16 + g * 4 + i) >> 2) & 1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[n][e][j][i] = __uint_as_float(0x7FC00000u);
-          }
-    }
-    float* mine = join + (wave * 16 + c) * kPitch;
-#pragma unroll
-    for (int e = 0; e < kSets; ++e)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int chunk = e * 16 + g * 4 + i;
-        if (chunk < NC) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f32x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = acc[n][e][4 * h + j][i] * f;
-            *reinterpret_cast<f32x4*>(mine + chunk * 8 + 4 * h) = v;
           }
         }
-      }
-    __syncthreads();
-    for (int x = tid; x < 16 * seg_per; x += kAttnThreads) {
-      const int r = x / seg_per, seg = x - r * seg_per, row = row0 + n * 16 + r;
-      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
-      float rm = stat_m[0][n * 16 + r], rl = 0.0f;
+        if (kLate) {
 #pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) rm = fmaxf(rm, stat_m[w][n * 16 + r]);
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
-        const float* p = join + (w * 16 + r) * kPitch + seg * 8;
-        o0 += *reinterpret_cast<const f32x4*>(p);
-        o1 += *reinterpret_cast<const f32x4*>(p + 4);
-        if (rm != -INFINITY) rl += stat_l[w][n * 16 + r] * exp2_fast(stat_m[w][n * 16 + r] - rm);
+            for (int e = 0; e < kSets; ++e) now.v[u][e] = next.v[u][e], now.vs[u][e] = next.vs[u][e];
+        } else {
+          now = next;
+        }
+        both = both_next;
       }
-      if (row >= rows) continue;
-      if (!alone) {
-        const uint32_t at = static_cast<uint32_t>((2 * w + (before == 0)) * R + n * 16 + r);
-        ar::st16<ar::kCoh>(part, (at * D + seg * 8) * 4, __builtin_bit_cast(u32x4, o0));
-        ar::st16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4, __builtin_bit_cast(u32x4, o1));
-        if (seg == 0)
-          ar::st8<ar::kCoh>(part, args.stats_at + at * 8, u32x2{__float_as_uint(rm), __float_as_uint(rl)});
-        continue;
+
+      // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        l[n] = row_sum(l[n]);
+        nan_groups[n] = row_or(nan_groups[n]);
+        if (g == 0) stat_m[wave][n * 16 + c] = m[n], stat_l[wave][n * 16 + c] = l[n];
       }
-      finish(n * 16 + r, seg, o0, o1, rm, rl);
+      __syncthreads();
+      const int seg_per = NC;  // eight elements a thread
+      const bool alone = parts == 1;
+      auto finish = [&](int r, int seg, f32x4 o0, f32x4 o1, float top, float rl) {
+        const int i = i0 + token_of(r), head = run.head * group + row0 + r - i * group;
+        finish_row<DT>(a, me.q0 + i, head, seg, o0, o1, top, rl);
+      };
+      const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float top = stat_m[0][n * 16 + c];
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][n * 16 + c]);
+        const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
+        if (__any(nan_groups[n] != 0)) {
+#pragma unroll
+          for (int e = 0; e < kSets; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (nan_groups[n] >> ((e * 16 + g * 4 + i) >> 2) & 1) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[n][e][j][i] = __uint_as_float(0x7FC00000u);
+              }
+        }
+        float* mine = join + (wave * 16 + c) * kPitch;
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int chunk = e * 16 + g * 4 + i;
+            if (chunk < NC) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                f32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = acc[n][e][4 * h + j][i] * f;
+                *reinterpret_cast<f32x4*>(mine + chunk * 8 + 4 * h) = v;
+              }
+            }
+          }
+        __syncthreads();
+        for (int x = tid; x < 16 * seg_per; x += kAttnThreads) {
+          const int r = x / seg_per, seg = x - r * seg_per, row = row0 + n * 16 + r;
+          f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+          float rm = stat_m[0][n * 16 + r], rl = 0.0f;
+#pragma unroll
+          for (int w = 1; w < kAttnWaves; ++w) rm = fmaxf(rm, stat_m[w][n * 16 + r]);
+#pragma unroll
+          for (int w = 0; w < kAttnWaves; ++w) {
+            const float* p = join + (w * 16 + r) * kPitch + seg * 8;
+            o0 += *reinterpret_cast<const f32x4*>(p);
+            o1 += *reinterpret_cast<const f32x4*>(p + 4);
+            if (rm != -INFINITY) rl += stat_l[w][n * 16 + r] * exp2_fast(stat_m[w][n * 16 + r] - rm);
+          }
+          if (row >= rows) continue;
+          if (!alone) {
+            const uint32_t at = static_cast<uint32_t>((2 * w + (before == 0)) * R + n * 16 + r);
+            ar::st16<ar::kCoh>(part, (at * D + seg * 8) * 4, __builtin_bit_cast(u32x4, o0));
+            ar::st16<ar::kCoh>(part, (at * D + seg * 8 + 4) * 4, __builtin_bit_cast(u32x4, o1));
+            if (seg == 0)
+              ar::st8<ar::kCoh>(part, args.stats_at + at * 8, u32x2{__float_as_uint(rm), __float_as_uint(rl)});
+            continue;
+          }
+          finish(n * 16 + r, seg, o0, o1, rm, rl);
+        }
+        if (n + 1 < NQ) __syncthreads();
+      }
+      if (!alone && arrive(args.arrived + first_wg, parts, &last))
+        join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0), join, finish);
     }
-    if (n + 1 < NQ) __syncthreads();
-  }
-  if (!alone && arrive(args.arrived + first_wg, parts, &last))
-    join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0), join, finish);
-  }
-  if (run.left <= 0) return;
-  next_job<R>(args, run, me);
-  if (run.left <= 0) return;
-  __syncthreads();  // the next job's joins use the same LDS
+    if (run.left <= 0) return;
+    next_job<R>(args, run, me);
+    if (run.left <= 0) return;
+    __syncthreads();  // the next job's joins use the same LDS
   }
 }
 
