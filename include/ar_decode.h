@@ -154,8 +154,9 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * kv_len[b], token i of m at position p = kv_len - m + i,
  *   out[i] = sum_t softmax_t(scale * q[i] . k[t]) v[t]  over 0 <= t <= p, t < kv_len, and with
  * window > 0 also t > p - window. q has q_heads = kv_heads * group heads, head h reads kv head
- * h / group. A row that sees nothing (p < 0) gives zeros and lse = -inf. lse [ntokens][q_heads],
- * or NULL, is the natural logarithm of the row's sum of exponentials. Statistics and sums are
+ * h / group. A row that sees nothing (p < 0) gives zeros and lse = -inf; one with a NaN score (a NaN
+ * or infinite query, a visible NaN key) NaN for both. lse [ntokens][q_heads], or NULL, is the
+ * natural logarithm of the row's sum of exponentials. Statistics and sums are
  * binary32; probabilities are rounded to bfloat16 for AR_BFLOAT16 (their products with the values,
  * which 4 bits hold exactly, are summed in binary32), kept to 24 bits for AR_FLOAT32. Where
  * requests bring more than 128 rows (tokens x group) on average and enough of them, AR_BFLOAT16

@@ -3,7 +3,9 @@
 // Mathematics. One pass over the keys and values with a running reference m and sum l per row:
 // s = scale q.k in base-2 units, p = 2^(s - m), l += p, o += p v; where a row's maximum passes m by
 // more than 8, l and o are scaled by 2^(m - m') first (p then stays below 2^8, far from any
-// limit). Parts of a row are joined by the same rule.
+// limit). Parts of a row are joined by the same rule. m starts from a finite value: a masked score
+// (minus infinity) less it is minus infinity without a test, and a NaN score, which a maximum
+// passes over, still reaches l. So l is 0 only where a row sees nothing.
 //
 // Shape. The products run transposed, so that nothing is moved between lanes in the loop:
 //   S^T [32 tokens x 16 rows]  = K  [tokens x D]  Q^T      two 16x16x32 tiles
@@ -59,6 +61,9 @@ __device__ __forceinline__ int row_or(int x) {
   return x | __shfl_xor(x, 32);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A running maximum that no score has reached yet: the lowest finite value.
+constexpr float kLowest = -3.4028235e38f;
 
 // x as a sum of PARTS bfloat16 values (three hold all 24 bits). An infinity or NaN stays in the
 // first part alone.
@@ -310,11 +315,11 @@ __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, i
         if (p0 + k * groups >= parts) st[k].x = 0xFF800000u;  // -infinity
         to = fmaxf(to, __uint_as_float(st[k].x));
       }
-      const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
+      const float f0 = exp2_fast(top - to);
       o0 *= f0, o1 *= f0, rl *= f0;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float f = to == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[k].x) - to);
+        const float f = exp2_fast(__uint_as_float(st[k].x) - to);
         rl += __uint_as_float(st[k].y) * f;
         o0 += __builtin_bit_cast(f32x4, v0[k]) * f, o1 += __builtin_bit_cast(f32x4, v1[k]) * f;
       }
@@ -332,8 +337,7 @@ __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, i
         for (int k = 1; k < groups; ++k) {
           const float* p = lds + (k * items + x) * 12;
           const float to = fmaxf(top, p[8]);
-          const float f0 = to == -INFINITY ? 0.0f : exp2_fast(top - to);
-          const float f1 = to == -INFINITY ? 0.0f : exp2_fast(p[8] - to);
+          const float f0 = exp2_fast(top - to), f1 = exp2_fast(p[8] - to);
           o0 = o0 * f0 + *reinterpret_cast<const f32x4*>(p) * f1;
           o1 = o1 * f0 + *reinterpret_cast<const f32x4*>(p + 4) * f1;
           rl = rl * f0 + p[9] * f1, top = to;
@@ -375,7 +379,7 @@ __device__ __forceinline__ void join_few(ar::rsrc_t part, uint32_t stats_at, int
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         if (k >= parts) continue;
-        const float f = top == -INFINITY ? 0.0f : exp2_fast(__uint_as_float(st[i][k].x) - top);
+        const float f = exp2_fast(__uint_as_float(st[i][k].x) - top);
         rl += __uint_as_float(st[i][k].y) * f;
         o0 += __builtin_bit_cast(f32x4, v0[i][k]) * f, o1 += __builtin_bit_cast(f32x4, v1[i][k]) * f;
       }
@@ -514,7 +518,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       int nan_groups[NQ];  // groups of 32 elements in which a visible value is NaN
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        m[n] = -INFINITY, l[n] = 0.0f, nan_groups[n] = 0;
+        m[n] = kLowest, l[n] = 0.0f, nan_groups[n] = 0;
 #pragma unroll
         for (int e = 0; e < kSets; ++e)
 #pragma unroll
@@ -641,7 +645,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
             for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
             if (__any(top > m[n] + 8.0f)) {
               const float to = fmaxf(m[n], row_max(top));
-              const float f = to == -INFINITY ? 1.0f : exp2_fast(m[n] - to);
+              const float f = exp2_fast(m[n] - to);
               m[n] = to;
               l[n] *= f;
 #pragma unroll
@@ -649,10 +653,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc[n][e][j] *= f;
             }
-            const float ref = m[n] == -INFINITY ? 0.0f : m[n];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              x[i] = exp2_fast(x[i] - ref);
+              x[i] = exp2_fast(x[i] - m[n]);
               l[n] += x[i];
             }
             split<PARTS>(x, pr[n]);
@@ -713,7 +716,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
         float top = stat_m[0][n * 16 + c];
 #pragma unroll
         for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][n * 16 + c]);
-        const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
+        const float f = exp2_fast(m[n] - top);
         if (__any(nan_groups[n] != 0)) {
 #pragma unroll
           for (int e = 0; e < kSets; ++e)
@@ -752,7 +755,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
             const float* p = join + (w * 16 + r) * kPitch + seg * 8;
             o0 += *reinterpret_cast<const f32x4*>(p);
             o1 += *reinterpret_cast<const f32x4*>(p + 4);
-            if (rm != -INFINITY) rl += stat_l[w][n * 16 + r] * exp2_fast(stat_m[w][n * 16 + r] - rm);
+            rl += stat_l[w][n * 16 + r] * exp2_fast(stat_m[w][n * 16 + r] - rm);
           }
           if (row >= rows) continue;
           if (!alone) {

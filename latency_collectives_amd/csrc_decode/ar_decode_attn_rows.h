@@ -30,10 +30,6 @@ namespace ard {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// A running maximum that no score has reached yet: finite, so that a masked score less it is minus
-// infinity without a test.
-constexpr float kLowest = -3.0e38f;
-
 // A request as the split sees it: units of tile r (of one head) are below(r + 1) - below(r).
 struct Series {
   int q0, m, kv, tiles;
