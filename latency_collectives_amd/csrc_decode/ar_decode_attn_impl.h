@@ -204,6 +204,11 @@ __device__ __forceinline__ void next_job(const AttnArgs& args, Run& run, Cost& m
   mine.q0 = uniform(mine.q0), mine.m = uniform(mine.m), mine.kv = uniform(mine.kv), mine.span = uniform(mine.span);
 }
 
+// The first position that a row at `pos` sees with a window. Positions below 0 see nothing and count
+// as -1: less a window of nearly 2^31 they would wrap to a positive start, which the tile's other
+// rows would miss their tokens by.
+__device__ __forceinline__ int window_start(int pos, int window) { return max(pos, -1) - window + 1; }
+
 // Memory that a computed address is known to lie in: a load of unknown place counts as one from
 // LDS too, and every wait for LDS would wait for it.
 #define ARD_GLOBAL __attribute__((address_space(1)))
@@ -438,7 +443,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
     const int first_pos = me.kv - me.m;  // position of the request's first new token
     const int end = min(max(first_pos + i1 + 1, 0), kv_end);
     int begin = 0;
-    if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
+    if (a.window > 0) begin = max(window_start(first_pos + i0, a.window), 0) & ~31;
     const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
     const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
     const int taken = min(run.left, me.span - run.at);  // units of the run in this job
@@ -488,7 +493,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
         const int r = min(n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
         const int pos = first_pos + i;
         hi[n] = real ? min(pos + 1, kv_end) : 0;
-        lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+        lo[n] = a.window > 0 ? window_start(pos, a.window) : 0;
         const int64_t at = static_cast<int64_t>(me.q0 + i) * a.q_token +
                            static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head + g * (D / 4);
 #pragma unroll
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
       }
       // Tiles from here on need masks: the first row's end, the last row's window.
       const int whole_end = min(first_pos + i0 + 1, kv_end);
-      const int whole_begin = a.window > 0 ? first_pos + i1 - a.window + 1 : 0;
+      const int whole_begin = a.window > 0 ? window_start(first_pos + i1, a.window) : 0;
 
       f32x4 acc[NQ][kSets][8];
       float m[NQ], l[NQ];

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
     const int first_pos = me.kv - me.m;
     const int end = min(max(first_pos + i1 + 1, 0), kv_end);
     int begin = 0;
-    if (a.window > 0) begin = max(first_pos + i0 - a.window + 1, 0) & ~31;
+    if (a.window > 0) begin = max(window_start(first_pos + i0, a.window), 0) & ~31;
     const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
     const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
     const int taken = min(run.left, span - run.at);
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         const int r = min(wave * RW + n * 16 + c, rows - 1 - row0), i = i0 + token_of(r);
         const int pos = first_pos + i;
         hi[n] = min(pos + 1, kv_end);
-        lo[n] = a.window > 0 ? pos - a.window + 1 : 0;
+        lo[n] = a.window > 0 ? window_start(pos, a.window) : 0;
         const uint16_t* x = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(me.q0 + i) * a.q_token +
                             static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head;
 #pragma unroll
@@ -298,8 +298,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       const int i_first = i0 + token_of(min(wave * RW, rows - 1 - row0));
       const int whole_end = uniform(min(first_pos + i_first + 1, kv_end));
       const int whole_begin =
-          uniform(a.window > 0 ? first_pos + i0 + token_of(min(wave * RW + RW, rows - row0) - 1) - a.window + 1 : 0);
-      const int my_begin = uniform(a.window > 0 ? max(first_pos + i_first - a.window + 1, 0) : 0);
+          uniform(a.window > 0 ? window_start(first_pos + i0 + token_of(min(wave * RW + RW, rows - row0) - 1), a.window) : 0);
+      const int my_begin = uniform(a.window > 0 ? max(window_start(first_pos + i_first, a.window), 0) : 0);
 
       f32x4 acc[NQ][kSets][8];
       float m[NQ], l[NQ];

@@ -1,0 +1,81 @@
+"""ar_kv4_attention with windows in tiles of 128 rows, and windows and lengths at the ends of their
+range with either kind of tiles, against the plain 64-bit form. `large_tiles` repeats the rule by which
+the call picks its tiles, so that a case here says which it reaches."""
+
+import os
+import re
+
+import pytest
+import torch
+
+from tests import decode_ref as R
+from tests.test_gpu_decode_attention import BF, F32, Case
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+MOST = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def lc():
+    import latency_collectives_amd as lc
+
+    return lc
+
+
+def large_tiles(c, window):
+    """Whether the call takes the tiles of 128 rows: choose() of ar_decode_attn.hip."""
+    with open(os.path.join(ROOT, "latency_collectives_amd", "csrc_decode", "ar_decode_attn.hip")) as f:
+        many_tiles, shift = re.search(r"kManyTiles = (\d+), kManyUnits = 1 << (\d+)", f.read()).groups()
+    nreq, tokens = len(c.new), c.q.shape[0]
+    each = -(-tokens * (c.q.shape[1] // c.hkv) // nreq)
+    if c.q.dtype != BF or each <= 128:
+        return False
+    tiles = -(-each // 128) * min(nreq, tokens) * c.hkv
+    room = c.table.shape[1] * c.page
+    units = (min(room, window) if window > 0 else room) // 32 + 1
+    return (tiles >= int(many_tiles) and units >= 16) or tiles * units >= 1 << int(shift)
+
+
+class Wide(Case):
+    """A case whose table has room for `room` tokens a request, its columns past a request's pages out
+    of range."""
+
+    def __init__(self, lc, reqs, hq, hkv, d, page, dtype, room, **kw):
+        super().__init__(lc, reqs, hq, hkv, d, page, dtype, **kw)
+        n, width = self.table.shape
+        wide = torch.full((n, max(width, -(-room // page))), -1, dtype=torch.int32, device="cuda")
+        wide[:, 3::5] = MOST
+        wide[:, :width] = self.table
+        self.table = wide
+
+    def check_rows(self, rows):
+        """These rows of the step's tokens alone: token i of m is what a single new token of a request
+        of length kv - m + i + 1 is."""
+        starts = self.q_start.tolist()
+        who = [max(b for b in range(len(self.new)) if starts[b] <= r and self.new[b] > 0) for r in rows]
+        lens = [self.kv[b] - self.new[b] + r - starts[b] + 1 for r, b in zip(rows, who)]
+        k, v = R.unpack(self.data.cpu(), self.scales.cpu(), self.page)
+        out, lse, bound, lse_bound = R.attention(self.q[rows].cpu(), k, v, self.table[who].cpu(), lens,
+                                                 list(range(len(rows) + 1)), self.page, self.scale, self.window)
+        got, got_lse = self.out[rows].cpu().double(), self.lse[rows].cpu().double()
+        assert torch.equal(torch.isnan(got), torch.isnan(out))
+        assert not ((got - out).abs() > bound).any()
+        assert torch.equal(torch.isneginf(got_lse), torch.isneginf(lse))
+        assert torch.equal(torch.isnan(got_lse), torch.isnan(lse))
+        assert not ((got_lse - lse).abs() > lse_bound)[torch.isfinite(lse)].any()
+        return self
+
+
+@pytest.mark.parametrize("window", [MOST, MOST - 1, MOST - 30, 1 << 30])
+def test_the_largest_windows_beside_rows_below_position_zero(lc, window):
+    """As no window: rows before the first position see nothing, the others of their tile all."""
+    for dtype in (BF, F32):
+        c = Case(lc, [(40, 20), (3, -5), (2, 30), (17, 17)], 6, 2, 128, 16, dtype).call(window=window).check()
+        assert (c.out[:20] == 0).all() and (c.out[20:40] != 0).any()
+        c.done()
+    c = Wide(lc, [(1100, 600), (1100, 1100)], 32, 8, 64, 16, BF, 8192).call(window=window)
+    assert large_tiles(c, window)
+    assert (c.out[:500] == 0).all()
+    c.check_rows([0, 499, 500, 501, 530, 531, 532, 700, 1099, 1100, 1600, 2199]).done()
