@@ -445,6 +445,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention(AttnArgs args
     int begin = 0;
     if (a.window > 0) begin = max(window_start(first_pos + i0, a.window), 0) & ~31;
     const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
+    if (ntiles == 0) begin = 0;  // the window may begin anywhere past the table: no place is computed from there
     const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
     const int taken = min(run.left, me.span - run.at);  // units of the run in this job
     const int t_first = run.at << args.tile_shift;

@@ -176,6 +176,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
     int begin = 0;
     if (a.window > 0) begin = max(window_start(first_pos + i0, a.window), 0) & ~31;
     const int ntiles = end > begin ? (end - begin + 31) >> 5 : 0;
+    // Nothing to see, maybe because the window begins past the table (a length is any 31-bit number):
+    // no place is computed from there.
+    if (ntiles == 0) begin = 0;
     const int nunits = (ntiles + (1 << args.tile_shift) - 1) >> args.tile_shift;
     const int taken = min(run.left, span - run.at);
     const bool ends = run.at + taken == span;  // the last part takes what the series left out

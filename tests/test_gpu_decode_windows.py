@@ -79,3 +79,33 @@ def test_the_largest_windows_beside_rows_below_position_zero(lc, window):
     assert large_tiles(c, window)
     assert (c.out[:500] == 0).all()
     c.check_rows([0, 499, 500, 501, 530, 531, 532, 700, 1099, 1100, 1600, 2199]).done()
+
+
+@pytest.mark.parametrize("kv", [MOST, MOST - 1, MOST - 1700, MOST - 5000, 1 << 24])
+def test_windows_that_begin_past_the_table(lc, kv):
+    """Lengths up to the type's end over a short table: what the windows hold counts as masked."""
+    for dtype in (BF, F32):
+        c = Case(lc, [(1, 40), (3, 77), (20, 90)], 6, 2, 64, 16, dtype)
+        c.kv_len[0] = c.kv_len[2] = c.kv[0] = c.kv[2] = kv
+        c.call(window=33).check()
+        assert (c.out[0] == 0).all() and torch.isneginf(c.lse[4:]).all() and (c.out[1:4] != 0).any()
+        c.done()
+    c = Wide(lc, [(1100, 600), (1100, 1100)], 32, 8, 64, 16, BF, 8192)
+    c.kv_len[0] = c.kv[0] = kv
+    c.call(window=500)
+    assert large_tiles(c, 500)
+    assert (c.out[:1100] == 0).all() and torch.isneginf(c.lse[:1100]).all()
+    c.check_rows([0, 1099, 1100, 1599, 1600, 1601, 1700, 2199]).done()
+
+
+def test_lengths_past_the_table(lc):
+    """The same without a window: a row sees what the table holds."""
+    c = Case(lc, [(1, 40), (20, 90)], 6, 2, 64, 16, BF)
+    c.kv_len[:] = MOST
+    c.kv = [MOST] * 2
+    c.call().check().done()
+    c = Wide(lc, [(1100, 600), (1100, 1100)], 32, 8, 64, 16, BF, 8192)
+    c.kv_len[0] = c.kv[0] = MOST
+    c.call()
+    assert large_tiles(c, 0)
+    c.check_rows([0, 31, 32, 1099, 1100, 1600, 2199]).done()
