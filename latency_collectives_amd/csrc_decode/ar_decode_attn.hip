@@ -19,6 +19,11 @@ namespace {
 // 355 tokens at most 37 and 56. Binary32, three products for one, stays with the small tiles.
 constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
+// Tokens that a row of the table holds, below 2^31 by more than a wave looks ahead.
+int64_t room_of(const ar_kv4* h, const ar_kv4_attention_args* a) {
+  return std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
+}
+
 struct Choice {
   ard::AttnKernel k;
   int rows;  // of a tile
@@ -32,7 +37,7 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
   if (bf16 && each > 128) {
     const int large = 64 * ard::rows_columns(h->head_dim);
     const int64_t tiles = (each + large - 1) / large * std::min(a->nreq, a->ntokens) * h->heads;
-    const int64_t tokens = static_cast<int64_t>(a->table_width) << h->page_shift;
+    const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
     if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
       return {ard::select_attn_rows(h->head_dim), large, true};
@@ -136,11 +141,18 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
     return ar_fail(AR_EINVAL, "q and out: addresses and strides must be multiples of 16 bytes");
   if (a->q_token < 0 || a->q_head < 0 || a->o_token < 0 || a->o_head < 0)
     return ar_fail(AR_EINVAL, "negative stride");
-  if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
-
+  // Rows of a kv head, and a unit of every job beside what its start and end count for, in 31 bits.
+  const int64_t all_rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
+  if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
   const Choice choice = choose(h, a);
   const AttnKernel& k = choice.k;
   if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
+  const int rows_per_tile = choice.rows;
+  const int64_t tiles = all_rows / rows_per_tile + std::min(a->nreq, a->ntokens), jobs = tiles * h->heads;
+  if (tiles * rows_per_tile > 0x7FFFFFFF || jobs * (1 + kJobUnits) > 0x7FFFFFFF)
+    return ar_fail(AR_ETOOBIG, "too many rows");
+  if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
+
   AttnArgs args;
   args.a = *a;
   args.cache = Cache{const_cast<uint8_t*>(a->data), const_cast<uint8_t*>(a->scales), a->num_pages,
@@ -161,25 +173,22 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   args.stats_at = 2u * k.fill * choice.rows * h->head_dim * 4;
   args.arrived = reinterpret_cast<uint32_t*>(args.part + h->work_bytes);
   // As many workgroups as the device holds at once, of at least four units of 32 tokens each: fewer
-  // where the requests cannot have more. Larger units where 32-bit sums of them could overflow.
-  const int rows_per_tile = choice.rows;
-  // (below 2^31 by more than a wave looks ahead)
-  const int64_t room = std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
+  // where the requests cannot have more. Larger units where 32-bit sums of them could overflow: a unit
+  // of 2^31 tokens is the last, which leaves each job the one that the check above counts.
+  const int64_t room = room_of(h, a);
   int64_t seen = room;
   // what a tile's rows see with a window: their tokens and the start's rounding down to 32
   if (a->window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(a->window) + rows_per_tile / args.group + 33);
-  const int64_t tiles = static_cast<int64_t>(a->ntokens) * args.group / rows_per_tile + std::min(a->nreq, a->ntokens);
-  if (tiles * rows_per_tile > 0x7FFFFFFF || tiles * h->heads > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
   args.room = static_cast<int>(room);
   args.most_seen = static_cast<uint32_t>(seen);
   args.unit_shift = 5;
-  const auto span = [&] { return ((seen + (1 << args.unit_shift) - 1) >> args.unit_shift) + kJobUnits; };
-  while (span() * (tiles * h->heads) > 0x7FFFFFFF) ++args.unit_shift;
+  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + kJobUnits; };
+  while (span() * jobs > 0x7FFFFFFF) ++args.unit_shift;
   args.unit = 1u << args.unit_shift;
   args.tile_shift = args.unit_shift - 5;
   args.tile_tokens = (rows_per_tile - 1) / args.group + 1;
   args.job_units = kJobUnits;
-  const int64_t runs = (tiles * h->heads * span() + kAttnWaves - 1) / kAttnWaves;
+  const int64_t runs = (jobs * span() + kAttnWaves - 1) / kAttnWaves;
   int64_t grid = std::min<int64_t>(k.fill, runs);
   if (choice.many) grid = (grid + 7) & ~7;  // the same number for every XCD
   args.runs = static_cast<uint32_t>(grid);
