@@ -1,5 +1,5 @@
-"""ar_kv4_attention with windows in tiles of 128 rows, and windows and lengths at the ends of their
-range with either kind of tiles, against the plain 64-bit form. `large_tiles` repeats the rule by which
+"""ar_kv4_attention with windows in tiles of 128 rows, and windows, lengths and tables at the ends of
+their range with either kind of tiles, against the plain 64-bit form. `large_tiles` repeats the rule by which
 the call picks its tiles, so that a case here says which it reaches."""
 
 import os
@@ -109,3 +109,23 @@ def test_lengths_past_the_table(lc):
     c.call()
     assert large_tiles(c, 0)
     c.check_rows([0, 31, 32, 1099, 1100, 1600, 2199]).done()
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (16, 8), (48, 24)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_tables_so_wide_that_units_grow(lc, hq, hkv, window):
+    """Tables for 2^31 tokens a request: with 33 jobs and more the sums of all requests' units of 32 tokens
+    would pass 31 bits, so they are counted in units of 128 tokens (8 kv heads) or 512 (24)."""
+    reqs = [(1, 5000), (3, 100), (1, 0), (9, 9), (40, 2100), (1, 127), (1, 129), (2, 4097)]
+    for dtype in (BF, F32):
+        c = Wide(lc, reqs, hq, hkv, 64, 1024, dtype, MOST).call(window=window)
+        assert not large_tiles(c, window)
+        c.check_rows([0, 1, 3, 4, 5, 12, 13, 14, 20, 53, 54, 55, 56, 57]).done()
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 2), (24, 12)])
+def test_wide_tables_with_large_tiles(lc, hq, hkv):
+    reqs = [(140, 5000), (90, 100), (1, 0), (200, 200), (333, 2100), (1, 127), (64, 4097)]
+    c = Wide(lc, reqs, hq, hkv, 64, 1024, BF, MOST).call()
+    assert large_tiles(c, 0)
+    c.check_rows([0, 1, 127, 139, 140, 150, 229, 230, 231, 240, 430, 431, 500, 763, 764, 765, 828]).done()
