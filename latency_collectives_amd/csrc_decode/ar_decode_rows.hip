@@ -98,6 +98,14 @@ __device__ __forceinline__ void put_row(const Cache& c, int64_t slot, int head, 
   if ((u & 3) == 0) c.scales[part * (page * (d / 32)) + (u >> 2) * page + off] = static_cast<uint8_t>(byte);
 }
 
+// Between a wave's LDS stores and the loads of them by other lanes, and between those and the next
+// stores. A wave's LDS accesses are done in order; this keeps them in it.
+__device__ __forceinline__ void lds_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Sum over the G lanes of a row, the same in each.
 template <int G>
 __device__ __forceinline__ double row_total(double x) {
@@ -234,12 +242,10 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope(RowArgs r) {
           float* mine = stage + (threadIdx.x / G) * (G * 8);
 #pragma unroll
           for (int j = 0; j < 4; ++j) mine[lo + j] = x[i][j], mine[hi + j] = x[i][4 + j];
-          // the row's lanes are one wave's, whose LDS accesses are in order
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-          __builtin_amdgcn_wave_barrier();
-          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+          lds_turn();  // the row's lanes are one wave's
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[i][j] = mine[8 * u + j];
+          lds_turn();  // the next row goes through the same place
         }
         if (live) put_row(r.cache, slot, head + i, is_v, d, u, x[i]);
       } else if (live) {
