@@ -41,7 +41,10 @@ extern "C" {
  *                         left, its row of the table or the step's ntokens are too short, or a
  *                         length is negative. Its kv_len stays cached_len[b] (at least 0), its
  *                         tokens keep their places (slots and positions -1), its table row stays.
- * Tokens from q_start[nreq] to ntokens are padding: slots and positions -1. pool and the lengths
+ * Tokens from q_start[nreq] to ntokens are padding: slots and positions -1. What the calls below
+ * give for tokens without a position means nothing: ar_kv4_norm_rope_append leaves their rows of
+ * q_out, and ar_kv4_attention attends with those for a refused request, whose tokens q_start still
+ * counts. A caller masks them by their positions. pool and the lengths
  * are read only, so a call can be repeated; pool_out and kv_len must be other buffers. The free
  * list is entries [pool[0], min(pool[1], nfree)). A negative page id gives slots -1.
  */

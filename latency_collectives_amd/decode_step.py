@@ -61,7 +61,7 @@ class DecodeStep:
         self.pool[0][1] = pages
         self.free = torch.randperm(pages, device="cuda", generator=g).int()
         self.table = torch.full((requests, width), -1, dtype=torch.int32, device="cuda")
-        self.refused, self.q_start = i32(requests), i32(requests + 1)
+        self.refused, self.refusals, self.q_start = i32(requests), i32(requests), i32(requests + 1)
         self.slots = torch.zeros(max_tokens, dtype=torch.int64, device="cuda")
         self.positions = i32(max_tokens)
         self.q_out = [torch.empty(max_tokens, self.hq, head_dim, dtype=torch.bfloat16, device="cuda")
@@ -75,13 +75,16 @@ class DecodeStep:
         return self.len[self.turn]
 
     def __call__(self, x, new_len):
-        """x [tokens, hidden] bfloat16, the new tokens of every request one after the other; new_len
-        [requests] int32 on the GPU. Returns every rank's copy of the result."""
+        """x [tokens, hidden] bfloat16, the new tokens of every request one after the other, padding
+        after them; new_len [requests] int32 on the GPU. Returns every rank's copy of the result. Tokens
+        of a request that was refused (`refused`, and `refusals` over all steps) and padding come back
+        as they were."""
         t, now, then = x.shape[0], self.turn, 1 - self.turn
         slots, positions = self.slots[:t], self.positions[:t]
         lc.ar_page_tables(self.len[now], new_len, self.pool[now], self.free, self.table, self.len[then],
                           self.q_start, slots, positions, self.pool[then], self.refused, self.page)
         self.turn = then
+        torch.maximum(self.refusals, self.refused, out=self.refusals)
         xs = [x] * self.ranks
         for layer in range(self.layers):
             partial = []
@@ -99,7 +102,9 @@ class DecodeStep:
             total = [y[:t] for y in self.total]
             lc.ar_allreduce(self.sum, partial, total, t * self.hidden, lc.AR_ALGO_AUTO)
             xs = [a + b for a, b in zip(xs, total)]
-        return xs
+        # Tokens without a position were attended for with what q_out held before.
+        placed = positions[:, None] >= 0
+        return [torch.where(placed, y, x) for y in xs]
 
     def close(self):
         torch.cuda.synchronize()
@@ -136,7 +141,7 @@ def main(argv=None) -> None:
     us = (time.perf_counter() - start) / max(1, a.steps) * 1e6
     if any(not torch.equal(y, xs[0]) for y in xs):
         raise AssertionError("the ranks' results differ")
-    if int(run.refused.sum()) or run.lengths.tolist() != [n + a.steps for n in prompts]:
+    if int(run.refusals.sum()) or run.lengths.tolist() != [n + a.steps for n in prompts]:
         raise AssertionError("a request was refused")
     run.close()
     print(f"{a.ranks} ranks, {a.layers} layers, {a.requests} requests of up to {a.prompt} tokens: "
