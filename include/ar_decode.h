@@ -118,7 +118,8 @@ int ar_qk_norm_rope(const ar_qk_norm_rope_args* a, void* stream);
  * or 256, page_size a power of two, 16..1024. It owns the attention's workspace (35 to 70 MB); the
  * caches themselves are the caller's, one handle serves every layer. As with ar_create, calls on
  * one handle are issued in order on one stream (only ar_kv4_attention uses the workspace).
- * Synchronous. NULL on error. On a machine without a GPU the handle has no workspace: its calls
+ * It belongs to the GPU that is current when it is created, where ar_kv4_attention has to be called;
+ * AR_EINVAL elsewhere. Synchronous. NULL on error. On a machine without a GPU the handle has no workspace: its calls
  * check their arguments and then return AR_EHIP.
  */
 typedef struct ar_kv4 ar_kv4;

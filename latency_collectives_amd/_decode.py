@@ -90,17 +90,23 @@ def __getattr__(name):
 
 
 class _Handle(ctypes.c_void_p):
-    """An ar_kv4 handle with its geometry (kv_heads, head_dim, page_size)."""
+    """An ar_kv4 handle with its geometry (kv_heads, head_dim, page_size) and its GPU (-1: none)."""
 
     geometry = (0, 0, 0)
+    device = -1
 
 
 def ar_kv4_create(kv_heads: int, head_dim: int, page_size: int) -> _Handle:
+    """A handle for caches of one geometry, whose attention runs on the GPU that is current now."""
     p = _bind().ar_kv4_create(int(kv_heads), int(head_dim), int(page_size))
     if not p:
         raise ArError(-1, ar_last_error())
     h = _Handle(p)
     h.geometry = (int(kv_heads), int(head_dim), int(page_size))
+    import torch
+
+    if torch.cuda.is_available():
+        h.device = torch.cuda.current_device()
     return h
 
 

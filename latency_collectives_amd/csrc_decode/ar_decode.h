@@ -56,6 +56,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
 // The handle behind ar_kv4 (ar_decode_attn.hip creates it).
 struct ar_kv4 {
   int heads, head_dim, page_size, page_shift;
+  int device;          // where it was created, -1 without a GPU
   void* work;          // partial results, then arrival counters; NULL without a GPU
   size_t work_bytes;
 };

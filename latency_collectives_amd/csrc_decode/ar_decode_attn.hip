@@ -86,7 +86,7 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
     ar_fail(AR_ENORES, "out of host memory");
     return nullptr;
   }
-  *h = ar_kv4{kv_heads, head_dim, page_size, __builtin_ctz(page_size), nullptr, 0};
+  *h = ar_kv4{kv_heads, head_dim, page_size, __builtin_ctz(page_size), -1, nullptr, 0};
   for (int n = 1; n <= 2; ++n)
     for (const ard::AttnKernel& k : {ard::select_attn_bf16(head_dim, n), ard::select_attn_f32(head_dim, n)})
       h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
@@ -97,7 +97,8 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
     (void)hipGetLastError();
     return h;
   }
-  hipError_t e = hipMalloc(&h->work, h->work_bytes + kArrivedBytes);
+  hipError_t e = hipGetDevice(&h->device);
+  if (e == hipSuccess) e = hipMalloc(&h->work, h->work_bytes + kArrivedBytes);
   if (e == hipSuccess) e = hipMemset(static_cast<uint8_t*>(h->work) + h->work_bytes, 0, kArrivedBytes);
   if (e == hipSuccess) e = hipDeviceSynchronize();
   if (e != hipSuccess) {
@@ -112,8 +113,12 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
 void ar_kv4_destroy(ar_kv4* h) {
   if (h == nullptr) return;
   if (h->work != nullptr) {
+    int current = h->device;
+    (void)hipGetDevice(&current);
+    if (current != h->device) (void)hipSetDevice(h->device);
     (void)hipDeviceSynchronize();
     (void)hipFree(h->work);
+    if (current != h->device) (void)hipSetDevice(current);
   }
   delete h;
 }
@@ -152,6 +157,10 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   if (tiles * rows_per_tile > 0x7FFFFFFF || jobs * (1 + kJobUnits) > 0x7FFFFFFF)
     return ar_fail(AR_ETOOBIG, "too many rows");
   if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
+  int device = -1;
+  AR_HIP(hipGetDevice(&device));
+  if (device != h->device)
+    return ar_fail(AR_EINVAL, "the handle was created on GPU %d, the current one is %d", h->device, device);
 
   AttnArgs args;
   args.a = *a;

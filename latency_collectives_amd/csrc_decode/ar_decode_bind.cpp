@@ -8,19 +8,22 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <optional>
 
 #include "../../include/ar_decode.h"
 
 namespace {
 
 PyObject* g_error = nullptr;  // ArError(code, message)
-PyObject *g_value = nullptr, *g_geometry = nullptr, *g_cuda_stream = nullptr;
+PyObject *g_value = nullptr, *g_geometry = nullptr, *g_device = nullptr, *g_cuda_stream = nullptr;
 
 struct Bad {};  // a Python exception is set
 
@@ -177,17 +180,30 @@ struct Reader {
   }
 };
 
+// The GPU of a call's tensors as the current one, for the launch: a stream belongs to its GPU.
+struct Here {
+  std::optional<c10::DeviceGuard> guard;
+  explicit Here(const Reader& r) {
+    if (r.device >= 0 && r.device != c10::hip::current_device())
+      guard.emplace(c10::Device(c10::DeviceType::CUDA, static_cast<c10::DeviceIndex>(r.device)));
+  }
+};
+
 struct Handle {
   ar_kv4* h;
-  long heads, dim, page;
+  long heads, dim, page, device;
   explicit Handle(PyObject* o) {
     PyObject* v = o == nullptr ? nullptr : PyObject_GetAttr(o, g_value);
     PyObject* g = v == nullptr ? nullptr : PyObject_GetAttr(o, g_geometry);
-    if (g == nullptr) {
+    PyObject* d = g == nullptr ? nullptr : PyObject_GetAttr(o, g_device);
+    if (d == nullptr) {
       Py_XDECREF(v);
+      Py_XDECREF(g);
       PyErr_Clear();
       bad("h", "needs a handle of ar_kv4_create");
     }
+    device = PyLong_AsLong(d);
+    Py_DECREF(d);
     h = v == Py_None ? nullptr : static_cast<ar_kv4*>(PyLong_AsVoidPtr(v));
     long* to[3] = {&heads, &dim, &page};
     for (int i = 0; i < 3; ++i)
@@ -195,6 +211,11 @@ struct Handle {
     Py_DECREF(v);
     Py_DECREF(g);
     if (PyErr_Occurred()) throw Bad();
+  }
+  // After the call's tensors are read.
+  void check_place(const Reader& r) const {
+    if (device >= 0 && r.device >= 0 && r.device != device)
+      bad("h", "made on GPU %ld, the tensors are on GPU %d", device, r.device);
   }
 };
 
@@ -257,6 +278,7 @@ PyObject* page_tables(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     a.refused = r.vec<int32_t>(10, at::kInt, b);
     a.nreq = static_cast<int>(b), a.nfree = static_cast<int>(nfree), a.ntokens = static_cast<int>(t);
     a.page_size = r.small(11, 0);
+    const Here here(r);
     return done(ar_page_tables(&a, r.stream(12)));
   });
 }
@@ -303,6 +325,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
     Reader r{kRope, p};
     ar_qk_norm_rope_args a = {};
     norm_rope(r, a, 0, 1, -1, 2, 3, 4, 6);
+    const Here here(r);
     return done(ar_qk_norm_rope(&a, r.stream(10)));
   });
 }
@@ -320,6 +343,7 @@ PyObject* kv4_norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, P
     norm_rope(r, a, 1, 2, 3, 4, -1, 5, 10);
     a.slots = r.vec<int64_t>(7, at::kLong, a.ntokens);
     cache(r, 8, h, a.data, a.scales, a.num_pages);
+    const Here here(r);
     return done(ar_kv4_norm_rope_append(h.h, &a, r.stream(14)));
   });
 }
@@ -341,6 +365,7 @@ PyObject* rows(const Signature& s, int k, int slots, PyObject* const* args, Py_s
     a.v = r.heads(k + 1, type, t, h.heads, h.dim, a.v_token, a.v_head);
     a.slots = r.vec<int64_t>(slots, at::kLong, t);
     cache(r, slots + 1, h, a.data, a.scales, a.num_pages);
+    const Here here(r);
     return done(CALL(h.h, &a, r.stream(6)));
   });
 }
@@ -378,6 +403,8 @@ PyObject* kv4_attention(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject
     a.q_start = r.vec<int32_t>(6, at::kInt, b + 1);
     a.scale = r.real(9, 1.0 / std::sqrt(static_cast<double>(d)));
     a.window = r.small(10, 0);
+    h.check_place(r);
+    const Here here(r);
     return done(ar_kv4_attention(h.h, &a, r.stream(11)));
   });
 }
@@ -418,7 +445,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_decode_calls", nullptr, -1, kMet
 PyMODINIT_FUNC PyInit__decode_calls() {
   g_value = PyUnicode_InternFromString("value");
   g_geometry = PyUnicode_InternFromString("geometry");
+  g_device = PyUnicode_InternFromString("device");
   g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  if (g_value == nullptr || g_geometry == nullptr || g_cuda_stream == nullptr) return nullptr;
+  if (g_value == nullptr || g_geometry == nullptr || g_device == nullptr || g_cuda_stream == nullptr) return nullptr;
   return PyModule_Create(&kModule);
 }
