@@ -3,8 +3,9 @@
 Every function has the name of the C entry point it wraps and takes torch tensors; sizes, types
 and strides are the tensors' own. The calls are those of the compiled module ``_decode_calls``
 (``csrc_decode/ar_decode_bind.cpp``), loaded with the library on first use: it checks what the C
-entry point cannot see (that tensors are on the GPU, of the right type and shape) and raises
-``ValueError``; a failing call raises :class:`ArError` as in :mod:`latency_collectives_amd._ar`.
+entry point cannot see (that tensors are on the GPU, of the right type and shape, and that no
+gradient is wanted of them) and raises ``ValueError``; a failing call raises :class:`ArError` as in
+:mod:`latency_collectives_amd._ar`.
 Nothing here computes, and there is no fallback.
 
 One step of tensor-parallel decoding on a rank, before its AllReduce::

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -89,6 +90,8 @@ struct Reader {
     return THPVariable_Unpack(o);
   }
   void* address(int j, const at::Tensor& t) {
+    if (t.requires_grad() && at::GradMode::is_enabled())
+      bad(s.name[j], "requires a gradient, which this call does not give (torch.no_grad() allows it)");
     if (!t.is_cuda()) bad(s.name[j], "not on the GPU");
     const int d = t.get_device();
     if (device < 0) device = d;
