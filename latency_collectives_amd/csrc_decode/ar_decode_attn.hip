@@ -133,7 +133,8 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
     return ar_fail(AR_EINVAL, "q_heads must be a multiple of the %d kv heads, got %d", h->heads, a->q_heads);
   if (a->q_heads > 65536) return ar_fail(AR_ETOOBIG, "too many heads");
   if (a->window < 0) return ar_fail(AR_EINVAL, "window must not be negative, got %d", a->window);
-  if (!std::isfinite(a->scale)) return ar_fail(AR_EINVAL, "scale must be finite");
+  const float scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return ar_fail(AR_EINVAL, "scale must be finite in binary32, as its product with log2(e)");
   if (int rc = check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
   if (a->table_stride < a->table_width) return ar_fail(AR_EINVAL, "table_stride is below table_width");
   if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
@@ -170,7 +171,7 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   args.per_group = 1.0f / args.group;
   args.page_bytes = static_cast<int64_t>(h->heads) * h->page_size * h->head_dim;
   args.page_scales = static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32);
-  args.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  args.scale_log2 = scale_log2;
   args.q_sign = 0;
   if (choice.many) {
     if (a->scale < 0) args.q_sign = 0x80008000u;

@@ -24,3 +24,13 @@ def test_more_rows_than_the_split_can_count(D, A, heads, group, nreq, tokens, dt
     assert D._entry.ar_kv4_attention(h, D._ATTENTION.pack(*args), None) == A.AR_ETOOBIG
     assert "rows" in A.ar_last_error()
     D.ar_kv4_destroy(h)
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 1e39, 1e308])
+def test_scales_past_binary32(D, A, scale):
+    """In base-2 units, as the kernels hold it, such a scale would be an infinity, and NaN for a product
+    that is zero."""
+    h = D.ar_kv4_create(2, 128, 16)
+    assert D._entry.ar_kv4_attention(h, D._ATTENTION.pack(*_attn(scale=scale)), None) == A.AR_EINVAL
+    assert "scale" in A.ar_last_error()
+    D.ar_kv4_destroy(h)
