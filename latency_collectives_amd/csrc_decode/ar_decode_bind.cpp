@@ -128,7 +128,8 @@ struct Reader {
     if (size[0] != tokens || size[1] != n || size[2] != dim)
       bad(s.name[j], "needs [%lld, %lld, %lld], got [%lld, %lld, %lld]", (long long)tokens, (long long)n,
           (long long)dim, (long long)size[0], (long long)size[1], (long long)size[2]);
-    token = stride[0], head = stride[1];
+    // a dimension of size one may have any stride
+    token = size[0] == 1 ? 0 : stride[0], head = size[1] == 1 ? 0 : stride[1];
     return a;
   }
   // The sizes of the tensor that sets a call's geometry.

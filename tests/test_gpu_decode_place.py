@@ -45,3 +45,29 @@ def test_calls_go_to_the_gpu_of_their_tensors(lc):
     rc = _decode._entry.ar_kv4_attention(c.h, _decode._ATTENTION.pack(*_attn(hq=4)), None)
     assert rc == lc.AR_EINVAL and "GPU 1" in lc.ar_last_error()
     c.done()
+
+
+def test_strides_of_one_token_or_one_head_do_not_count(lc):
+    """torch lets a dimension of size one have any stride; a slice of a wider buffer keeps its pitch."""
+    d, n = 64, 6 * 64
+    wide = torch.randn(5, n + 3, device="cuda").to(BF)
+    q, k, v = (wide.as_strided((1, h, d), (n + 3, d, 1), at * d) for h, at in ((4, 0), (1, 4), (1, 5)))
+    assert q.stride(0) % 4 == 3
+    plain = [x.contiguous() for x in (q, k, v)]
+    outs = []
+    for a, b, c in ((q, k, v), plain):
+        qo, ko = torch.zeros(1, 4, d, dtype=BF, device="cuda"), torch.zeros(1, 1, d, dtype=BF, device="cuda")
+        lc.ar_qk_norm_rope(a, b, qo, ko, q_weight=torch.ones(d, dtype=BF, device="cuda"))
+        h = lc.ar_kv4_create(1, d, 16)
+        data, scales = lc.ar_kv4_cache(h, 2)
+        lc.ar_kv4_append(h, b, c, torch.tensor([5], device="cuda"), data, scales)
+        # one head a kv head: its stride is not used either
+        one = a.as_strided((1, 1, d), (n + 3, 7, 1))
+        out = torch.zeros(1, 1, d, dtype=BF, device="cuda").as_strided((1, 1, d), (13, 5, 1))
+        table, kv, starts = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0]], [6], [0, 1]))
+        lc.ar_kv4_attention(h, one, data, scales, table, kv, starts, out)
+        outs.append([qo, ko, data, scales, out])
+        torch.cuda.synchronize()
+        lc.ar_kv4_destroy(h)
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
