@@ -129,3 +129,65 @@ def test_wide_tables_with_large_tiles(lc, hq, hkv):
     c = Wide(lc, reqs, hq, hkv, 64, 1024, BF, MOST).call()
     assert large_tiles(c, 0)
     c.check_rows([0, 1, 127, 139, 140, 150, 229, 230, 231, 240, 430, 431, 500, 763, 764, 765, 828]).done()
+
+
+@pytest.mark.parametrize("window", [480, 481, 500, 639, 1000, 1100])
+@pytest.mark.parametrize("kv", [1100, 1101, 1937])
+def test_windows_in_large_tiles(lc, window, kv):
+    """One prompt, from nothing and after a prefix: tiles whose windows begin inside a unit, rows of one
+    wave with different windows, a length of work that grows and then stays."""
+    c = Wide(lc, [(1100, kv)], 64, 8, 64, 16, BF, 2048, seed=window).call(window=window)
+    assert large_tiles(c, window)
+    c.check_rows([0, 1, 15, 16, 31, 32, 33, 470, 479, 480, 481, 500, 512, 600, 777, 1001, 1098, 1099]).done()
+
+
+@pytest.mark.parametrize("d", [96, 128, 192, 256])
+@pytest.mark.parametrize("page", [16, 256])
+def test_windows_in_large_tiles_of_other_heads(lc, d, page):
+    c = Wide(lc, [(700, 900), (5, 5), (900, 900), (1, 800)], 40, 8, d, page, BF, 2048, seed=d).call(window=523)
+    assert large_tiles(c, 523)
+    c.check_rows([0, 7, 320, 323, 324, 699, 700, 704, 705, 706, 1000, 1227, 1228, 1229, 1300, 1604, 1605]).done()
+
+
+@pytest.mark.parametrize("tokens,hq,hkv,window", [(4096, 32, 8, 4096), (8192, 32, 8, 1024), (3001, 32, 16, 777)])
+def test_long_prompts_with_windows(lc, tokens, hq, hkv, window):
+    """A window's work grows over the first tiles and stays for the others, which the split takes for a
+    straight line: what it leaves out goes to a tile's last part. The same bits twice."""
+    c = Wide(lc, [(tokens, tokens)], hq, hkv, 64, 16, BF, 0).call(window=window)
+    assert large_tiles(c, window)
+    first, first_lse = c.out.clone(), c.lse.clone()
+    c.out.fill_(7.0), c.lse.fill_(7.0)
+    c.call(window=window)
+    assert torch.equal(c.out, first) and torch.equal(c.lse, first_lse)
+    some = sorted({0, 1, 63, 64, 500, window - 1, window % tokens, (window + 1) % tokens, 2 * window % tokens,
+                   tokens // 2, tokens - 33, tokens - 1})
+    c.check_rows(some).done()
+
+
+def test_windows_and_nan_in_large_tiles(lc):
+    """NaN keys and values where some rows' windows hold them and others' have passed them."""
+    for which in (0, 1):
+        c = Wide(lc, [(1100, 1300)], 64, 8, 64, 16, BF, 2048)
+        pos = [400, 901]
+        slots = torch.tensor([int(c.table[0, p // 16]) * 16 + p % 16 for p in pos], device="cuda")
+        kv = torch.ones(2, 2, 8, 64, device="cuda")
+        kv[which, 0, :, 5], kv[which, 1, 3, 40] = float("nan"), float("nan")
+        c.lc.ar_kv4_append(c.h, kv[0], kv[1], slots, c.data, c.scales)
+        c.call(window=490)
+        assert large_tiles(c, 490)
+        # row r is at position r + 200; windows that hold 400 begin at rows 200, end at 689
+        c.check_rows([0, 199, 200, 201, 300, 400, 688, 689, 690, 691, 700, 701, 702, 1000, 1099])
+        assert torch.isnan(c.out[200:690, :, :32]).all() and not torch.isnan(c.out[:200]).any()
+        if which == 1:
+            assert not torch.isnan(c.out[:, :24, 32:]).any() and torch.isfinite(c.lse).all()
+            assert torch.isnan(c.out[701:, 24:32, 32:]).all()
+        c.done()
+
+
+@pytest.mark.parametrize("window", [500, 900])
+def test_rows_that_see_nothing_with_windows_in_large_tiles(lc, window):
+    c = Wide(lc, [(700, 150), (600, 0), (300, -7), (500, 1200)], 64, 8, 64, 16, BF, 2048).call(window=window)
+    assert large_tiles(c, window)
+    assert (c.out[:550] == 0).all() and (c.out[700:1600] == 0).all()
+    assert torch.isneginf(c.lse[:550]).all() and torch.isneginf(c.lse[700:1600]).all()
+    c.check_rows([0, 549, 550, 551, 580, 699, 700, 1299, 1300, 1599, 1600, 1601, 1800, 2099]).done()
