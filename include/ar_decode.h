@@ -158,14 +158,13 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * kv_len[b], token i of m at position p = kv_len - m + i,
  *   out[i] = sum_t softmax_t(scale * q[i] . k[t]) v[t]  over 0 <= t <= p, t < kv_len, and with
  * window > 0 also t > p - window. q has q_heads = kv_heads * group heads, head h reads kv head
- * h / group. A row that sees nothing (p < 0) gives zeros and lse = -inf; one with a NaN score (a NaN
- * or infinite query, a visible NaN key) NaN for both. lse [ntokens][q_heads], or NULL, is the
+ * h / group. A row that sees nothing (p < 0), or scores of minus infinity alone, gives zeros and
+ * lse = -inf; one with a score that is NaN or plus infinity NaN for both. lse [ntokens][q_heads], or NULL, is the
  * natural logarithm of the row's sum of exponentials. Statistics and sums are
  * binary32; probabilities are rounded to bfloat16 for AR_BFLOAT16 (their products with the values,
- * which 4 bits hold exactly, are summed in binary32), kept to 24 bits for AR_FLOAT32. Where
- * requests bring more than 128 rows (tokens x group) on average and enough of them, AR_BFLOAT16
- * queries enter their products in two parts: elements down to 2^-6 of the largest of their 32
- * exactly, smaller ones to 2^-13 of it.
+ * which 4 bits hold exactly, are summed in binary32), kept to 24 bits for AR_FLOAT32; queries and
+ * keys enter their products as they are. Which parts a row's sums are joined from depends on the
+ * whole call's lengths, so a request's last bits may change with the others'.
  * Masked places do not reach a result whatever they hold. Page ids outside [0, num_pages) and
  * tokens beyond table_width * page_size count as masked. Tokens that no request covers keep their
  * rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.

@@ -18,7 +18,7 @@ struct AttnArgs {
   int unit_shift, tile_shift;
   int job_units;      // what starting and ending a job costs, in units
   float scale_log2;   // scale * log2(e); its absolute value for the kernel of many rows
-  uint32_t q_sign;    // there: its sign, over two bfloat16
+  uint32_t q_sign;    // there: its sign, on two bfloat16
   int tile_tokens;    // there: tokens that a tile of rows may touch
   uint8_t* part;      // partial sums [slot][row][head_dim], then {max, sum} [slot][row]
   uint32_t part_bytes;

@@ -15,7 +15,10 @@
 // reads a quarter of token c's row, its operand of every step along D. Values: a lane reads eight
 // elements of four tokens at once (the cache's interleaved layout) and pairs tokens with one byte
 // permute per pair. Codes become bfloat16 with one conversion per two elements, the scale applied
-// by the conversion, exactly; no LDS is used before the join.
+// by the conversion, exactly; no LDS is used before the join. Probabilities of bfloat16 calls
+// are rounded to bfloat16 (by 2^-8 at most, under a result that is rounded by as much): results of 8
+// requests of up to 131072 tokens are off by 0.0022 of their norm, by 0.0017 with their own rounding
+// alone. A second part a probability took 129 us for them against 125, and 37 % more for prompt chunks.
 //
 // Work. A job is a tile of query rows (16 * NQ: tokens x heads of the group) of one request and kv
 // head; its tokens are 32-token units. All jobs' units in one row are cut into equal runs, one run a

@@ -3,21 +3,19 @@
 // Mathematics as in ar_decode_attn_impl.h; the products are shared out the other way round: a
 // workgroup's four waves hold 16 * NQ rows each and go through the same tokens together.
 //
-//   S^T = K Q^T   by the scaled 16x16x128 product with K in its 4 bits as stored, the cache's scale
-//                 bytes as the product's own. A query is two e4m3 values, its upper four
-//                 significant bits and what they leave, each with a scale for 32 elements. The
-//                 product adds eight neighbours at a time and drops what lies 2^-13 below the
-//                 largest of them (measured), then sums in binary32. With the largest of 32
-//                 elements in [2^7, 2^8) and upper parts that are multiples of 2^-2, nothing of
-//                 them lies there, and all of a bfloat16 down to 2^-6 of the largest arrives
-//                 exactly; smaller elements are off by less than 2^-13 of it. (Upper parts as
-//                 fine as e4m3 goes lost 2^-11 of the largest product.) Keys need no conversion
-//                 and no LDS.
-//   O^T += V^T P^T  by 16x16x32 products in bfloat16. The scales of V run along the wrong axis
-//                 for the scaled product, so V becomes bfloat16 (exactly), once a workgroup: each
-//                 wave converts a quarter of a round's tokens into LDS in the order of the
-//                 product's operand, for the next round while this one is computed. One barrier a
-//                 round.
+//   S^T = K Q^T   as there: a wave converts its own operands of K in registers, in the shadow of the
+//                 products. (The scaled product takes K in its 4 bits, but a query only as e4m3
+//                 values and drops what lies 2^-13 below the largest of eight products: 634
+//                 against 640 us for two chunks of up to 2048 tokens against 12288, 32 heads, with
+//                 elements below 2^-6 of the largest of their 32 cut.)
+//   O^T += V^T P^T  V becomes bfloat16 (exactly) once a workgroup: each wave converts a quarter of a
+//                 round's tokens into LDS in the order of the product's operand, for the next
+//                 round while this one is computed. One barrier a round. P is one bfloat16 a
+//                 value, as there; two (16 bits) took 874 us for the case above.
+//
+// Two waves share a SIMD. One of them multiplies while the other takes exponentials only if the products
+// go first where both could issue: the scores and the conversions of V have a wave's higher priority
+// (695 -> 640 us for the case above with the second operands read further ahead).
 //
 // Work. As there, equal runs of units for as many workgroups as the device holds; the units of a
 // request's tiles grow with the tile (each sees the tokens before it), so they are summed as an
@@ -27,8 +25,6 @@
 #include "ar_decode_attn_impl.h"
 
 namespace ard {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // A request as the split sees it: units of tile r (of one head) are below(r + 1) - below(r).
 struct Series {
@@ -112,15 +108,12 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run,
   return true;
 }
 
-// A lane's share of a block of scores' keys: rows of 16 tokens, 32 elements each.
+// A lane's share of 16 tokens' keys: a quarter of a row and the scales of the groups of 32 it lies in.
 template <int D>
 struct Keys16 {
-  // groups of 32, three with a fourth that stays empty: both parts of q then meet the same loads
-  static constexpr int NB = D == 96 ? 4 : D / 32;
-  static constexpr int NM = (2 * NB + 3) / 4;    // products: four groups each, of both parts of q
-  static constexpr int NL = NB % 4 == 0 ? NB / 4 : NM;  // different loads for them
-  u32x4 k[NL];
-  uint32_t s[NL];
+  static constexpr int kDw = Tile32<D>::kDw, kKs = Tile32<D>::kKs;
+  uint32_t k[kDw];
+  uint32_t s[kKs];
 };
 
 template <int D, int NQ, int OCC>
@@ -130,7 +123,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   constexpr int SUB = kAttnWaves / kSets;  // units of 32 tokens of a round
   constexpr int TURNS = kSets == 1 ? 2 : 1;  // units in the loop's body: with two, keys stay where they are
   typedef Keys16<D> Keys;
-  constexpr int NB = Keys::NB, NM = Keys::NM, NL = Keys::NL;
+  constexpr int kDw = Keys::kDw, kKs = Keys::kKs;
   __shared__ u32x4 values[2][kAttnWaves][8][64];      // [buffer][unit, set][element][lane]
   __shared__ uint32_t nan_token[2][kAttnWaves][32];   // groups of 32 elements that are NaN
   __shared__ u32x4 any_nan[2];  // a word a wave
@@ -149,14 +142,8 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
   const int page = 1 << shift;
   const int k_bytes = page * (D / 2), s_bytes = page * (D / 32);
   const int num_pages = static_cast<int>(args.cache.num_pages);
-  // This lane's groups of a key for every load, its values for this wave's share of a round.
-  uint32_t k_off[NL], ks_off[NL];
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int kb = min((4 * i + g) % NB, D / 32 - 1);
-    k_off[i] = c * (D / 2) + kb * 16;
-    ks_off[i] = kb * page + c;
-  }
+  const int k_group = (g * kDw) >> 2;  // 32-group of a lane's first K dword
+  const uint32_t k_off = c * (D / 2) + g * (D / 8);
   const int my_set = wave % kSets, my_unit = wave / kSets;
   const int chunk = min(my_set * 16 + c, NC - 1);
   const uint32_t v_off = k_bytes + g * (D * 2) + chunk * 16;
@@ -225,8 +212,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
       // This wave's rows.
       const int mine0 = row0 + wave * RW;
       int hi[NQ], lo[NQ];
-      i32x8 q[NQ][NM];
-      int qs[NQ][NM];
+      bf16x8 q[NQ][kDw];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         // rows past the last repeat it
@@ -235,65 +221,10 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         hi[n] = min(pos + 1, kv_end);
         lo[n] = a.window > 0 ? window_start(pos, a.window) : 0;
         const uint16_t* x = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(me.q0 + i) * a.q_token +
-                            static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head;
+                            static_cast<int64_t>(run.head * group + row0 + r - i * group) * a.q_head + g * (D / 4);
 #pragma unroll
-        for (int mm = 0; mm < NM; ++mm) {
-          int bytes[2];  // scale bytes of the two groups that this lane holds halves of
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // group 4 mm + 2 h + g / 2 of the upper parts' groups, then the lower parts'
-            const int idx = 4 * mm + 2 * h + (g >> 1);
-            const bool low = idx >= NB;
-            const int kb = idx >= NB ? idx - NB : idx;
-            const u32x4* p = reinterpret_cast<const u32x4*>(x + min(kb, D / 32 - 1) * 32 + (g & 1) * 16);
-            const u32x4 v0 = p[0], v1 = p[1];
-            float f[16];
-            uint32_t most = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t word = (j < 4 ? v0[j & 3] : v1[j & 3]) ^ args.q_sign;
-              f[2 * j] = bf16_lo(word), f[2 * j + 1] = bf16_hi(word);
-              most = max(most, max(word << 16 & 0x7FFFFFFFu, word & 0x7FFF0000u));
-            }
-            most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 16)));
-            // in units of the upper scale the largest is in [2^7, 2^8) (e4m3 ends at 448), what
-            // the upper parts leave is at most 2^3: 2^7 of a scale 2^4 smaller
-            const int up = max(static_cast<int>(most >> 23) - 7, 6);
-            const float unit = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);  // 1 / scale
-            const bool wild = most >= 0x7F800000u;  // an infinity or NaN: NaN for the whole row
-            bytes[h] = wild ? 255 : low ? up - 4 : up;
-            if (wild || idx >= 2 * NB || kb >= D / 32) {
-              if (!wild) bytes[h] = 127;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] = 0.0f;
-            }
-            typedef short s16x2 __attribute__((ext_vector_type(2)));
-            typedef float f32x2 __attribute__((ext_vector_type(2)));
-            constexpr float kRound = 1.5f * (1 << 21);  // added and taken away: a multiple of 2^-2
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] *= unit;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float* x4 = f + 4 * j;
-              s16x2 code = {0, 0};
-              code = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(code, (x4[0] + kRound) - kRound, (x4[1] + kRound) - kRound, 1.0f, false);
-              code = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(code, (x4[2] + kRound) - kRound, (x4[3] + kRound) - kRound, 1.0f, true);
-              uint32_t word = __builtin_bit_cast(uint32_t, code);
-              const f32x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, false);
-              const f32x2 b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, true);
-              s16x2 rest = {0, 0};
-              rest = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(rest, x4[0] - b0[0], x4[1] - b0[1], 0.0625f, false);
-              rest = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(rest, x4[2] - b1[0], x4[3] - b1[1], 0.0625f, true);
-              if (low) word = __builtin_bit_cast(uint32_t, rest);
-              q[n][mm][4 * h + j] = static_cast<int>(word);
-            }
-          }
-          // The scale that this lane supplies is group 4 mm + g's: lanes 2 g and 2 g + 1 hold the
-          // first two groups, their second bytes the others.
-          const int from = c + 16 * ((2 * g) & 3);
-          const int b0 = __shfl(bytes[0], from), b1 = __shfl(bytes[1], from);
-          qs[n][mm] = g < 2 ? b0 : b1;
-        }
+        for (int k = 0; k < kDw; ++k)
+          q[n][k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(x + k * 8) ^ args.q_sign);
       }
       const int mine_end = mine0 < rows ? min(max(first_pos + i0 + token_of(min(wave * RW + RW, rows - row0) - 1) + 1, 0), kv_end) : 0;
       const int my_end = uniform(min(mine_end, t_end));
@@ -320,11 +251,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const global_bytes kd = lane_address(k_at, h + u - base), sd = lane_address(s_at, h + u - base);
+          load_dwords<kDw>(kd, k_off, x[u].k);
 #pragma unroll
-          for (int i = 0; i < NL; ++i) {
-            x[u].k[i] = load_at<u32x4>(kd, k_off[i]);
-            x[u].s[i] = load_at<uint8_t>(sd, ks_off[i]);
-          }
+          for (int i = 0; i < kKs; ++i) x[u].s[i] = load_at<uint8_t>(sd, min(k_group + i, D / 32 - 1) * page + c);
         }
       };
       u32x4 v[2];
@@ -394,22 +323,27 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
           const int t0 = t_begin + h * 16;
           if (t0 < my_end && t0 + 32 > my_begin) {
             // Scores.
+            __builtin_amdgcn_s_setprio(1);
             f32x4 s[NQ][2];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+            float sc[2][kKs];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int mm = 0; mm < NM; ++mm) {
-                const u32x4 k = now[u].k[mm % NL];
-                const uint32_t ks = now[u].s[mm % NL];
-                const i32x8 kk = {static_cast<int>(k[0]), static_cast<int>(k[1]), static_cast<int>(k[2]),
-                                  static_cast<int>(k[3]), 0, 0, 0, 0};
-                const int scale = ks > kMaxScale ? 255 : static_cast<int>(ks);
+              for (int i = 0; i < kKs; ++i) sc[u][i] = scale_of(now[u].s[i]);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)  // formats: 4 e2m1, 0 e4m3
-                  s[n][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kk, q[n][mm], s[n][u], 4, 0, 0, scale, 0, qs[n][mm]);
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < kDw; ++i) {
+                float x = sc[u][0];
+                if (kKs > 1) x = ((g * kDw + i) >> 2) == k_group ? sc[u][0] : sc[u][kKs - 1];
+                const uint32_t w = now[u].k[i];
+                const bf16x8 kk = operand(codes<0>(w, x), codes<1>(w, x), codes<2>(w, x), codes<3>(w, x));
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) s[n][u] = mfma(kk, q[n][i], s[n][u]);
               }
+            __builtin_amdgcn_s_setprio(0);
             const int both = static_cast<int>(seen >> (h - base)) & 3;  // the halves that have a page
             if (t0 + 32 > whole_end || t0 < whole_begin || both != 3) {
 #pragma unroll
@@ -423,7 +357,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
                   }
             }
             // The first operands of the second product, under way with the probabilities.
-            constexpr int AHEAD = 4;
+            constexpr int AHEAD = 8;
             bf16x8 vv[AHEAD];
             auto operand_of = [&](int j) {
               return __builtin_bit_cast(bf16x8, values[buf][sub * kSets + (j >> 3)][j & 7][lane]);
@@ -479,7 +413,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
           }
           if (TURNS == 1) keys[0][0] = keys[1][0], keys[0][1] = keys[1][1];
         }
+        __builtin_amdgcn_s_setprio(1);
         if (more) convert(buf ^ 1);
+        __builtin_amdgcn_s_setprio(0);
         buf ^= 1;
         if (h0 + 2 * SUB - base == STEP) {
           base += STEP;
