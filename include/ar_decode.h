@@ -30,7 +30,9 @@ extern "C" {
  * new_len[b]; its tokens live in pages of page_size tokens, table[b * table_stride + j] the page of
  * tokens j * page_size and on. Requests take the pages they lack from the free list in order:
  *   need[b] = ceil((cached + new) / page_size) - ceil(cached / page_size)
- * pages, the entries free_pages[pool[0] + need[0] + .. + need[b-1]] and on. Written are
+ * pages, the entries free_pages[pool[0] + need[0] + .. + need[b-1]] and on, where need is 0 for a
+ * request refused for its lengths, its row or its places, but not for one that finds too few pages:
+ * those after it that need any find too few as well. Written are
  *   table                 the new entries only
  *   kv_len[b]             cached_len[b] + new_len[b]
  *   q_start[0..nreq]      where each request's new tokens start among the step's tokens
@@ -44,9 +46,9 @@ extern "C" {
  * Tokens from q_start[nreq] to ntokens are padding: slots and positions -1. What the calls below
  * give for tokens without a position means nothing: ar_kv4_norm_rope_append leaves their rows of
  * q_out, and ar_kv4_attention attends with those for a refused request, whose tokens q_start still
- * counts. A caller masks them by their positions. pool and the lengths
- * are read only, so a call can be repeated; pool_out and kv_len must be other buffers. The free
- * list is entries [pool[0], min(pool[1], nfree)). A negative page id gives slots -1.
+ * counts. A caller masks them by their positions. pool and the lengths are read only, so a call can
+ * be repeated; pool_out and kv_len must be other buffers. The free list is entries
+ * [pool[0], min(pool[1], nfree)). A negative page id gives slots -1.
  */
 typedef struct {
   const int32_t* cached_len; /* [nreq] */
@@ -75,7 +77,7 @@ int ar_page_tables(const ar_page_tables_args* a, void* stream);
  *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)   over the first `rot` elements
  * with pairs (i, i + rot/2), or (2i, 2i+1) with `interleaved`; cos and sin of pair i are
  * cos_sin[p][i] and cos_sin[p][rot/2 + i] of the token's position p. Computed in 64 bits, rounded
- * once. head_dim a multiple of 8 up to 256, rot a multiple of 8 up to head_dim, 0 for none (then
+ * to binary32 and, for AR_BFLOAT16, from there. head_dim a multiple of 8 up to 256, rot a multiple of 8 up to head_dim, 0 for none (then
  * positions and cos_sin may be NULL). A token of negative position is padding: nothing is written
  * for it. A position at or beyond `rows` gives NaN. q_out may be q and k_out k (in place, equal
  * strides). q_heads or kv_heads may be 0. Addresses and strides are multiples of 4 elements.
@@ -130,8 +132,7 @@ void ar_kv4_destroy(ar_kv4* h);
  * ar_kv4_append: token t's rows k and v to slot slots[t] (page * page_size + offset); a slot
  * outside the cache, as -1, is skipped. Two tokens with one slot leave it undefined.
  * ar_kv4_read: the rows at `slots` as values of `dtype` in k and v (zeros for a slot outside).
- * dtype is that of k and v. Addresses and strides are multiples of 4 elements (8 for ar_kv4_read's
- * outputs and, with AR_BFLOAT16, ar_kv4_append's inputs need 4).
+ * dtype is that of k and v. Addresses and strides are multiples of 4 elements.
  */
 typedef struct {
   void* k;
@@ -166,8 +167,9 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * keys enter their products as they are. Which parts a row's sums are joined from depends on the
  * whole call's lengths, so a request's last bits may change with the others'.
  * Masked places do not reach a result whatever they hold. Page ids outside [0, num_pages) and
- * tokens beyond table_width * page_size count as masked. Tokens that no request covers keep their
- * rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.
+ * tokens beyond table_width * page_size count as masked. table_width is also what the host knows of
+ * the lengths when it chooses between kernels: the width that the step needs serves better than the
+ * buffer's. Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.
  */
 typedef struct {
   const void* q;

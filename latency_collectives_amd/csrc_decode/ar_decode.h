@@ -73,13 +73,12 @@ inline int check_dtype(int dt) {
              ? AR_OK
              : ar_fail(AR_ENOTSUP, "dtype must be AR_FLOAT32 or AR_BFLOAT16, got %d", dt);
 }
-inline int check_cache(const uint8_t* data, const uint8_t* scales, int64_t num_pages, int page_size) {
+inline int check_cache(const uint8_t* data, const uint8_t* scales, int64_t num_pages) {
   if (data == nullptr || scales == nullptr) return ar_fail(AR_EINVAL, "null cache");
   if (!aligned(data, 16) || !aligned(scales, 16))
     return ar_fail(AR_EINVAL, "the cache is not 16-byte aligned");
   if (num_pages < 1 || num_pages > (int64_t(1) << 31) - 1)
     return ar_fail(AR_EINVAL, "num_pages must be in [1, 2^31 - 1], got %lld", (long long)num_pages);
-  (void)page_size;
   return AR_OK;
 }
 

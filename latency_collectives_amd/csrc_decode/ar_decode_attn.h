@@ -37,8 +37,8 @@ struct AttnKernel {
 };
 AttnKernel select_attn_bf16(int head_dim, int columns);
 AttnKernel select_attn_f32(int head_dim, int columns);
-// Many rows a request: tiles of 16 * columns rows for each of a workgroup's waves.
+// Many rows a request: 32 rows for each of a workgroup's waves.
+constexpr int kRowsColumns = 2, kRowsTile = 16 * kRowsColumns * kAttnWaves;
 AttnKernel select_attn_rows(int head_dim);
-int rows_columns(int head_dim);
 
 }  // namespace ard

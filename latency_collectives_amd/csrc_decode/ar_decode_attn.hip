@@ -11,12 +11,15 @@ namespace {
 // The kernel for a call. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose
 // parts join quickly. Tiles of 128 rows, waves on different rows: values are converted once for all
 // of them, but a job is four times as long and so is its join, so they pay where the tiles alone
-// fill the device's 512 places and have some tokens to read, or where the tokens behind them (their
-// bound, the tables' width) are many. Measured, head_dim 128, 4 kv heads of 8 query heads, small
-// tiles against large: 8 requests of 256 rows, 4096 tokens 43 and 67 us; of 1024 rows 106 and 122;
-// of 2048 rows (512 tiles) 206 and 193; of 8192 rows 810 and 540; one of 4096 rows and 16384 tokens
-// (128 tiles) 199 and 183; head_dim 64, 552 tiles of one prompt, 786 tokens 64 and 49; 528 tiles,
-// 355 tokens at most 37 and 56. Binary32, three products for one, stays with the small tiles.
+// fill the device's 512 places and have some tokens to read, or where the tokens behind them are many.
+// Small tiles against large, head_dim 128, 4 kv heads of 8 query heads, 4096 tokens: 8 requests of 512
+// rows 59 and 87 us, of 1024 103 and 112, of 2048 (512 tiles) 190 and 183, of 4096 373 and 307, of 16384
+// 1492 and 915; one of 4096 rows and 16384 tokens 188 and 182, of 8192 rows 349 and 302; head_dim 64, 552
+// tiles of one prompt, 786 tokens 62 and 46. Binary32, three products for one, stays with the small
+// tiles. The tokens that the host knows are the tables' width, and these are times of tables as wide
+// as the longest request. Wider ones move the second rule's border and not the work: with room for
+// 131072 tokens the 8 requests of 512 rows take the large tiles' 87 us, one of 1004 rows and 1711
+// tokens 53 for 29. Tables no wider than the step's longest request avoid it.
 constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
 // Tokens that a row of the table holds, below 2^31 by more than a wave looks ahead.
@@ -35,7 +38,7 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
   if (bf16 && each > 128) {
-    const int large = 64 * ard::rows_columns(h->head_dim);
+    const int large = ard::kRowsTile;
     const int64_t tiles = (each + large - 1) / large * std::min(a->nreq, a->ntokens) * h->heads;
     const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
@@ -91,7 +94,7 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
     for (const ard::AttnKernel& k : {ard::select_attn_bf16(head_dim, n), ard::select_attn_f32(head_dim, n)})
       h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
   h->work_bytes = std::max(h->work_bytes, part_bytes(ard::select_attn_rows(head_dim).fill,
-                                                     64 * ard::rows_columns(head_dim), head_dim));
+                                                     ard::kRowsTile, head_dim));
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -135,7 +138,7 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   if (a->window < 0) return ar_fail(AR_EINVAL, "window must not be negative, got %d", a->window);
   const float scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
   if (!std::isfinite(scale_log2)) return ar_fail(AR_EINVAL, "scale must be finite in binary32, as its product with log2(e)");
-  if (int rc = check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (int rc = check_cache(a->data, a->scales, a->num_pages)) return rc;
   if (a->table_stride < a->table_width) return ar_fail(AR_EINVAL, "table_stride is below table_width");
   if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
   if (a->q == nullptr || a->out == nullptr) return ar_fail(AR_EINVAL, "null q or out");

@@ -4,16 +4,14 @@
 
 namespace ard {
 
-int rows_columns(int) { return 2; }
-
 AttnKernel select_attn_rows(int head_dim) {
-#define ARD_CASE(D, NQ, OCC) \
-  if (head_dim == D) return {kv4_attention_rows<D, NQ, OCC>, 256 * OCC}
-  ARD_CASE(64, 2, 2);
-  ARD_CASE(96, 2, 2);
-  ARD_CASE(128, 2, 2);
-  ARD_CASE(192, 2, 1);
-  ARD_CASE(256, 2, 1);
+#define ARD_CASE(D, OCC) \
+  if (head_dim == D) return {kv4_attention_rows<D, kRowsColumns, OCC>, 256 * OCC}
+  ARD_CASE(64, 2);
+  ARD_CASE(96, 2);
+  ARD_CASE(128, 2);
+  ARD_CASE(192, 1);
+  ARD_CASE(256, 1);
 #undef ARD_CASE
   return {nullptr, 0};
 }

@@ -9,7 +9,7 @@
 //
 // Arithmetic of the norm and the rotation is 64-bit: gfx950's binary64 rate is that of unpacked
 // binary32, the kernel is bound by bytes (or by its launch), and what is rounded to bfloat16 and
-// then to 4 bits no longer depends on the order of the sum of squares.
+// then to 4 bits hardly depends on the order of the sum of squares.
 //
 // Measured, 8191 tokens of 32 + 8 heads of 128 in bfloat16 (172 MB): 38.7 us, 4.4 TB/s; one row a group
 // with a 64-bit division for its place and a library square root and reciprocal was bound by its
@@ -22,9 +22,9 @@
 namespace ard {
 
 constexpr int kRowThreads = 256;
-// Workgroups below which rows are spread over more of them: 1000 tokens of 16 heads take 6.4 us in
-// runs of one to four heads, 8.2 us in runs of eight; 5001 tokens of 16 take 23 us in runs of one
-// and 18.6 us in runs of eight (into the cache and back), 8191 of 40 take 79 us and 42 us.
+// Workgroups below which rows are spread over more of them. In runs of one head and of eight: one token
+// of 9 heads 3.5 and 7.1 us, 1000 tokens of 16 (binary32) 5.2 and 7.0 us; 5001 tokens of 16 into the cache
+// and back 21.0 and 19.1 us, 8191 of 40 67 and 33 us (inputs in the last cache).
 constexpr int kFewBlocks = 512;
 
 // Four elements of either type: as they lie in memory, as binary32, and back.
@@ -55,7 +55,7 @@ struct Elem<DT_BF16> {
   __device__ static Raw* at(const void* base, int64_t i) {
     return reinterpret_cast<Raw*>(static_cast<uint16_t*>(const_cast<void*>(base)) + i);
   }
-  __device__ static float round(double y) {
+  __device__ static float round(double y) {  // by way of binary32: 2^-8 of it and 2^-24
     return bf16_lo(ar::bf16x2_rne(static_cast<float>(y), 0.0f));
   }
 };
@@ -311,7 +311,11 @@ int launch_norm_rope(RowArgs& r, hipStream_t stream) {
   if (r.a.ntokens == 0 || rows == 0) return AR_OK;
   r.per_dim = 1.0 / r.a.head_dim;
   r.run = pick_run(r.a.ntokens, rows, g);
-  // More than the XCDs' L2 hold is not read from there again: 8191 tokens of 40 heads 42 and 38 us.
+  // More than the XCDs' L2 hold (32 MiB) is not read from there again. Through the caches and past them,
+  // 40 heads of 128 in bfloat16, 16, 30, 36 and 80 MiB of outputs: 13.3 and 12.0, 16.7 and 14.6, 20.8
+  // and 18.1, 42.5 and 38.0 us alone; with an elementwise call that reads q after them 18.7 and 18.1,
+  // 27.4 and 27.7, 33.0 and 34.7, 63.2 and 66.0 us. So the threshold is the L2's size, and what a
+  // call gains alone below it, or its reader above, is within 15 % and 5 %.
   // Only where every store is of neighbouring lanes' neighbouring elements: halves of lines that
   // go past the L2 one by one took 29 us for 8000 tokens of 17 interleaved heads of 64 in binary32, 18 us through it.
   const bool pass = !CACHE && !r.a.interleaved && r.a.rot == r.a.head_dim &&
@@ -384,7 +388,7 @@ int check_kv_rows(const ar_kv4* h, const ar_kv4_rows_args* a) {
   if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
   if (int rc = check_dtype(a->dtype)) return rc;
   if (a->ntokens < 0) return ar_fail(AR_EINVAL, "negative size");
-  if (int rc = check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (int rc = check_cache(a->data, a->scales, a->num_pages)) return rc;
   if (a->ntokens == 0) return AR_OK;
   if (a->slots == nullptr) return ar_fail(AR_EINVAL, "null slots");
   if (int rc = check_rows("k", a->k, a->k_token, a->k_head, h->heads, a->dtype)) return rc;
@@ -412,7 +416,7 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
   if (a->kv_heads != h->heads || a->head_dim != h->head_dim)
     return ar_fail(AR_EINVAL, "the handle is for %d kv heads of %d, got %d of %d", h->heads, h->head_dim,
                    a->kv_heads, a->head_dim);
-  if (int rc = ard::check_cache(a->data, a->scales, a->num_pages, h->page_size)) return rc;
+  if (int rc = ard::check_cache(a->data, a->scales, a->num_pages)) return rc;
   if (a->ntokens > 0) {
     if (a->slots == nullptr) return ar_fail(AR_EINVAL, "null slots");
     if (int rc = ard::check_rows("v", a->v, a->v_token, a->v_head, a->kv_heads, a->dtype)) return rc;
