@@ -80,6 +80,8 @@ class DecodeStep:
         of a request that was refused (`refused`, and `refusals` over all steps) and padding come back
         as they were."""
         t, now, then = x.shape[0], self.turn, 1 - self.turn
+        if t > self.slots.numel():
+            raise ValueError(f"a step holds up to {self.slots.numel()} tokens, got {t}")
         slots, positions = self.slots[:t], self.positions[:t]
         lc.ar_page_tables(self.len[now], new_len, self.pool[now], self.free, self.table, self.len[then],
                           self.q_start, slots, positions, self.pool[then], self.refused, self.page)

@@ -41,3 +41,16 @@ def test_tokens_without_a_place_come_back_as_they_were(ranks):
     for y in xs:
         assert torch.isfinite(y.float()).all() and (y != x).any(dim=1).all()
     run.close()
+
+
+def test_a_step_past_the_buffers_changes_nothing():
+    from latency_collectives_amd.decode_step import DecodeStep
+
+    run = DecodeStep(1, 1, 2, 64, 20, q_heads=4, kv_heads=2, head_dim=64, hidden=128, page=16)
+    x = torch.zeros(21, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="20"):
+        run(x, torch.tensor([15, 6], dtype=torch.int32, device="cuda"))
+    assert run.lengths.tolist() == [0, 0] and run.turn == 0
+    run(x[:20], torch.tensor([15, 5], dtype=torch.int32, device="cuda"))
+    assert run.lengths.tolist() == [15, 5]
+    run.close()
