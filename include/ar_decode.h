@@ -169,7 +169,9 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * Masked places do not reach a result whatever they hold. Page ids outside [0, num_pages) and
  * tokens beyond table_width * page_size count as masked. table_width is also what the host knows of
  * the lengths when it chooses between kernels: the width that the step needs serves better than the
- * buffer's. Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.
+ * buffer's. Lengths and starts must not change while a call runs: it stays inside its buffers, but
+ * its results and those of the handle's later calls may be wrong; a new handle is needed then.
+ * Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.
  */
 typedef struct {
   const void* q;

@@ -169,6 +169,7 @@ __device__ __forceinline__ bool find_run(const AttnArgs& args, int w, Run& run, 
   while (__ballot(upto > from) == 0) {
     from -= lane_value(upto, 63);
     b += 64;
+    if (b >= args.a.nreq) return false;  // only if lengths change under the call
     c = cost_of<R>(args, b + lane);
     upto = wave_scan(static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span));
   }

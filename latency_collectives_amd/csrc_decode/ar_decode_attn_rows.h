@@ -55,6 +55,15 @@ __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
   return c;
 }
 
+// The series that lane `l` holds.
+__device__ __forceinline__ Series lane_series(const Series& c, int l) {
+  const uint64_t slope = __builtin_bit_cast(uint64_t, c.half_slope);
+  const uint32_t lo = lane_value(static_cast<uint32_t>(slope), l), hi = lane_value(static_cast<uint32_t>(slope >> 32), l);
+  return {lane_value(c.q0, l), lane_value(c.m, l), lane_value(c.kv, l), lane_value(c.tiles, l),
+          static_cast<uint32_t>(lane_value(c.first, l)),
+          __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo)};
+}
+
 // As find_run, with a job's units in `span`.
 template <int R>
 __device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run, Series& mine, int& span) {
@@ -81,15 +90,15 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run,
   while (__ballot(upto > from) == 0) {
     from -= lane_value(upto, 63);
     b += 64;
+    if (b >= args.a.nreq) return false;  // only if lengths change under the call
     c = series_of<R>(args, b + lane);
     upto = wave_scan(c.below(c.tiles) * heads);
   }
   const int who = __builtin_ctzll(__ballot(upto > from));
   run.request = b + who;
-  const uint32_t before = who > 0 ? lane_value(upto, who - 1) : 0;
-  mine = series_of<R>(args, run.request);
-  mine.tiles = uniform(mine.tiles);
-  from -= before;
+  from -= who > 0 ? lane_value(upto, who - 1) : 0;
+  // What the place was found by, not read again: head and tile stay inside it whatever changes.
+  mine = lane_series(c, who);
   const uint32_t head_units = uniform(mine.below(mine.tiles));
   run.head = uniform(from / head_units);
   from -= run.head * head_units;
