@@ -38,7 +38,7 @@ extern "C" {
  *   q_start[0..nreq]      where each request's new tokens start among the step's tokens
  *   slots[i]              page * page_size + offset of new token i
  *   positions[i]          its position in its request
- *   pool_out[0..1]        pool[0] + pages taken, pool[1]
+ *   pool_out[0..1]        pool[0] (at least 0) + pages taken, pool[1]
  *   refused[b]            0, or 1 for a request that got nothing: the free list has too few pages
  *                         left, its row of the table or the step's ntokens are too short, or a
  *                         length is negative. Its kv_len stays cached_len[b] (at least 0), its
@@ -120,9 +120,9 @@ int ar_qk_norm_rope(const ar_qk_norm_rope_args* a, void* stream);
  * or 256, page_size a power of two, 16..1024. It owns the attention's workspace (35 to 70 MB); the
  * caches themselves are the caller's, one handle serves every layer. As with ar_create, calls on
  * one handle are issued in order on one stream (only ar_kv4_attention uses the workspace).
- * It belongs to the GPU that is current when it is created, where ar_kv4_attention has to be called;
- * AR_EINVAL elsewhere. Synchronous. NULL on error. On a machine without a GPU the handle has no workspace: its calls
- * check their arguments and then return AR_EHIP.
+ * It belongs to the GPU that is current when it is created, where ar_kv4_attention has to be
+ * called; AR_EINVAL elsewhere. Synchronous. NULL on error. On a machine without a GPU the handle has
+ * no workspace: its calls check their arguments and then return AR_EHIP.
  */
 typedef struct ar_kv4 ar_kv4;
 ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size);
@@ -160,8 +160,8 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  *   out[i] = sum_t softmax_t(scale * q[i] . k[t]) v[t]  over 0 <= t <= p, t < kv_len, and with
  * window > 0 also t > p - window. q has q_heads = kv_heads * group heads, head h reads kv head
  * h / group. A row that sees nothing (p < 0), or scores of minus infinity alone, gives zeros and
- * lse = -inf; one with a score that is NaN or plus infinity NaN for both. lse [ntokens][q_heads], or NULL, is the
- * natural logarithm of the row's sum of exponentials. Statistics and sums are
+ * lse = -inf; one with a score that is NaN or plus infinity NaN for both. lse [ntokens][q_heads], or
+ * NULL, is the natural logarithm of the row's sum of exponentials. Statistics and sums are
  * binary32; probabilities are rounded to bfloat16 for AR_BFLOAT16 (their products with the values,
  * which 4 bits hold exactly, are summed in binary32), kept to 24 bits for AR_FLOAT32; queries and
  * keys enter their products as they are. Which parts a row's sums are joined from depends on the
@@ -171,7 +171,8 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * the lengths when it chooses between kernels: the width that the step needs serves better than the
  * buffer's. Lengths and starts must not change while a call runs: it stays inside its buffers, but
  * its results and those of the handle's later calls may be wrong; a new handle is needed then.
- * Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides multiples of 16 bytes.
+ * Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides
+ * multiples of 16 bytes.
  */
 typedef struct {
   const void* q;

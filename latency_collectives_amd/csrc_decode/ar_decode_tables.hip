@@ -66,8 +66,8 @@ __global__ __launch_bounds__(kTableThreads) void page_tables(ar_page_tables_args
   __shared__ uint32_t used_pages;
   const int tid = threadIdx.x, n = a.nreq;
   const uint32_t page = a.page_size, places = a.ntokens;
-  const int32_t pool_first = a.pool[0];
-  const int64_t head = max(pool_first, 0);
+  const int32_t pool_first = max(a.pool[0], 0);
+  const int64_t head = pool_first;
   const uint32_t avail = static_cast<uint32_t>(max<int64_t>(0, min(a.pool[1], a.nfree) - head));
   if (tid == 0) used_pages = 0;
 
