@@ -41,4 +41,18 @@ AttnKernel select_attn_f32(int head_dim, int columns);
 constexpr int kRowsColumns = 2, kRowsTile = 16 * kRowsColumns * kAttnWaves;
 AttnKernel select_attn_rows(int head_dim);
 
+
+// A cache's format as the host sees it: its kernels, and the bytes of a page's heads in data and scales.
+struct AttnFormat {
+  AttnKernel (*bf16)(int head_dim, int columns);
+  AttnKernel (*f32)(int head_dim, int columns);
+  AttnKernel (*rows)(int head_dim);
+  int64_t (*page_bytes)(const ar_kv4* h);
+  int64_t (*page_scales)(const ar_kv4* h);
+};
+// ar_decode_attn.hip: a handle with the workspace of these kernels, NULL on error (`name` is the entry
+// point); a checked call.
+ar_kv4* create_handle(const AttnFormat& f, int kv_heads, int head_dim, int page_size, const char* name);
+int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args* a, void* stream);
+
 }  // namespace ard

@@ -1,4 +1,4 @@
-// Host side of the attention over the 4-bit paged cache: the handle and the launch.
+// Host side of the attention over the paged caches: the handle and the launch, for any format of the cache.
 
 #include <algorithm>
 #include <cmath>
@@ -33,7 +33,7 @@ struct Choice {
   bool many;
 };
 
-Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
+Choice choose(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
@@ -43,15 +43,16 @@ Choice choose(const ar_kv4* h, const ar_kv4_attention_args* a) {
     const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
     if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
-      return {ard::select_attn_rows(h->head_dim), large, true};
+      return {f.rows(h->head_dim), large, true};
   }
   // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
   // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and
-  // 30 us; one of 32 rows, 4096 tokens 11.8 and 15.7). Binary32 gains from it at head_dim 64 only.
+  // 30 us; one of 32 rows, 4096 tokens 11.8 and 15.7), and where there is such an instance: binary32 gains from it at
+  // head_dim 64 only.
   const int64_t tiles = (each + 31) / 32 * std::min(a->nreq, a->ntokens) * h->heads;
-  const int columns = each > 16 && tiles >= kFewTiles && (bf16 || h->head_dim == 64) ? 2 : 1;
-  return {bf16 ? ard::select_attn_bf16(h->head_dim, columns) : ard::select_attn_f32(h->head_dim, columns), 16 * columns,
-          false};
+  const auto select = bf16 ? f.bf16 : f.f32;
+  const int columns = each > 16 && tiles >= kFewTiles && select(h->head_dim, 2).fn != nullptr ? 2 : 1;
+  return {select(h->head_dim, columns), 16 * columns, false};
 }
 
 // Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each
@@ -69,9 +70,9 @@ constexpr int kJobUnits = 12;
 
 }  // namespace
 
-extern "C" {
+namespace ard {
 
-ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
+ar_kv4* create_handle(const AttnFormat& f, int kv_heads, int head_dim, int page_size, const char* name) {
   if (kv_heads < 1 || kv_heads > 1024) {
     ar_fail(AR_EINVAL, "kv_heads must be in [1, 1024], got %d", kv_heads);
     return nullptr;
@@ -91,10 +92,9 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
   }
   *h = ar_kv4{kv_heads, head_dim, page_size, __builtin_ctz(page_size), -1, nullptr, 0};
   for (int n = 1; n <= 2; ++n)
-    for (const ard::AttnKernel& k : {ard::select_attn_bf16(head_dim, n), ard::select_attn_f32(head_dim, n)})
+    for (const AttnKernel& k : {f.bf16(head_dim, n), f.f32(head_dim, n)})
       h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
-  h->work_bytes = std::max(h->work_bytes, part_bytes(ard::select_attn_rows(head_dim).fill,
-                                                     ard::kRowsTile, head_dim));
+  h->work_bytes = std::max(h->work_bytes, part_bytes(f.rows(head_dim).fill, kRowsTile, head_dim));
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -105,7 +105,7 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
   if (e == hipSuccess) e = hipMemset(static_cast<uint8_t*>(h->work) + h->work_bytes, 0, kArrivedBytes);
   if (e == hipSuccess) e = hipDeviceSynchronize();
   if (e != hipSuccess) {
-    ar_fail_hip(e, "the workspace of ar_kv4_create");
+    ar_fail_hip(e, name);
     if (h->work != nullptr) (void)hipFree(h->work);
     delete h;
     return nullptr;
@@ -113,21 +113,7 @@ ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
   return h;
 }
 
-void ar_kv4_destroy(ar_kv4* h) {
-  if (h == nullptr) return;
-  if (h->work != nullptr) {
-    int current = h->device;
-    (void)hipGetDevice(&current);
-    if (current != h->device) (void)hipSetDevice(h->device);
-    (void)hipDeviceSynchronize();
-    (void)hipFree(h->work);
-    if (current != h->device) (void)hipSetDevice(current);
-  }
-  delete h;
-}
-
-int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
-  using namespace ard;
+int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   if (int rc = check_handle(h)) return rc;
   if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
   if (int rc = check_dtype(a->dtype)) return rc;
@@ -153,7 +139,7 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
   // Rows of a kv head, and a unit of every job beside what its start and end count for, in 31 bits.
   const int64_t all_rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  const Choice choice = choose(h, a);
+  const Choice choice = choose(f, h, a);
   const AttnKernel& k = choice.k;
   if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
   const int rows_per_tile = choice.rows;
@@ -172,8 +158,8 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
                      h->heads, h->page_shift};
   args.group = a->q_heads / h->heads;
   args.per_group = 1.0f / args.group;
-  args.page_bytes = static_cast<int64_t>(h->heads) * h->page_size * h->head_dim;
-  args.page_scales = static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32);
+  args.page_bytes = f.page_bytes(h);
+  args.page_scales = f.page_scales(h);
   args.scale_log2 = scale_log2;
   args.q_sign = 0;
   if (choice.many) {
@@ -209,6 +195,36 @@ int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
                      static_cast<hipStream_t>(stream), args);
   AR_HIP(hipGetLastError());
   return AR_OK;
+}
+
+static const AttnFormat kFormat4 = {
+    select_attn_bf16, select_attn_f32, select_attn_rows,
+    [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * h->page_size * h->head_dim; },
+    [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32); }};
+
+}  // namespace ard
+
+extern "C" {
+
+ar_kv4* ar_kv4_create(int kv_heads, int head_dim, int page_size) {
+  return ard::create_handle(ard::kFormat4, kv_heads, head_dim, page_size, "ar_kv4_create");
+}
+
+void ar_kv4_destroy(ar_kv4* h) {
+  if (h == nullptr) return;
+  if (h->work != nullptr) {
+    int current = h->device;
+    (void)hipGetDevice(&current);
+    if (current != h->device) (void)hipSetDevice(h->device);
+    (void)hipDeviceSynchronize();
+    (void)hipFree(h->work);
+    if (current != h->device) (void)hipSetDevice(current);
+  }
+  delete h;
+}
+
+int ar_kv4_attention(ar_kv4* h, const ar_kv4_attention_args* a, void* stream) {
+  return ard::launch_attention(ard::kFormat4, h, a, stream);
 }
 
 }  // extern "C"

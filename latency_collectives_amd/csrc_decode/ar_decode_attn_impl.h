@@ -124,7 +124,7 @@ __device__ __forceinline__ Cost cost_of(const AttnArgs& args, int b) {
     const int at = a.q_start[b], to = a.q_start[b + 1];
     c.kv = max(a.kv_len[b], 0);
     c.q0 = min(max(at, 0), a.ntokens);
-    c.m = max(min(to, a.ntokens) - c.q0, 0);
+    c.m = max(min(to, a.ntokens), c.q0) - c.q0;  // an end may be any number
     c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
     const uint32_t seen = min(static_cast<uint32_t>(c.kv), args.most_seen);
     c.span = static_cast<int>((seen + args.unit - 1) >> args.unit_shift) + args.job_units;
@@ -260,8 +260,8 @@ struct Tile32 {  // a lane's share of 32 tokens, as loaded
 };
 
 // Eight elements of a row of `out` from its sums, and its logarithm.
-template <int DT>
-__device__ __forceinline__ void finish_row(const ar_kv4_attention_args& a, int64_t token, int head, int seg,
+template <int DT, class ARGS>
+__device__ __forceinline__ void finish_row(const ARGS& a, int64_t token, int head, int seg,
                                            f32x4 o0, f32x4 o1, float top, float rl) {
   const float inv = rl == 0.0f ? 0.0f : 1.0f / rl;
   o0 *= inv, o1 *= inv;

@@ -42,7 +42,7 @@ __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
     const int at = a.q_start[b], to = a.q_start[b + 1];
     c.kv = max(a.kv_len[b], 0);
     c.q0 = min(max(at, 0), a.ntokens);
-    c.m = max(min(to, a.ntokens) - c.q0, 0);
+    c.m = max(min(to, a.ntokens), c.q0) - c.q0;  // an end may be any number
     c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
     const int end = min(c.kv, args.room);
     const int low = min(max(c.kv - c.m + min(args.tile_tokens, c.m), 0), end);
@@ -64,9 +64,9 @@ __device__ __forceinline__ Series lane_series(const Series& c, int l) {
           __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo)};
 }
 
-// As find_run, with a job's units in `span`.
-template <int R>
-__device__ __forceinline__ bool find_rows(const AttnArgs& args, int w, Run& run, Series& mine, int& span) {
+// As find_run, with a job's units in `span`; series_of<R>(args, b) gives request b.
+template <int R, class ARGS>
+__device__ __forceinline__ bool find_rows(const ARGS& args, int w, Run& run, Series& mine, int& span) {
   const int lane = threadIdx.x & 63, heads = args.cache.heads;
   uint32_t total = 0, longest = 0;
   Series c;

@@ -1,0 +1,163 @@
+// Host side of the attention over packed prompts: the handle and the launch.
+
+#include "ar_prompt.h"
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+// The handle behind ar_prompt.
+struct ar_prompt {
+  int heads, head_dim;
+  int device;      // where it was created, -1 without a GPU
+  void* work;      // partial results, then arrival counters; NULL without a GPU
+  size_t work_bytes;
+};
+
+namespace ard {
+namespace {
+
+// Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each
+// `rows` rows of head_dim sums and a {max, sum} pair.
+size_t prompt_part_bytes(const PromptKernel& k, int head_dim) {
+  return size_t(2) * k.fill * k.rows * (head_dim + 2) * sizeof(float);
+}
+
+constexpr size_t kPromptArrived = 1024 * sizeof(uint32_t);  // at least every kernel's `fill`
+
+// What starting and ending a job costs, in units of 32 tokens.
+constexpr int kPromptJobUnits = 12;
+
+// Bytes between two tokens' keys or values: a round's 128 tokens stay below 2^31.
+constexpr int64_t kMostStride = int64_t(1) << 23;
+
+}  // namespace
+}  // namespace ard
+
+extern "C" {
+
+ar_prompt* ar_prompt_create(int kv_heads, int head_dim) {
+  using namespace ard;
+  if (kv_heads < 1 || kv_heads > 1024) {
+    ar_fail(AR_EINVAL, "kv_heads must be in [1, 1024], got %d", kv_heads);
+    return nullptr;
+  }
+  const PromptKernel bf16 = select_prompt_bf16(head_dim), f32 = select_prompt_f32(head_dim);
+  if (bf16.fn == nullptr || f32.fn == nullptr) {
+    ar_fail(AR_ENOTSUP, "head_dim must be 64, 96, 128, 192 or 256, got %d", head_dim);
+    return nullptr;
+  }
+  ar_prompt* h = new (std::nothrow) ar_prompt;
+  if (h == nullptr) {
+    ar_fail(AR_ENORES, "out of host memory");
+    return nullptr;
+  }
+  *h = ar_prompt{kv_heads, head_dim, -1, nullptr,
+                 std::max(prompt_part_bytes(bf16, head_dim), prompt_part_bytes(f32, head_dim))};
+  int devices = 0;
+  if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
+    (void)hipGetLastError();
+    return h;
+  }
+  hipError_t e = hipGetDevice(&h->device);
+  if (e == hipSuccess) e = hipMalloc(&h->work, h->work_bytes + kPromptArrived);
+  if (e == hipSuccess) e = hipMemset(static_cast<uint8_t*>(h->work) + h->work_bytes, 0, kPromptArrived);
+  if (e == hipSuccess) e = hipDeviceSynchronize();
+  if (e != hipSuccess) {
+    ar_fail_hip(e, "ar_prompt_create");
+    if (h->work != nullptr) (void)hipFree(h->work);
+    delete h;
+    return nullptr;
+  }
+  return h;
+}
+
+void ar_prompt_destroy(ar_prompt* h) {
+  if (h == nullptr) return;
+  if (h->work != nullptr) {
+    int current = h->device;
+    (void)hipGetDevice(&current);
+    if (current != h->device) (void)hipSetDevice(h->device);
+    (void)hipDeviceSynchronize();
+    (void)hipFree(h->work);
+    if (current != h->device) (void)hipSetDevice(current);
+  }
+  delete h;
+}
+
+int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* stream) {
+  using namespace ard;
+  if (h == nullptr) return ar_fail(AR_EINVAL, "null handle");
+  if (a == nullptr) return ar_fail(AR_EINVAL, "null arguments");
+  if (int rc = check_dtype(a->dtype)) return rc;
+  if (a->ntokens < 0 || a->nreq < 0) return ar_fail(AR_EINVAL, "negative size");
+  if (a->q_heads < 1 || a->q_heads % h->heads != 0)
+    return ar_fail(AR_EINVAL, "q_heads must be a multiple of the %d kv heads, got %d", h->heads, a->q_heads);
+  if (a->q_heads > 65536) return ar_fail(AR_ETOOBIG, "too many heads");
+  if (a->window < 0) return ar_fail(AR_EINVAL, "window must not be negative, got %d", a->window);
+  const float scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return ar_fail(AR_EINVAL, "scale must be finite in binary32, as its product with log2(e)");
+  if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
+  if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr) return ar_fail(AR_EINVAL, "null q, k, v or out");
+  if (a->q_start == nullptr) return ar_fail(AR_EINVAL, "null q_start");
+  const bool bf16 = a->dtype == AR_BFLOAT16;
+  const int64_t unit = bf16 ? 8 : 4, bytes = bf16 ? 2 : 4;
+  for (const void* p : {a->q, a->k, a->v, static_cast<const void*>(a->out)})
+    if (!aligned(p, 16)) return ar_fail(AR_EINVAL, "q, k, v and out: addresses must be multiples of 16 bytes");
+  for (int64_t s : {a->q_token, a->q_head, a->k_token, a->k_head, a->v_token, a->v_head, a->o_token, a->o_head}) {
+    if (s % unit != 0) return ar_fail(AR_EINVAL, "q, k, v and out: strides must be multiples of 16 bytes");
+    if (s < 0) return ar_fail(AR_EINVAL, "negative stride");
+  }
+  if (std::max(a->k_token, a->v_token) > kMostStride / bytes) return ar_fail(AR_ETOOBIG, "a token's keys or values are more than 2^23 bytes apart");
+  const PromptKernel k = bf16 ? select_prompt_bf16(h->head_dim) : select_prompt_f32(h->head_dim);
+  // Rows of a kv head, and a unit of every job beside what its start and end count for, in 31 bits.
+  const int group = a->q_heads / h->heads;
+  const int64_t all_rows = static_cast<int64_t>(a->ntokens) * group;
+  if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  const int64_t tiles = all_rows / k.rows + std::min(a->nreq, a->ntokens), jobs = tiles * h->heads;
+  if (tiles * k.rows > 0x7FFFFFFF || jobs * (1 + kPromptJobUnits) > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
+  int device = -1;
+  AR_HIP(hipGetDevice(&device));
+  if (device != h->device)
+    return ar_fail(AR_EINVAL, "the handle was created on GPU %d, the current one is %d", h->device, device);
+
+  PromptArgs args;
+  args.a = *a;
+  args.cache.heads = h->heads;
+  args.group = group;
+  args.per_group = 1.0f / group;
+  args.scale_log2 = scale_log2;
+  args.q_sign = 0;
+  if (bf16) {
+    if (a->scale < 0) args.q_sign = 0x80008000u;
+    // not zero: a masked score's infinity times it has to stay one
+    args.scale_log2 = std::max(std::fabs(args.scale_log2), 1e-38f);
+  }
+  args.part = static_cast<uint8_t*>(h->work);
+  args.part_bytes = static_cast<uint32_t>(prompt_part_bytes(k, h->head_dim));
+  args.stats_at = 2u * k.fill * k.rows * h->head_dim * 4;
+  args.arrived = reinterpret_cast<uint32_t*>(args.part + h->work_bytes);
+  args.tile_tokens = (k.rows - 1) / group + 1;
+  int64_t seen = a->ntokens;
+  // what a tile's rows see with a window: their tokens and the start's rounding down to 32
+  if (a->window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(a->window) + k.rows / group + 33);
+  args.most_seen = static_cast<uint32_t>(seen);
+  // Larger units where 32-bit sums of them could overflow.
+  args.unit_shift = 5;
+  args.job_units = kPromptJobUnits;
+  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + kPromptJobUnits; };
+  while (span() * jobs > 0x7FFFFFFF) ++args.unit_shift;
+  args.unit = 1u << args.unit_shift;
+  args.tile_shift = args.unit_shift - 5;
+  // As many workgroups as the device holds at once, fewer where there cannot be a round of units for each;
+  // the same number for every XCD.
+  const int64_t runs = (jobs * span() + kAttnWaves - 1) / kAttnWaves;
+  const int64_t grid = (std::min<int64_t>(k.fill, runs) + 7) & ~int64_t(7);
+  args.runs = static_cast<uint32_t>(grid);
+  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, static_cast<hipStream_t>(stream), args);
+  AR_HIP(hipGetLastError());
+  return AR_OK;
+}
+
+}  // extern "C"
