@@ -280,16 +280,23 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_rows(AttnArgs
               split<1>(x, &pr[n]);
             }
             // Values.
+            if (scrub) {
 #pragma unroll
-            for (int j = 0; j < 4 * kSets; ++j) {
-              bf16x8 x = vv[j % AHEAD];
-              if (j + AHEAD < 4 * kSets) vv[j % AHEAD] = operand_of(j + AHEAD);
-              if (scrub) {
-                const u32x4 y = __builtin_bit_cast(u32x4, x);
-                x = operand(finite_only(y[0]), finite_only(y[1]), finite_only(y[2]), finite_only(y[3]));
+              for (int j = 0; j < 4 * kSets; ++j) {
+                const u32x4 y = __builtin_bit_cast(u32x4, operand_of(j));
+                const bf16x8 x = operand(finite_only(y[0]), finite_only(y[1]), finite_only(y[2]), finite_only(y[3]));
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
+                __builtin_amdgcn_sched_barrier(0);
               }
+            } else {
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
+              for (int j = 0; j < 4 * kSets; ++j) {
+                const bf16x8 x = vv[j % AHEAD];
+                if (j + AHEAD < 4 * kSets) vv[j % AHEAD] = operand_of(j + AHEAD);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
+              }
             }
           }
           if (TURNS == 1) {

@@ -2,14 +2,15 @@
 // projection left them.
 //
 // Mathematics, split of the work and joins as in csrc_decode/ar_decode_attn_rows.h: products transposed, a running maximum, a
-// workgroup's four waves on 16 * NQ rows each and on the same tokens. Keys and values come through LDS, a
-// round (SUB units of 32 tokens) ahead, in the order of the products' operands:
+// workgroup's four waves on 16 * NQ rows each and on the same tokens. Keys and values go from memory into LDS without
+// passing through registers, a round (SUB units of 32 tokens) ahead; what lies past a request's end
+// arrives as zero by the buffer's bounds and is masked like any other.
 //
-//   bfloat16   S^T = K Q^T in 16x16x32 products; an operand of K is 16 bytes of a row as they are. O^T += V^T P^T:
-//              a lane loads four elements of eight tokens and pairs tokens with one permute a word.
-//   binary32   in 16x16x4 products, whose operands are single values: K in fours along a row, V as it lies.
-//
-// Keys and values past a request's end read as zero by the buffer's bounds and are masked like any other.
+//   keys       in the order of the product's operands: 1 KB is 16 tokens and 64 bytes of their rows
+//   values     as rows. bfloat16: the operand of the second product is a column of eight tokens, two of the
+//              transposing reads of LDS; pairs of 16-byte pieces change places within a row so that the 16
+//              rows of a read fall into different banks. binary32 (16x16x4 products, whose operands
+//              are single values): in fours along a row.
 #pragma once
 
 #include "../csrc_decode/ar_decode_attn_rows.h"
@@ -67,110 +68,73 @@ __device__ __forceinline__ ar::rsrc_t rows_from(const uint8_t* base, int64_t row
                        static_cast<uint32_t>(uniform(static_cast<int>(min(bytes, int64_t(0x7FFFFFFF))))));
 }
 
-// A round of tokens on its way into LDS: what each of four waves loads of it, and where it goes.
+// 64 lanes' 16 bytes each, at voffset + soffset of the buffer, into LDS at `to` and on, in the lanes' order. The
+// compiler does not count them: wait_vm before the barrier that hands them over. (An SGPR that a vector
+// instruction wrote has to be five wait states old, M0 one.)
+__device__ __forceinline__ void into_lds(uint32_t to, ar::rsrc_t from, uint32_t voffset, uint32_t soffset) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(to), "v"(voffset), "s"(from), "s"(soffset)
+               : "memory", "m0");
+}
+#define ARD_LDS __attribute__((address_space(3)))
+template <class T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *reinterpret_cast<const ARD_LDS T*>(at);
+}
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// Of 16 lanes that address a row's four elements each, four lanes a row: lane c gets column c of the four rows.
+__device__ __forceinline__ u32x2 lds_columns(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<ARD_LDS s16x4*>(at)));
+}
+
+// A round of tokens in LDS: keys, then values, BYTES each.
 template <int DT, int D, int SUB>
-struct Stage;
+struct Round {
+  static constexpr bool kBf16 = DT == DT_BF16;
+  static constexpr int ES = kBf16 ? 2 : 4;
+  static constexpr int BYTES = SUB * 32 * D * ES;
+  static constexpr int kSteps = D * ES / 64;                 // KB of 16 tokens' keys
+  static constexpr int kItems = BYTES / 1024 / kAttnWaves;   // KB that a wave moves, of either
+  static constexpr int kPieces = D * ES / 16;                // of a row
+  static_assert(BYTES % (1024 * kAttnWaves) == 0 && kItems * kAttnWaves == SUB * 2 * kSteps);
 
-template <int D, int SUB>
-struct Stage<DT_BF16, D, SUB> {
-  static constexpr int kSteps = D / 32, kSets = (D + 63) / 64;
-  static constexpr int kHalves = SUB * 2 / kAttnWaves;                       // 16 tokens of keys, of a wave
-  static constexpr int kItems = (SUB * kSets + kAttnWaves - 1) / kAttnWaves;  // (unit, set) of values, of a wave
-  static_assert(SUB * 2 % kAttnWaves == 0);
-  struct Lds {
-    u32x4 keys[SUB * 2][kSteps][64];
-    u32x4 values[SUB][kSets][4][64];
-  };
-  u32x4 k[kHalves][kSteps];
-  u32x2 v[kItems][8];
+  // Where piece pair `p` (32 bytes, 16 columns) of a bfloat16 row stands: eight rows' 32 bytes fall into
+  // different banks (256 bytes) whatever p is. `back`: the other way round.
+  __device__ static int place(int p, int row, bool back) {
+    if (!kBf16) return p;
+    constexpr int P = kPieces / 2;
+    if (P == 6) {
+      const int by = row >> 2 & 1;
+      return back ? (p + (by ? 5 : 0)) % 6 : (p + by) % 6;
+    }
+    return p ^ (P % 8 == 0 ? row & 7 : row >> 1 & 3);  // rows of 128 and 384 bytes: two of a bank's turn
+  }
 
-  __device__ void load(ar::rsrc_t kr, ar::rsrc_t vr, uint32_t k_row, uint32_t v_row, int wave, int c, int g) {
+  uint32_t key_off, value_off[kItems];  // of a lane, in the round's buffers
+  __device__ void setup(uint32_t k_row, uint32_t v_row, int wave, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+    key_off = (first_half(wave) * 16 + c) * k_row + g * 16;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int at = (wave * kItems + i) * 64 + lane, row = at / kPieces, piece = at - row * kPieces;
+      value_off[i] = row * v_row + (place(piece >> 1, row, true) * 2 + (piece & 1)) * 16;
+    }
+  }
+  // A wave's keys: whole halves where there are four or more, else half of one's steps.
+  static constexpr int kHalves = SUB * 2 >= kAttnWaves ? SUB * 2 / kAttnWaves : 1;
+  static constexpr int kMySteps = kItems / kHalves;
+  __device__ static int first_half(int wave) { return SUB * 2 >= kAttnWaves ? wave * kHalves : wave % (SUB * 2); }
+  __device__ static int first_step(int wave) { return SUB * 2 >= kAttnWaves ? 0 : wave / (SUB * 2) * kMySteps; }
+  __device__ void load(uint32_t lds, ar::rsrc_t kr, ar::rsrc_t vr, uint32_t k_row, int wave) const {
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        k[h][s] = ar::ld16<ar::kPlain>(kr, ((wave * kHalves + h) * 16 + c) * k_row + s * 64 + g * 16);
+      for (int s = 0; s < kMySteps; ++s)
+        into_lds(lds + ((first_half(wave) + h) * kSteps + first_step(wave) + s) * 1024, kr, key_off,
+                 h * 16 * k_row + (first_step(wave) + s) * 64);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int item = min(wave * kItems + i, SUB * kSets - 1), unit = item / kSets, set = item - unit * kSets;
-#pragma unroll
-      for (int t = 0; t < 8; ++t)  // lanes beyond the row repeat its last elements
-        v[i][t] = ar::ld8<ar::kPlain>(vr, (unit * 32 + (t >> 2) * 16 + g * 4 + (t & 3)) * v_row + min(set * 64 + c * 4, D - 4) * 2);
-    }
-  }
-  __device__ bool odd() const {  // a value that is not finite
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-      for (int t = 0; t < 8; ++t) bad |= finite_only(v[i][t].x) != v[i][t].x || finite_only(v[i][t].y) != v[i][t].y;
-    return bad;
-  }
-  __device__ void store(Lds& to, int wave, int lane) const {
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) to.keys[wave * kHalves + h][s][lane] = k[h][s];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int item = wave * kItems + i;
-      if (item >= SUB * kSets) break;
-      const int unit = item / kSets, set = item - unit * kSets;
-      const u32x2* x = v[i];
-      to.values[unit][set][0][lane] = u32x4{pair_lo(x[0].x, x[1].x), pair_lo(x[2].x, x[3].x), pair_lo(x[4].x, x[5].x), pair_lo(x[6].x, x[7].x)};
-      to.values[unit][set][1][lane] = u32x4{pair_hi(x[0].x, x[1].x), pair_hi(x[2].x, x[3].x), pair_hi(x[4].x, x[5].x), pair_hi(x[6].x, x[7].x)};
-      to.values[unit][set][2][lane] = u32x4{pair_lo(x[0].y, x[1].y), pair_lo(x[2].y, x[3].y), pair_lo(x[4].y, x[5].y), pair_lo(x[6].y, x[7].y)};
-      to.values[unit][set][3][lane] = u32x4{pair_hi(x[0].y, x[1].y), pair_hi(x[2].y, x[3].y), pair_hi(x[4].y, x[5].y), pair_hi(x[6].y, x[7].y)};
-    }
-  }
-};
-
-template <int D, int SUB>
-struct Stage<DT_F32, D, SUB> {
-  static constexpr int kSteps = D / 16, kSets = (D + 63) / 64;  // a step: four products along a row
-  static constexpr int kKeys = SUB * 2 * kSteps / kAttnWaves;   // (half, step) of a wave
-  static constexpr int kRows = SUB * 32 / kAttnWaves;           // tokens of values, of a wave
-  static constexpr int kItems = kRows * D / 256;                // 64 lanes, four elements each
-  static_assert(SUB * 2 * kSteps % kAttnWaves == 0 && kRows * D % 256 == 0);
-  struct Lds {
-    f32x4 keys[SUB * 2][kSteps][64];
-    f32x4 values[SUB * 32][D / 4];
-  };
-  f32x4 k[kKeys];
-  f32x4 v[kItems];
-
-  __device__ void load(ar::rsrc_t kr, ar::rsrc_t vr, uint32_t k_row, uint32_t v_row, int wave, int c, int g) {
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int x = wave * kKeys + i, half = x / kSteps, s = x - half * kSteps;
-      k[i] = __builtin_bit_cast(f32x4, ar::ld16<ar::kPlain>(kr, (half * 16 + c) * k_row + s * 64 + g * 16));
-    }
-    const int lane = g * 16 + c;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int x = i * 64 + lane, row = x / (D / 4);
-      v[i] = __builtin_bit_cast(f32x4, ar::ld16<ar::kPlain>(vr, (wave * kRows + row) * v_row + (x - row * (D / 4)) * 16));
-    }
-  }
-  __device__ bool odd() const {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= !(fabsf(v[i][j]) < INFINITY);
-    return bad;
-  }
-  __device__ void store(Lds& to, int wave, int lane) const {
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int x = wave * kKeys + i, half = x / kSteps, s = x - half * kSteps;
-      to.keys[half][s][lane] = k[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int x = i * 64 + lane, row = x / (D / 4);
-      to.values[wave * kRows + row][x - row * (D / 4)] = v[i];
-    }
+    for (int i = 0; i < kItems; ++i) into_lds(lds + BYTES + (wave * kItems + i) * 1024, vr, value_off[i], 0);
   }
 };
 
@@ -181,10 +145,14 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
   constexpr int RW = 16 * NQ, R = RW * kAttnWaves;
   constexpr bool kBf16 = DT == DT_BF16;
   constexpr int ES = kBf16 ? 2 : 4;
-  typedef Stage<DT, D, SUB> Round;
-  constexpr int kSteps = Round::kSteps, kSets = Round::kSets;
+  typedef Round<DT, D, SUB> Stage;
+  constexpr int kSteps = Stage::kSteps, kSets = (D + 63) / 64;
+  // bfloat16: tile t has elements 16 t + 4 g + i of row c in [i]; binary32: 64 (t / 4) + 16 g + 4 i + t % 4.
+  constexpr int kTiles = kBf16 ? D / 16 : 4 * kSets;
   typedef typename std::conditional<kBf16, bf16x8, f32x4>::type Q;  // a lane's elements of a step
-  __shared__ typename Round::Lds tokens[2];
+  constexpr bool kAhead = kBf16 && D <= 192;  // the next unit's keys are read behind this one's scores
+  constexpr int kValuesAhead = kBf16 ? (D <= 128 ? D / 16 : 4) : 0;  // values read behind them
+  __shared__ __attribute__((aligned(1024))) uint8_t tokens[2][2 * Stage::BYTES];
   __shared__ u32x4 any_odd[2];  // a word a wave
   __shared__ int last;
 
@@ -199,6 +167,18 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
   const int c = lane & 15, g = lane >> 4;
   const int group = args.group;
   const int64_t k_row = a.k_token * ES, v_row = a.v_token * ES;
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((ARD_LDS uint8_t*)&tokens[0][0]));
+  Stage stage;
+  stage.setup(static_cast<uint32_t>(k_row), static_cast<uint32_t>(v_row), wave, lane);
+  // A lane's places in a round's LDS.
+  uint32_t key_at = lds + lane * 16;
+  uint32_t value_at[kBf16 ? kTiles : 1];
+#pragma unroll
+  for (int t = 0; t < (kBf16 ? kTiles : 1); ++t) {
+    const int row = g * 4 + (kBf16 ? c >> 2 : 0);
+    value_at[t] = lds + Stage::BYTES + row * (D * ES) + (kBf16 ? Stage::place(t, row, false) * 32 + (c & 3) * 8 : 0);
+  }
+  int turn = 2 * Stage::BYTES;  // from one round's LDS to the other's
   const ar::rsrc_t part = ar::make_rsrc(args.part, args.part_bytes);
 
   for (;;) {
@@ -231,20 +211,16 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
       const uint8_t* keys = static_cast<const uint8_t*>(a.k) + me.q0 * k_row + run.head * a.k_head * ES;
       const uint8_t* vals = static_cast<const uint8_t*>(a.v) + me.q0 * v_row + run.head * a.v_head * ES;
       const int t_begin = begin + t_first * 32, t_end = min(begin + t_last * 32, end);
-      Round next;
-      auto load = [&](int t) {
-        next.load(rows_from(keys, k_row, t, end, D * ES), rows_from(vals, v_row, t, end, D * ES),
-                  static_cast<uint32_t>(k_row), static_cast<uint32_t>(v_row), wave, c, g);
+      auto load = [&](uint32_t to, int t) {
+        stage.load(to, rows_from(keys, k_row, t, end, D * ES), rows_from(vals, v_row, t, end, D * ES),
+                   static_cast<uint32_t>(k_row), wave);
       };
+      // LDS of the round that is read next (key_at's), and its turn among any_odd's.
+      const auto now_at = [&] { return uniform(static_cast<int>(key_at - lane * 16)); };
+      const auto now = [&] { return turn < 0; };
       // Rounds that some row sees in part: from the first row's end on, and up to the last one's window.
       const int odd_begin = a.window > 0 ? window_start(i1, a.window) : 0;
-      auto store = [&](int buf, int t) {
-        next.store(tokens[buf], wave, lane);
-        bool some = false;
-        if (t + SUB * 32 > i0 + 1 || t < odd_begin) some = __any(next.odd());
-        if (lane == 0) reinterpret_cast<uint32_t*>(&any_odd[buf])[wave] = some;
-      };
-      if (t_begin < t_end) load(t_begin);
+      if (t_begin < t_end) load(now_at(), t_begin);
 
       // This wave's rows.
       const int mine0 = row0 + wave * RW;
@@ -275,121 +251,137 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
       const int whole_begin = uniform(a.window > 0 ? window_start(i_last, a.window) : 0);
       const int my_begin = uniform(a.window > 0 ? max(window_start(i_first, a.window), 0) : 0);
 
-      f32x4 acc[NQ][kSets][4];  // [i]: element 64 e + 16 g + 4 i + j of row c
+      f32x4 acc[NQ][kTiles];
       float m[NQ], l[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         m[n] = kLowest, l[n] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kSets; ++e)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[n][e][j] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < kTiles; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
       }
 
-      int buf = 0;
-      if (t_begin < t_end) store(0, t_begin);
-      __syncthreads();
       for (int tr = t_begin; tr < t_end; tr += SUB * 32) {
+        ar::wait_vm<0>();
+        __syncthreads();  // the round has arrived, and the one before has been read
         const bool more = tr + SUB * 32 < t_end;
-        const u32x4 some_odd = any_odd[buf];
-        const bool round_odd = uniform(some_odd[0] | some_odd[1] | some_odd[2] | some_odd[3]) != 0;
-        if (more) load(tr + SUB * 32);
+        auto keys_of = [&](int sub, int x) { return __builtin_bit_cast(Q, lds_at<u32x4>(key_at + (sub * 2 * kSteps + x) * 1024)); };
+        Q kk[kAhead ? 2 * kSteps : 1];
+        if (kAhead)
+#pragma unroll
+          for (int x = 0; x < 2 * kSteps; ++x) kk[x] = keys_of(0, x);
+        if (more) load(now_at() + turn, tr + SUB * 32);
+        if (tr + SUB * 32 > i0 + 1 || tr < odd_begin) {
+          // Infinities and NaN that not all rows see: taken out of the round, and added for the rows that do.
+          uint32_t* const mine = reinterpret_cast<uint32_t*>(tokens[now()] + Stage::BYTES) + tid * 4;
+          bool some = false;
+          for (int x = 0; x < Stage::BYTES / 16; x += kAttnThreads) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + x * 4);
+            u32x4 y = v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kBf16) y[i] = finite_only(v[i]);
+              else y[i] = (v[i] & 0x7F800000u) == 0x7F800000u ? 0 : v[i];
+            }
+            if (y[0] != v[0] || y[1] != v[1] || y[2] != v[2] || y[3] != v[3]) {
+              some = true;
+              *reinterpret_cast<u32x4*>(mine + x * 4) = y;
+            }
+          }
+          some = __any(some);
+          if (lane == 0) reinterpret_cast<uint32_t*>(&any_odd[now()])[wave] = some;
+          __syncthreads();
+          const u32x4 odd = any_odd[now()];
+          if (uniform(odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
+            const int upto = min(tr + SUB * 32, t_end);
 #pragma unroll 1
-        for (int sub = 0; sub < SUB; ++sub) {
-          const int t0 = tr + sub * 32;
-          if (t0 >= my_end || t0 + 32 <= my_begin) continue;
-          const bool masked = t0 + 32 > whole_end || t0 < whole_begin;
-          auto sees = [&](int n, int u, int i) {
-            const int t = t0 + u * 16 + g * 4 + i;
-            return t < hi[n] && t >= lo[n];
-          };
-          auto values_of = [&](int j) {  // bfloat16: the operand of elements 64 (j / 4) + 4 c + j % 4
-            if constexpr (kBf16) return tokens[buf].values[sub][j >> 2][j & 3][lane];
-            else return u32x4{};
-          };
-          auto value4 = [&](int u, int i, int e) {  // binary32: four elements of token 4 g + i of half u
-            if constexpr (kBf16) return f32x4{};
-            else return tokens[buf].values[sub * 32 + u * 16 + g * 4 + i][min(e * 16 + c, D / 4 - 1)];
-          };
-          const bool scrub = masked && round_odd;  // infinities and NaN of tokens that only some rows see
-          if (scrub) {
+            for (int t = tr; t < upto; ++t) {
+              const uint8_t* row = vals + t * v_row;
+              int part_of = g;
+              asm("" : "+v"(part_of));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              const bf16x8 visible = visible_of([&](int u, int i) { return sees(n, u, i); });
-              if constexpr (kBf16) {
+              for (int x = 0; x < kTiles; ++x) {
+                if (!kBf16 && (x & 3) != 0) continue;
+                float v[16];
+                constexpr int N = kBf16 ? 4 : 16;
+                const int from = 16 * x + N * part_of;
+                if (from >= D) continue;
 #pragma unroll
-                for (int j = 0; j < 4 * kSets; ++j) {
-                  add_infinite(values_of(j), visible, acc[n][j >> 2][j & 3]);
-                  __builtin_amdgcn_sched_barrier(0);
-                }
-              } else {
+                for (int i = 0; i < N; i += 4) {
+                  if constexpr (kBf16) {
+                    const u32x2 z = *reinterpret_cast<const u32x2*>(row + from * 2);
+                    v[0] = bf16_lo(z.x), v[1] = bf16_hi(z.x), v[2] = bf16_lo(z.y), v[3] = bf16_hi(z.y);
+                  } else {
+                    const f32x4 z = *reinterpret_cast<const f32x4*>(row + (from + i) * 4);
 #pragma unroll
-                for (int e = 0; e < kSets; ++e) {
-                  f32x4 up[4], down[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) up[j] = down[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                  for (int x = 0; x < 8; ++x) {
-                    const f32x4 y = value4(x >> 2, x & 3, e);
-                    const float one = sees(n, x >> 2, x & 3) ? 1.0f : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                      up[j] = mfma1(y[j] <= 3.4028235e38f ? 0.0f : 1.0f, one, up[j]);
-                      down[j] = mfma1(y[j] >= -3.4028235e38f ? 0.0f : 1.0f, one, down[j]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int j = 0; j < 4; ++j) v[i + j] = z[j];
                   }
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      if (up[j][i] > 0.0f) acc[n][e][j][i] += INFINITY;
-                      if (down[j][i] > 0.0f) acc[n][e][j][i] -= INFINITY;
-                    }
                 }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                  for (int i = 0; i < N; ++i)
+                    if (!(fabsf(v[i]) < INFINITY) && t < hi[n] && t >= lo[n])
+                      acc[n][kBf16 ? x : x + (i & 3)][kBf16 ? i : i >> 2] += v[i];
               }
             }
           }
-          // Scores.
-          __builtin_amdgcn_s_setprio(1);
+        }
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+          const int t0 = tr + sub * 32;
+          const bool mine = t0 < my_end && t0 + 32 > my_begin;
           f32x4 s[NQ][2];
+          u32x4 vv[kBf16 ? kTiles : 1];
+          auto values_of = [&](int t) {
+            const uint32_t at = value_at[kBf16 ? t : 0] + sub * (32 * D * ES);
+            const u32x2 x = lds_columns(at), y = lds_columns(at + 16 * D * ES);
+            return u32x4{x.x, x.y, y.x, y.y};
+          };
+          if (mine) {
+            // Scores.
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+            for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              const auto kk = __builtin_bit_cast(Q, tokens[buf].keys[sub * 2 + u][i][lane]);
+              for (int i = 0; i < kSteps; ++i) {
+                const Q k1 = kAhead ? kk[u * kSteps + i] : keys_of(sub, u * kSteps + i);
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) {
-                if constexpr (kBf16) {
-                  s[n][u] = mfma(kk, q[n][i], s[n][u]);
-                } else {
+                for (int n = 0; n < NQ; ++n) {
+                  if constexpr (kBf16) {
+                    s[n][u] = mfma(k1, q[n][i], s[n][u]);
+                  } else {
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) s[n][u] = mfma1(kk[j], q[n][i][j], s[n][u]);
+                    for (int j = 0; j < 4; ++j) s[n][u] = mfma1(k1[j], q[n][i][j], s[n][u]);
+                  }
                 }
               }
+            __builtin_amdgcn_s_setprio(0);
+            // The operands of the second product, under way with the probabilities.
+            if constexpr (kBf16) {
+#pragma unroll
+              for (int t = 0; t < kValuesAhead; ++t) vv[t] = values_of(t);
             }
-          __builtin_amdgcn_s_setprio(0);
+          }
+          if (kAhead && sub + 1 < SUB)
+#pragma unroll
+            for (int x = 0; x < 2 * kSteps; ++x) kk[x] = keys_of(sub + 1, x);
+          if (!mine) continue;
+          __builtin_amdgcn_sched_barrier(0);
           if (!kBf16)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
-          if (masked) {
+          if (t0 + 32 > whole_end || t0 < whole_begin) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!sees(n, u, i)) s[n][u][i] = -INFINITY;
-          }
-          // The first operands of the second product, under way with the probabilities.
-          constexpr int AHEAD = 4;
-          u32x4 vv[AHEAD];
-          if constexpr (kBf16) {
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) vv[j] = values_of(j);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 4; ++i) {
+                  const int t = t0 + u * 16 + g * 4 + i;
+                  if (t >= hi[n] || t < lo[n]) s[n][u][i] = -INFINITY;
+                }
           }
           // Probabilities.
           bf16x8 pr[NQ];
@@ -405,9 +397,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
               m[n] = to;
               l[n] *= f;
 #pragma unroll
-              for (int e = 0; e < kSets; ++e)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[n][e][j] *= f;
+              for (int t = 0; t < kTiles; ++t) acc[n][t] *= f;
             }
             float x[8];
 #pragma unroll
@@ -423,37 +413,35 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
           // Values.
           if constexpr (kBf16) {
 #pragma unroll
-            for (int j = 0; j < 4 * kSets; ++j) {
-              u32x4 x = vv[j % AHEAD];
-              if (j + AHEAD < 4 * kSets) vv[j % AHEAD] = values_of(j + AHEAD);
-              if (scrub)
+            for (int t = 0; t < kTiles; ++t) {
+              if (t >= kValuesAhead) vv[t] = values_of(t);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = finite_only(x[i]);
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(__builtin_bit_cast(bf16x8, x), pr[n], acc[n][j >> 2][j & 3]);
+              for (int n = 0; n < NQ; ++n) acc[n][t] = mfma(__builtin_bit_cast(bf16x8, vv[t]), pr[n], acc[n][t]);
             }
           } else {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
 #pragma unroll
               for (int e = 0; e < kSets; ++e) {
-                f32x4 y = value4(x >> 2, x & 3, e);
-                if (scrub)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) y[j] = fabsf(y[j]) < INFINITY ? y[j] : 0.0f;
+                // four elements of token 4 g + x % 4 of half x / 4
+                const f32x4 y = lds_at<f32x4>(value_at[0] + (sub * 32 + (x >> 2) * 16 + (x & 3)) * (D * 4) + min(e * 64 + c * 4, D - 4) * 4);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) acc[n][e][j] = mfma1(y[j], s[n][x >> 2][x & 3], acc[n][e][j]);
+                  for (int j = 0; j < 4; ++j) acc[n][4 * e + j] = mfma1(y[j], s[n][x >> 2][x & 3], acc[n][4 * e + j]);
               }
           }
         }
-        if (more) store(buf ^ 1, tr + SUB * 32);
-        buf ^= 1;
-        __syncthreads();
+        key_at += turn;
+#pragma unroll
+        for (int t = 0; t < (kBf16 ? kTiles : 1); ++t) value_at[t] += turn;
+        turn = -turn;
       }
 
-      // This wave's rows are its own: out, or into the workspace.
+      // This wave's rows are its own: out, or into the workspace. (Places computed anew: kept from job to job they
+      // would take the loop's registers.)
+      int own = g;
+      asm("" : "+v"(own));
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         l[n] = row_sum(l[n]);
@@ -463,30 +451,25 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void prompt_attention(PromptArgs
           const int64_t token = me.q0 + i;
           const float f = parts > 1 ? 1.0f : l[n] == 0.0f ? 0.0f : 1.0f / l[n];
           const uint32_t at = static_cast<uint32_t>((2 * w + (before == 0)) * R + r);
+          constexpr int N = kBf16 ? 4 : 16;  // neighbouring elements of a lane
 #pragma unroll
-          for (int e = 0; e < kSets; ++e) {
-            if (e * 64 + g * 16 >= D) continue;  // a lane's sixteen elements: all in the row or none
-            float o[16];
+          for (int x = 0; x < kTiles; x += kBf16 ? 1 : 4) {
+            const int from = 16 * x + N * own;
+            if (from >= D) continue;  // all in the row or none
+            float o[N];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = acc[n][e][x & 3][x >> 2] * f;
-            const int from = e * 64 + g * 16;
+            for (int y = 0; y < N; ++y) o[y] = (kBf16 ? acc[n][x][y & 3] : acc[n][x + (y & 3)][y >> 2]) * f;
             const int64_t to = token * a.o_token + head * a.o_head + from;
-            if (parts > 1) {
 #pragma unroll
-              for (int x = 0; x < 16; x += 4)
-                ar::st16<ar::kCoh>(part, (at * D + from + x) * 4,
-                                   u32x4{__float_as_uint(o[x]), __float_as_uint(o[x + 1]), __float_as_uint(o[x + 2]),
-                                         __float_as_uint(o[x + 3])});
-            } else if constexpr (kBf16) {
-              u32x4* p = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + to);
-#pragma unroll
-              for (int x = 0; x < 16; x += 8)
-                p[x / 8] = u32x4{ar::bf16x2_rne(o[x], o[x + 1]), ar::bf16x2_rne(o[x + 2], o[x + 3]),
-                                 ar::bf16x2_rne(o[x + 4], o[x + 5]), ar::bf16x2_rne(o[x + 6], o[x + 7])};
-            } else {
-              f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to);
-#pragma unroll
-              for (int x = 0; x < 16; x += 4) p[x / 4] = f32x4{o[x], o[x + 1], o[x + 2], o[x + 3]};
+            for (int y = 0; y < N; y += 4) {
+              if (parts > 1)
+                ar::st16<ar::kCoh>(part, (at * D + from + y) * 4,
+                                   u32x4{__float_as_uint(o[y]), __float_as_uint(o[y + 1]), __float_as_uint(o[y + 2]),
+                                         __float_as_uint(o[y + 3])});
+              else if constexpr (kBf16)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + to) = u32x2{ar::bf16x2_rne(o[0], o[1]), ar::bf16x2_rne(o[2], o[3])};
+              else
+                *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to + y) = f32x4{o[y], o[y + 1], o[y + 2], o[y + 3]};
             }
           }
           if (g == 0) {
