@@ -209,8 +209,8 @@ int ar_pages_copy(const ar_pages_copy_args* a, void* stream);
  * head h reads kv head h / group. lse, types, statistics and special values are as in
  * ar_kv4_attention: probabilities are rounded to bfloat16 for AR_BFLOAT16; AR_FLOAT32 calls multiply in
  * binary32. A NaN or infinity of a masked place does not reach a result. Starts are taken between 0 and
- * ntokens; tokens that no request covers keep their rows of out and lse. q, k, v and out are 16-byte aligned, their
- * strides multiples of 16 bytes.
+ * ntokens; tokens that no request covers keep their rows of out and lse, those of requests that overlap are
+ * undefined. q, k, v and out are 16-byte aligned, their strides multiples of 16 bytes.
  *
  * ar_prompt_create: a handle with the workspace (partial results), for kv_heads 1..1024 and head_dim 64,
  * 96, 128, 192 or 256. Calls on one handle are issued in order on one stream, on the GPU that was

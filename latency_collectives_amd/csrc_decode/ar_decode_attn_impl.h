@@ -292,20 +292,35 @@ __device__ __forceinline__ bool arrive(uint32_t* arrived, int parts, int* last) 
   return *last;
 }
 
+// The thread's number, computed where it is used: places that follow from it would be kept from job to job, in registers
+// that the loop over the tokens needs.
+__device__ __forceinline__ int thread_here() {
+  int t = threadIdx.x;
+  asm("" : "+v"(t));
+  return t;
+}
+
+// Zeros that are not a constant kept from job to job either.
+__device__ __forceinline__ f32x4 zeros_here() {
+  float z = 0.0f;
+  asm("" : "+v"(z));
+  return f32x4{z, z, z, z};
+}
+
 // Joins a job's parts, in the order of the tokens. A thread reads eight elements of a row from
 // every part, or from every `groups`-th where threads are left over; N parts are under way at once.
-template <int D, int R, int N, class F>
+template <int D, int R, int N, int THREADS = kAttnThreads, class F>
 __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, int first_wg, int parts, int rows,
                                            float* lds, F finish) {
   constexpr int NC = D / 8;
-  const int tid = threadIdx.x, items = rows * NC;
+  const int tid = thread_here(), items = rows * NC;
   int groups = 1;
-  while (groups * 2 * items <= kAttnThreads && groups * N < parts) groups *= 2;
-  for (int x0 = 0; x0 < items * groups; x0 += kAttnThreads) {
+  while (groups * 2 * items <= THREADS && groups * N < parts) groups *= 2;
+  for (int x0 = 0; x0 < items * groups; x0 += THREADS) {
     const int x = x0 + tid, mine = x / items, y = x - mine * items;
     const int r = y / NC, seg = y - r * NC;
     float top = -INFINITY, rl = 0.0f;
-    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+    f32x4 o0 = zeros_here(), o1 = zeros_here();
     for (int p0 = mine; p0 < parts && mine < groups; p0 += N * groups) {
       u32x2 st[N];
       u32x4 v0[N], v1[N];
@@ -357,17 +372,17 @@ __device__ __forceinline__ void join_parts(ar::rsrc_t part, uint32_t stats_at, i
 }
 
 // The same for many rows and at most N parts: a thread has N parts of I segments under way at once.
-template <int D, int R, int N, int I, class F>
+template <int D, int R, int N, int I, int THREADS = kAttnThreads, class F>
 __device__ __forceinline__ void join_few(ar::rsrc_t part, uint32_t stats_at, int first_wg, int parts, int rows,
                                          F finish) {
   constexpr int NC = D / 8;
   const int items = rows * NC;
-  for (int x0 = threadIdx.x; x0 < items; x0 += I * kAttnThreads) {
+  for (int x0 = thread_here(); x0 < items; x0 += I * THREADS) {
     u32x2 st[I][N];
     u32x4 v0[I][N], v1[I][N];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int x = min(x0 + i * kAttnThreads, items - 1), r = x / NC, seg = x - r * NC;
+      const int x = min(x0 + i * THREADS, items - 1), r = x / NC, seg = x - r * NC;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const int p = min(k, parts - 1);
@@ -379,9 +394,9 @@ __device__ __forceinline__ void join_few(ar::rsrc_t part, uint32_t stats_at, int
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int x = x0 + i * kAttnThreads, r = x / NC, seg = x - r * NC;
+      const int x = x0 + i * THREADS, r = x / NC, seg = x - r * NC;
       float top = -INFINITY, rl = 0.0f;
-      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+      f32x4 o0 = zeros_here(), o1 = zeros_here();
 #pragma unroll
       for (int k = 0; k < N; ++k)
         if (k < parts) top = fmaxf(top, __uint_as_float(st[i][k].x));

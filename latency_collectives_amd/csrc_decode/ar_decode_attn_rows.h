@@ -64,6 +64,9 @@ __device__ __forceinline__ Series lane_series(const Series& c, int l) {
           __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo)};
 }
 
+// The same of a request's series that every lane has, held once for the wave.
+__device__ __forceinline__ Series wave_series(const Series& c) { return lane_series(c, 0); }
+
 // As find_run, with a job's units in `span`; series_of<R>(args, b) gives request b.
 template <int R, class ARGS>
 __device__ __forceinline__ bool find_rows(const ARGS& args, int w, Run& run, Series& mine, int& span) {

@@ -57,6 +57,21 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
+// Infinities and NaN that not all of a tile's rows see: 0 times them would be NaN for those that do not. Takes them
+// out of `bytes` of values in LDS and tells whether there were any; a barrier before and behind is the caller's.
+template <int DT, int THREADS>
+__device__ __forceinline__ bool take_out(uint8_t* values, int bytes) {
+  bool some = false;
+  for (int x = thread_here() * 16; x < bytes; x += THREADS * 16) {
+    u32x4* const p = reinterpret_cast<u32x4*>(values + x);
+    const u32x4 v = *p;
+    u32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = DT == DT_BF16 ? finite_only(v[i]) : (v[i] & 0x7F800000u) == 0x7F800000u ? 0 : v[i];
+    if (y[0] != v[0] || y[1] != v[1] || y[2] != v[2] || y[3] != v[3]) some = true, *p = y;
+  }
+  return __any(some);
+}
 // The operand of 1 where sees(u, i) holds for token 4 g + i of half u.
 template <class F>
 __device__ __forceinline__ bf16x8 visible_of(F sees) {

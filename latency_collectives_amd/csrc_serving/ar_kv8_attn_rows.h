@@ -190,6 +190,31 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_rows(AttnArgs
         const bool more = h0 + 2 * SUB < halves;
         const u32x4 some_nan = any_nan[buf];
         const bool round_nan = uniform(some_nan[0] | some_nan[1] | some_nan[2] | some_nan[3]) != 0;
+        if (round_nan) {
+          // NaN codes: added for the rows that see them and taken out, as masked ones times 0 would be NaN too.
+#pragma unroll 1
+          for (int sub = 0; sub < SUB; ++sub) {
+            const int h = h0 + 2 * sub, t0 = t_begin + h * 16 + (thread_here() >> 4 & 3) * 4;
+            const int both = static_cast<int>(seen >> (h - base)) & 3;
+            bf16x8 visible[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+              visible[n] = visible_of([&](int u, int i) {
+                const int t = t0 + u * 16 + i;
+                return t < hi[n] && t >= lo[n] && (both >> u & 1) != 0;
+              });
+#pragma unroll
+            for (int j = 0; j < 4 * kSets; ++j) {
+              const u32x4 x = values[buf][sub * SPLIT + j / OPS][j % OPS][lane];
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) add_infinite(x, visible[n], acc[n][j >> 2][j & 3]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          __syncthreads();
+          take_out<DT_BF16, kAttnThreads>(reinterpret_cast<uint8_t*>(values[buf]), sizeof(values[buf]));
+          __syncthreads();
+        }
         if (more) load_values(h0 + 2 * SUB + my_unit * 2);
 #pragma unroll 1
         for (int sub0 = 0; sub0 < SUB; sub0 += TURNS)
@@ -206,19 +231,6 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_rows(AttnArgs
               const int t = t0 + u * 16 + g * 4 + i;
               return t < hi[n] && t >= lo[n] && (both >> u & 1) != 0;
             };
-            const bool scrub = masked && round_nan;  // NaN values of tokens that only some rows see
-            if (scrub) {
-              bf16x8 visible[NQ];
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) visible[n] = visible_of([&](int u, int i) { return sees(n, u, i); });
-#pragma unroll
-              for (int j = 0; j < 4 * kSets; ++j) {
-                const u32x4 x = values[buf][sub * SPLIT + j / OPS][j % OPS][lane];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) add_infinite(x, visible[n], acc[n][j >> 2][j & 3]);
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            }
             // Scores.
             __builtin_amdgcn_s_setprio(1);
             f32x4 s[NQ][2];
@@ -280,23 +292,12 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_rows(AttnArgs
               split<1>(x, &pr[n]);
             }
             // Values.
-            if (scrub) {
 #pragma unroll
-              for (int j = 0; j < 4 * kSets; ++j) {
-                const u32x4 y = __builtin_bit_cast(u32x4, operand_of(j));
-                const bf16x8 x = operand(finite_only(y[0]), finite_only(y[1]), finite_only(y[2]), finite_only(y[3]));
+            for (int j = 0; j < 4 * kSets; ++j) {
+              const bf16x8 x = vv[j % AHEAD];
+              if (j + AHEAD < 4 * kSets) vv[j % AHEAD] = operand_of(j + AHEAD);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4 * kSets; ++j) {
-                const bf16x8 x = vv[j % AHEAD];
-                if (j + AHEAD < 4 * kSets) vv[j % AHEAD] = operand_of(j + AHEAD);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
-              }
+              for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(x, pr[n], acc[n][j >> 2][j & 3]);
             }
           }
           if (TURNS == 1) {
@@ -380,8 +381,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention_rows(AttnArgs
         run.head = 0;
         do {
           if (++run.request >= a.nreq) return;  // only if lengths change under the call
-          me = series_of<R>(args, run.request);
-          me.tiles = uniform(me.tiles);
+          me = wave_series(series_of<R>(args, run.request));
         } while (me.tiles == 0);
       }
     }

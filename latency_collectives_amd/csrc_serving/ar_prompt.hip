@@ -28,6 +28,17 @@ constexpr size_t kPromptArrived = 1024 * sizeof(uint32_t);  // at least every ke
 // What starting and ending a job costs, in units of 32 tokens.
 constexpr int kPromptJobUnits = 12;
 
+// Few rows: a workgroup for 16 rows and a kv head, which takes its units without a share for others. As long as jobs times
+// units, with kFewJobUnits for a job's start and end, stay below kFewWork. 8 query heads on one kv head of 128, us with
+// few rows' kernel and with the others: one prompt of 301 tokens 7.9 and 16.6, of 1000 (10 000) 20.3 and 28.1,
+// of 2000 (36 000) 57.5 and 41.8; 16 of up to 200, 32 heads on 8 (22 000), 38.9 and 28.9, of up to 100 (11 000), 19.3
+// and 16.2.
+constexpr int kFewJobUnits = 4, kFewWork = 10240;
+
+// Large tiles: where every workgroup gets so many units of its tile's rows. One prompt of 4000 tokens, 8 heads on one
+// of 128 (20): 74 us with large tiles, 64 without; eight of up to 2000, 32 on 8 (48): 163 and 174; one of 8000 (82): 151 and 168.
+constexpr int kLargeUnits = 40;
+
 // Bytes between two tokens' keys or values: a round's 128 tokens stay below 2^31.
 constexpr int64_t kMostStride = int64_t(1) << 23;
 
@@ -42,8 +53,10 @@ ar_prompt* ar_prompt_create(int kv_heads, int head_dim) {
     ar_fail(AR_EINVAL, "kv_heads must be in [1, 1024], got %d", kv_heads);
     return nullptr;
   }
-  const PromptKernel bf16 = select_prompt_bf16(head_dim), f32 = select_prompt_f32(head_dim);
-  if (bf16.fn == nullptr || f32.fn == nullptr) {
+  const PromptKernel all[] = {select_prompt_bf16(head_dim, false), select_prompt_bf16(head_dim, true), select_prompt_f32(head_dim)};
+  size_t work_bytes = 0;
+  for (const PromptKernel& k : all) work_bytes = std::max(work_bytes, k.fn == nullptr ? 0 : prompt_part_bytes(k, head_dim));
+  if (work_bytes == 0) {
     ar_fail(AR_ENOTSUP, "head_dim must be 64, 96, 128, 192 or 256, got %d", head_dim);
     return nullptr;
   }
@@ -52,8 +65,7 @@ ar_prompt* ar_prompt_create(int kv_heads, int head_dim) {
     ar_fail(AR_ENORES, "out of host memory");
     return nullptr;
   }
-  *h = ar_prompt{kv_heads, head_dim, -1, nullptr,
-                 std::max(prompt_part_bytes(bf16, head_dim), prompt_part_bytes(f32, head_dim))};
+  *h = ar_prompt{kv_heads, head_dim, -1, nullptr, work_bytes};
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -109,13 +121,24 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
     if (s < 0) return ar_fail(AR_EINVAL, "negative stride");
   }
   if (std::max(a->k_token, a->v_token) > kMostStride / bytes) return ar_fail(AR_ETOOBIG, "a token's keys or values are more than 2^23 bytes apart");
-  const PromptKernel k = bf16 ? select_prompt_bf16(h->head_dim) : select_prompt_f32(h->head_dim);
   // Rows of a kv head, and a unit of every job beside what its start and end count for, in 31 bits.
   const int group = a->q_heads / h->heads;
   const int64_t all_rows = static_cast<int64_t>(a->ntokens) * group;
   if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  const int64_t tiles = all_rows / k.rows + std::min(a->nreq, a->ntokens), jobs = tiles * h->heads;
-  if (tiles * k.rows > 0x7FFFFFFF || jobs * (1 + kPromptJobUnits) > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  // The units of 32 tokens that a row sees if prompts are alike, and the kernel.
+  const int prompts = std::min(a->nreq, a->ntokens);
+  int64_t sees = a->ntokens / prompts;
+  sees = a->window > 0 ? std::min<int64_t>(sees / 2, a->window) : sees / 2;
+  const int64_t units = sees / 32 + 1;
+  PromptKernel k = select_prompt_few(a->dtype, h->head_dim);
+  int64_t tiles = all_rows / k.rows + prompts, jobs = tiles * h->heads;
+  const bool few = jobs * (units + kFewJobUnits) <= kFewWork;
+  if (!few) {
+    k = bf16 ? select_prompt_bf16(h->head_dim, true) : select_prompt_f32(h->head_dim);
+    if (bf16 && all_rows * h->heads / k.rows * units < kLargeUnits * k.fill) k = select_prompt_bf16(h->head_dim, false);
+    tiles = all_rows / k.rows + prompts, jobs = tiles * h->heads;
+    if (tiles * k.rows > 0x7FFFFFFF || jobs * (1 + kPromptJobUnits) > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+  }
   if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
   int device = -1;
   AR_HIP(hipGetDevice(&device));
@@ -133,6 +156,11 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
     if (a->scale < 0) args.q_sign = 0x80008000u;
     // not zero: a masked score's infinity times it has to stay one
     args.scale_log2 = std::max(std::fabs(args.scale_log2), 1e-38f);
+  }
+  if (few) {
+    hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(tiles), h->heads), dim3(k.threads), 0, static_cast<hipStream_t>(stream), args);
+    AR_HIP(hipGetLastError());
+    return AR_OK;
   }
   args.part = static_cast<uint8_t*>(h->work);
   args.part_bytes = static_cast<uint32_t>(prompt_part_bytes(k, h->head_dim));
@@ -155,7 +183,7 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
   const int64_t runs = (jobs * span() + kAttnWaves - 1) / kAttnWaves;
   const int64_t grid = (std::min<int64_t>(k.fill, runs) + 7) & ~int64_t(7);
   args.runs = static_cast<uint32_t>(grid);
-  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, static_cast<hipStream_t>(stream), args);
+  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(k.threads), 0, static_cast<hipStream_t>(stream), args);
   AR_HIP(hipGetLastError());
   return AR_OK;
 }

@@ -1,0 +1,292 @@
+// Attention over packed prompts where rows are few (gfx950): a tile of 16 rows a workgroup, its four waves on different
+// tokens.
+//
+// Such a call is bound by latency: what stands one after the other is the launch, the starts, the first keys and values, a
+// wave's units, the join. So there is no split between workgroups and no workspace; a workgroup finds its tile by one scan
+// over the starts; a wave takes every fourth unit, straight from memory into the operands' registers (a unit ahead), and
+// the four sums meet in LDS.
+//
+//   bfloat16   a unit is 32 tokens; values: four elements of eight tokens a lane, tokens paired by one permute a word
+//   binary32   a unit is 16 tokens; values: four elements of a token a lane, as the 16x16x4 products take them
+//
+// One prompt of 301 tokens, 8 query heads on one kv head of 128, bfloat16: 7.9 us, 16.6 us by the kernels for many rows
+// (binary32: 16.6 and 24.9).
+#pragma once
+
+#include "ar_prompt.h"
+
+namespace ard {
+
+template <int DT, int D>
+struct FewUnit {  // a lane's share of a unit, as loaded
+  static constexpr bool kBf16 = DT == DT_BF16;
+  static constexpr int kSteps = kBf16 ? D / 32 : D / 16, kSets = (D + 63) / 64;
+  static constexpr int U = kBf16 ? 2 : 1;  // times 16 tokens
+  typedef typename std::conditional<kBf16, u32x2, u32x4>::type V;
+  u32x4 k[U][kSteps];
+  V v[4 * U][kSets];  // [u * 4 + i]: token 16 u + 4 g + i
+};
+
+template <int DT, int D>
+__global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attention_few(PromptArgs args) {
+  constexpr int R = 16;
+  constexpr bool kBf16 = DT == DT_BF16;
+  constexpr int ES = kBf16 ? 2 : 4, NC = D / 8;
+  typedef FewUnit<DT, D> Unit;
+  typedef typename std::conditional<kBf16, bf16x8, f32x4>::type Q;
+  constexpr int kSteps = Unit::kSteps, kSets = Unit::kSets, U = Unit::U, T = 16 * U;
+  constexpr int kPitch = D + 4;  // LDS row: 16 rows' 16-byte accesses fall into different banks
+  __shared__ float join[kAttnWaves * 16 * kPitch];
+  __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
+
+  const ar_prompt_attention_args& a = args.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  // The tile: lanes are requests.
+  uint32_t tile = blockIdx.x;
+  PromptJob j;
+  {
+    int b0 = 0;
+    uint32_t tiles, upto;
+    int q0, m;
+    for (;; b0 += 64) {
+      if (b0 >= a.nreq) return;
+      q0 = m = 0;
+      if (b0 + lane < a.nreq) {
+        const int at = a.q_start[b0 + lane], to = a.q_start[b0 + lane + 1];
+        q0 = min(max(at, 0), a.ntokens);
+        m = max(min(to, a.ntokens), q0) - q0;
+      }
+      tiles = (static_cast<uint32_t>(m) * static_cast<uint32_t>(args.group) + R - 1) / R;
+      upto = wave_scan(tiles);
+      if (__ballot(upto > tile) != 0) break;
+      tile -= static_cast<uint32_t>(lane_value(upto, 63));
+    }
+    const int who = __builtin_ctzll(__ballot(upto > tile));
+    tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
+    if (tile >= static_cast<uint32_t>(lane_value(tiles, who))) return;  // requests that overlap: their sum may have wrapped
+    j.q0 = lane_value(q0, who);
+    j.rows = lane_value(m, who) * args.group;
+  }
+  j.head = blockIdx.y, j.group = args.group, j.per_group = args.per_group, j.window = a.window;
+  j.row0 = uniform(static_cast<int>(tile * R));
+  j.i0 = uniform(static_cast<uint32_t>(j.row0) / static_cast<uint32_t>(j.group)), j.rem0 = j.row0 - j.i0 * j.group;
+  const int last = min(R, j.rows - j.row0) - 1;
+  j.i1 = j.i0 + uniform(j.token_of(last));
+  const int end = j.i1 + 1, begin = a.window > 0 ? max(window_start(j.i0, a.window), 0) & ~31 : 0;
+  j.k_row = a.k_token * ES, j.v_row = a.v_token * ES;
+  const uint8_t* keys = static_cast<const uint8_t*>(a.k) + j.q0 * j.k_row + j.head * a.k_head * ES;
+  const uint8_t* vals = static_cast<const uint8_t*>(a.v) + j.q0 * j.v_row + j.head * a.v_head * ES;
+
+  const uint32_t k_off = c * static_cast<uint32_t>(j.k_row) + g * 16;
+  auto load = [&](int t0, Unit& x) {
+    const ar::rsrc_t kr = rows_from(keys, j.k_row, t0, end, D * ES), vr = rows_from(vals, j.v_row, t0, end, D * ES);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        x.k[u][s] = ar::ld16<ar::kPlain>(kr, k_off + u * 16 * static_cast<uint32_t>(j.k_row) + s * 64);
+#pragma unroll
+    for (int t = 0; t < 4 * U; ++t)
+#pragma unroll
+      for (int e = 0; e < kSets; ++e) {  // lanes beyond the row repeat its last elements
+        const uint32_t at = ((t >> 2) * 16 + g * 4 + (t & 3)) * static_cast<uint32_t>(j.v_row) + min(e * 64 + c * 4, D - 4) * ES;
+        if constexpr (kBf16) x.v[t][e] = ar::ld8<ar::kPlain>(vr, at);
+        else x.v[t][e] = ar::ld16<ar::kPlain>(vr, at);
+      }
+  };
+  Unit now, next;
+  int t0 = begin + wave * T;
+  if (t0 < end) load(t0, now);
+
+  // The rows, the same for every wave.
+  const int r = min(c, last), i = j.i0 + j.token_of(r);
+  const int hi = i + 1, lo = a.window > 0 ? window_start(i, a.window) : 0;
+  const int whole_end = j.i0 + 1, whole_begin = a.window > 0 ? window_start(j.i1, a.window) : 0;
+  Q q[kSteps];
+  {
+    const int64_t at = static_cast<int64_t>(j.q0 + i) * a.q_token +
+                       static_cast<int64_t>(j.head * j.group + j.row0 + r - i * j.group) * a.q_head;
+    const uint8_t* x = static_cast<const uint8_t*>(a.q) + at * ES + g * 16;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const u32x4 y = *reinterpret_cast<const u32x4*>(x + s * 64);
+      if constexpr (kBf16) q[s] = __builtin_bit_cast(Q, y ^ args.q_sign);
+      else q[s] = __builtin_bit_cast(Q, y);
+    }
+  }
+
+  f32x4 acc[kSets][4];  // [k]: element 64 e + 16 g + 4 k + j of row c
+  float m = kLowest, l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kSets; ++e)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[e][k] = f32x4{0, 0, 0, 0};
+
+#pragma unroll 1
+  for (; t0 < end; t0 += T * kAttnWaves) {
+    if (t0 + T * kAttnWaves < end) load(t0 + T * kAttnWaves, next);
+    // Scores.
+    f32x4 s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Q kk = __builtin_bit_cast(Q, now.k[u][k]);
+        if constexpr (kBf16) {
+          s[u] = mfma(kk, q[k], s[u]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[u] = mfma1(kk[x], q[k][x], s[u]);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] *= args.scale_log2;
+    auto sees = [&](int u, int x) {
+      const int t = t0 + u * 16 + g * 4 + x;
+      return t < hi && t >= lo;
+    };
+    // bfloat16: the operand of elements 64 e + 4 c + k.
+    auto value_of = [&](int e, int k) {
+      u32x4 w = {0, 0, 0, 0};
+      if constexpr (kBf16) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const u32x2 v0 = now.v[2 * x][e], v1 = now.v[2 * x + 1][e];
+          w[x] = k == 0 ? pair_lo(v0.x, v1.x) : k == 1 ? pair_hi(v0.x, v1.x) : k == 2 ? pair_lo(v0.y, v1.y) : pair_hi(v0.y, v1.y);
+        }
+      }
+      return w;
+    };
+    if (t0 + T > whole_end || t0 < whole_begin) {
+#pragma unroll
+      for (int x = 0; x < 4 * U; ++x)
+        if (!sees(x >> 2, x & 3)) s[x >> 2][x & 3] = -INFINITY;
+      // Infinities and NaN that not all rows see: added by products of their own for the rows that do.
+      bool odd = false;
+#pragma unroll
+      for (int t = 0; t < 4 * U; ++t)
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int x = 0; x < ES; ++x) {
+            const uint32_t w = now.v[t][e][x];
+            odd |= kBf16 ? finite_only(w) != w : (w & 0x7F800000u) == 0x7F800000u;
+          }
+      if (__any(odd)) {
+        bf16x8 visible;
+        if constexpr (kBf16) visible = visible_of(sees);
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kBf16) {
+              add_infinite(value_of(e, k), visible, acc[e][k]);
+            } else {
+              f32x4 up = {0, 0, 0, 0}, down = {0, 0, 0, 0};
+#pragma unroll
+              for (int t = 0; t < 4 * U; ++t) {
+                const float y = __uint_as_float(now.v[t][e][k]), one = sees(t >> 2, t & 3) ? 1.0f : 0.0f;
+                up = mfma1(y <= 3.4028235e38f ? 0.0f : 1.0f, one, up);
+                down = mfma1(y >= -3.4028235e38f ? 0.0f : 1.0f, one, down);
+              }
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if (up[x] > 0.0f) acc[e][k][x] += INFINITY;
+                if (down[x] > 0.0f) acc[e][k][x] -= INFINITY;
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+        for (int t = 0; t < 4 * U; ++t)
+#pragma unroll
+          for (int e = 0; e < kSets; ++e)
+#pragma unroll
+            for (int x = 0; x < ES; ++x) {
+              const uint32_t w = now.v[t][e][x];
+              now.v[t][e][x] = kBf16 ? finite_only(w) : (w & 0x7F800000u) == 0x7F800000u ? 0 : w;
+            }
+      }
+    }
+    // Probabilities.
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 1; x < 4 * U; ++x) top = fmaxf(top, s[x >> 2][x & 3]);
+    if (__any(top > m + 8.0f)) {
+      const float to = fmaxf(m, row_max(top));
+      const float f = exp2_fast(m - to);
+      m = to;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kSets; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[e][k] *= f;
+    }
+    float p[4 * U];
+#pragma unroll
+    for (int x = 0; x < 4 * U; ++x) {
+      p[x] = exp2_fast(s[x >> 2][x & 3] - m);
+      l += p[x];
+    }
+    // Values.
+    if constexpr (kBf16) {
+      bf16x8 pr;
+      split<1>(p, &pr);
+#pragma unroll
+      for (int e = 0; e < kSets; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[e][k] = mfma(__builtin_bit_cast(bf16x8, value_of(e, k)), pr, acc[e][k]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4 * U; ++t)
+#pragma unroll
+        for (int e = 0; e < kSets; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[e][k] = mfma1(__uint_as_float(now.v[t][e][k]), p[t], acc[e][k]);
+    }
+    now = next;
+  }
+
+  // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
+  l = row_sum(l);
+  if (g == 0) stat_m[wave][c] = m, stat_l[wave][c] = l;
+  __syncthreads();
+  float most = stat_m[0][c];
+#pragma unroll
+  for (int x = 1; x < kAttnWaves; ++x) most = fmaxf(most, stat_m[x][c]);
+  const float f = exp2_fast(m - most);
+  float* mine = join + (wave * 16 + c) * kPitch + g * 16;
+#pragma unroll
+  for (int e = 0; e < kSets; ++e)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (e * 64 + g * 16 + x * 4 >= D) continue;
+      f32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[e][k][x] * f;
+      *reinterpret_cast<f32x4*>(mine + e * 64 + x * 4) = v;
+    }
+  __syncthreads();
+  for (int x = tid; x < 16 * NC; x += kAttnThreads) {
+    const int row = x / NC, seg = x - row * NC;
+    if (row > last) continue;
+    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+    float rm = stat_m[0][row], rl = 0.0f;
+#pragma unroll
+    for (int y = 1; y < kAttnWaves; ++y) rm = fmaxf(rm, stat_m[y][row]);
+#pragma unroll
+    for (int y = 0; y < kAttnWaves; ++y) {
+      const float* from = join + (y * 16 + row) * kPitch + seg * 8;
+      o0 += *reinterpret_cast<const f32x4*>(from);
+      o1 += *reinterpret_cast<const f32x4*>(from + 4);
+      rl += stat_l[y][row] * exp2_fast(stat_m[y][row] - rm);
+    }
+    const int token = j.i0 + j.token_of(row);
+    finish_row<DT>(a, j.q0 + token, j.head * j.group + j.row0 + row - token * j.group, seg, o0, o1, rm, rl);
+  }
+}
+
+}  // namespace ard
