@@ -31,13 +31,32 @@ struct Series {
   int q0, m, kv, tiles;
   uint32_t first;     // units of tile 0
   double half_slope;  // half of what a tile has more than the one before
-  __device__ uint32_t below(int r) const { return static_cast<uint32_t>(r * (first + (r - 1) * half_slope)); }
+  int knee;           // tiles from here on see a whole window: `most` units each
+  uint32_t most;
+  __device__ uint32_t below(int r) const {
+    const int s = min(r, knee);
+    return static_cast<uint32_t>(s * (first + (s - 1) * half_slope)) + (r - s) * most;
+  }
+  // Tile 0 sees `low` tokens, a tile R rows more than the one before, the last one `end`; units(t) of t tokens.
+  template <int R, class F>
+  __device__ void set(int low, int end, uint32_t most_seen, int group, F units) {
+    first = units(low);
+    knee = tiles, most = 0;
+    if (static_cast<uint32_t>(end) > most_seen) {
+      most = units(end);
+      const double rows = static_cast<uint32_t>(low) < most_seen ? static_cast<double>(most_seen - low) * group : 0.0;
+      knee = static_cast<int>(min(rows / R + 1.0, static_cast<double>(tiles)));
+      if (knee > 1) half_slope = static_cast<double>(most - first) / (2 * knee);
+    } else if (tiles > 1) {
+      half_slope = static_cast<double>(units(end) - first) / (2 * (tiles - 1));
+    }
+  }
 };
 
 template <int R>
 __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
   const ar_kv4_attention_args& a = args.a;
-  Series c = {0, 0, 0, 0, 1, 0.0};
+  Series c = {0, 0, 0, 0, 1, 0.0, 0, 0};
   if (b < a.nreq) {
     const int at = a.q_start[b], to = a.q_start[b + 1];
     c.kv = max(a.kv_len[b], 0);
@@ -49,8 +68,7 @@ __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
     auto units = [&](int seen) {
       return ((min(static_cast<uint32_t>(seen), args.most_seen) + args.unit - 1) >> args.unit_shift) + args.job_units;
     };
-    c.first = units(low);
-    if (c.tiles > 1) c.half_slope = static_cast<double>(units(end) - c.first) / (2 * (c.tiles - 1));
+    c.template set<R>(low, end, args.most_seen, args.group, units);
   }
   return c;
 }
@@ -61,7 +79,8 @@ __device__ __forceinline__ Series lane_series(const Series& c, int l) {
   const uint32_t lo = lane_value(static_cast<uint32_t>(slope), l), hi = lane_value(static_cast<uint32_t>(slope >> 32), l);
   return {lane_value(c.q0, l), lane_value(c.m, l), lane_value(c.kv, l), lane_value(c.tiles, l),
           static_cast<uint32_t>(lane_value(c.first, l)),
-          __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo)};
+          __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo), lane_value(c.knee, l),
+          static_cast<uint32_t>(lane_value(c.most, l))};
 }
 
 // The same of a request's series that every lane has, held once for the wave.
@@ -109,7 +128,9 @@ __device__ __forceinline__ bool find_rows(const ARGS& args, int w, Run& run, Ser
   int r = 0;
   if (mine.tiles > 1) {
     const double h = mine.half_slope, f = mine.first - h;
-    const double root = h > 0 ? (sqrt(f * f + 4 * h * from) - f) / (2 * h) : from / f;
+    const uint32_t ramp = mine.below(mine.knee);
+    const double root = from >= ramp && mine.most > 0 ? mine.knee + (from - ramp) / mine.most
+                        : h > 0 ? (sqrt(f * f + 4 * h * from) - f) / (2 * h) : from / f;
     r = min(max(static_cast<int>(root), 0), mine.tiles - 1);
     while (r > 0 && mine.below(r) > from) --r;
     while (r + 1 < mine.tiles && mine.below(r + 1) <= from) ++r;

@@ -31,7 +31,8 @@ struct PromptArgs {
 
 struct PromptKernel {
   void (*fn)(PromptArgs);
-  int fill, rows, threads;
+  int fill, rows, threads;  // workgroups that the device holds, rows of a tile
+  int job_units;            // what starting and ending a job costs, in units of 32 tokens
 };
 PromptKernel select_prompt_bf16(int head_dim, bool large);
 PromptKernel select_prompt_f32(int head_dim);
@@ -39,7 +40,7 @@ PromptKernel select_prompt_few(int dtype, int head_dim);  // a workgroup a tile 
 
 template <int R>
 __device__ __forceinline__ Series series_of(const PromptArgs& args, int b) {
-  Series c = {0, 0, 0, 0, 1, 0.0};
+  Series c = {0, 0, 0, 0, 1, 0.0, 0, 0};
   if (b < args.a.nreq) {
     const int at = args.a.q_start[b], to = args.a.q_start[b + 1];
     c.q0 = min(max(at, 0), args.a.ntokens);
@@ -48,8 +49,7 @@ __device__ __forceinline__ Series series_of(const PromptArgs& args, int b) {
     auto units = [&](int seen) {
       return ((min(static_cast<uint32_t>(seen), args.most_seen) + args.unit - 1) >> args.unit_shift) + args.job_units;
     };
-    c.first = units(min(args.tile_tokens, c.m));
-    if (c.tiles > 1) c.half_slope = static_cast<double>(units(c.m) - c.first) / (2 * (c.tiles - 1));
+    c.template set<R>(min(args.tile_tokens, c.m), c.m, args.most_seen, args.group, units);
   }
   return c;
 }

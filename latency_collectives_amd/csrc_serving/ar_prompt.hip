@@ -25,9 +25,6 @@ size_t prompt_part_bytes(const PromptKernel& k, int head_dim) {
 
 constexpr size_t kPromptArrived = 1024 * sizeof(uint32_t);  // at least every kernel's `fill`
 
-// What starting and ending a job costs, in units of 32 tokens.
-constexpr int kPromptJobUnits = 12;
-
 // Few rows: a workgroup for 16 rows and a kv head, which takes its units without a share for others. As long as jobs times
 // units, with kFewJobUnits for a job's start and end, stay below kFewWork. 8 query heads on one kv head of 128, us with
 // few rows' kernel and with the others: one prompt of 301 tokens 7.9 and 16.6, of 1000 (10 000) 20.3 and 28.1,
@@ -137,7 +134,7 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
     k = bf16 ? select_prompt_bf16(h->head_dim, true) : select_prompt_f32(h->head_dim);
     if (bf16 && all_rows * h->heads / k.rows * units < kLargeUnits * k.fill) k = select_prompt_bf16(h->head_dim, false);
     tiles = all_rows / k.rows + prompts, jobs = tiles * h->heads;
-    if (tiles * k.rows > 0x7FFFFFFF || jobs * (1 + kPromptJobUnits) > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
+    if (tiles * k.rows > 0x7FFFFFFF || jobs * (1 + k.job_units) > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
   }
   if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
   int device = -1;
@@ -173,8 +170,8 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
   args.most_seen = static_cast<uint32_t>(seen);
   // Larger units where 32-bit sums of them could overflow.
   args.unit_shift = 5;
-  args.job_units = kPromptJobUnits;
-  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + kPromptJobUnits; };
+  args.job_units = k.job_units;
+  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + k.job_units; };
   while (span() * jobs > 0x7FFFFFFF) ++args.unit_shift;
   args.unit = 1u << args.unit_shift;
   args.tile_shift = args.unit_shift - 5;

@@ -220,10 +220,14 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void prompt_attention_bf16(PromptA
 //   192   8 of 32      936    (12 of 16: 876)
 //   256   12 of 16     861    (8 of 16: 665)
 // Smaller calls, where a workgroup's own rows and the joins count for more: 8 waves of 16 rows, twice a compute unit.
+// Six prompts of up to 8191 tokens, 32 heads on 8, us with a job's start and end taken for 2, 4, 6, 8 and 12 units: 1679, 1612,
+// 1560, 1551, 1567 (head of 256, four of up to 8000: 1446, 1371, 1318, 1291, 1302).
+constexpr int kJobUnits = 8;
+
 PromptKernel select_prompt_bf16(int head_dim, bool large) {
 // rows / 16 of a wave, waves of a workgroup, units of a round, workgroups of a compute unit
 #define ARD_CASE(D, NQ, WAVES, SUB, OCC) \
-  if (head_dim == D) return {prompt_attention_bf16<D, NQ, WAVES, SUB, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES}
+  if (head_dim == D) return {prompt_attention_bf16<D, NQ, WAVES, SUB, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES, kJobUnits}
   if (large) {
     ARD_CASE(64, 2, 8, 2, 2);
     ARD_CASE(96, 2, 12, 3, 1);
@@ -237,7 +241,7 @@ PromptKernel select_prompt_bf16(int head_dim, bool large) {
   }
   ARD_CASE(256, 1, 12, 2, 1);
 #undef ARD_CASE
-  return {nullptr, 0, 0, 0};
+  return {nullptr, 0, 0, 0, 0};
 }
 
 }  // namespace ard
