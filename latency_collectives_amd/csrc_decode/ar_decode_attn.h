@@ -30,15 +30,21 @@ struct AttnArgs {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 
+// Many rows a request: 32 rows for each of a workgroup's waves, if the kernel does not say otherwise.
+constexpr int kRowsColumns = 2, kRowsTile = 16 * kRowsColumns * kAttnWaves;
+
 // A kernel and the workgroups of it that fill the device's 256 compute units.
 struct AttnKernel {
   void (*fn)(AttnArgs);
   int fill;
+  int rows = kRowsTile;  // of a tile, where it is one for many rows
+  int threads = kAttnThreads;
+  // Finding a job, its queries and its end take about what twelve units of 32 tokens take while the
+  // whole device reads; without them in the split, a run of many short requests ended last.
+  int job_units = 12;
 };
 AttnKernel select_attn_bf16(int head_dim, int columns);
 AttnKernel select_attn_f32(int head_dim, int columns);
-// Many rows a request: 32 rows for each of a workgroup's waves.
-constexpr int kRowsColumns = 2, kRowsTile = 16 * kRowsColumns * kAttnWaves;
 AttnKernel select_attn_rows(int head_dim);
 
 

@@ -38,12 +38,12 @@ Choice choose(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
   if (bf16 && each > 128) {
-    const int large = ard::kRowsTile;
-    const int64_t tiles = (each + large - 1) / large * std::min(a->nreq, a->ntokens) * h->heads;
+    const ard::AttnKernel many = f.rows(h->head_dim);
+    const int64_t tiles = (each + ard::kRowsTile - 1) / ard::kRowsTile * std::min(a->nreq, a->ntokens) * h->heads;
     const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
     if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
-      return {f.rows(h->head_dim), large, true};
+      return {many, many.rows, true};
   }
   // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
   // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and
@@ -63,10 +63,6 @@ size_t part_bytes(int runs, int rows, int head_dim) {
 
 constexpr int kMostRuns = 1024;  // at least every kernel's `fill`
 constexpr size_t kArrivedBytes = kMostRuns * sizeof(uint32_t);
-
-// Finding a job, its queries and its end take about what twelve units of 32 tokens take while the
-// whole device reads; without them in the split, a run of many short requests ended last.
-constexpr int kJobUnits = 12;
 
 }  // namespace
 
@@ -94,7 +90,8 @@ ar_kv4* create_handle(const AttnFormat& f, int kv_heads, int head_dim, int page_
   for (int n = 1; n <= 2; ++n)
     for (const AttnKernel& k : {f.bf16(head_dim, n), f.f32(head_dim, n)})
       h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
-  h->work_bytes = std::max(h->work_bytes, part_bytes(f.rows(head_dim).fill, kRowsTile, head_dim));
+  const AttnKernel many = f.rows(head_dim);
+  h->work_bytes = std::max(h->work_bytes, part_bytes(many.fill, many.rows, head_dim));
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -144,7 +141,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
   if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
   const int rows_per_tile = choice.rows;
   const int64_t tiles = all_rows / rows_per_tile + std::min(a->nreq, a->ntokens), jobs = tiles * h->heads;
-  if (tiles * rows_per_tile > 0x7FFFFFFF || jobs * (1 + kJobUnits) > 0x7FFFFFFF)
+  if (tiles * rows_per_tile > 0x7FFFFFFF || jobs * (1 + k.job_units) > 0x7FFFFFFF)
     return ar_fail(AR_ETOOBIG, "too many rows");
   if (h->work == nullptr) return ar_fail(AR_EHIP, "the handle was created without a GPU");
   int device = -1;
@@ -181,17 +178,17 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
   args.room = static_cast<int>(room);
   args.most_seen = static_cast<uint32_t>(seen);
   args.unit_shift = 5;
-  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + kJobUnits; };
+  const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + k.job_units; };
   while (span() * jobs > 0x7FFFFFFF) ++args.unit_shift;
   args.unit = 1u << args.unit_shift;
   args.tile_shift = args.unit_shift - 5;
   args.tile_tokens = (rows_per_tile - 1) / args.group + 1;
-  args.job_units = kJobUnits;
+  args.job_units = k.job_units;
   const int64_t runs = (jobs * span() + kAttnWaves - 1) / kAttnWaves;
   int64_t grid = std::min<int64_t>(k.fill, runs);
   if (choice.many) grid = (grid + 7) & ~7;  // the same number for every XCD
   args.runs = static_cast<uint32_t>(grid);
-  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0,
+  hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(grid)), dim3(k.threads), 0,
                      static_cast<hipStream_t>(stream), args);
   AR_HIP(hipGetLastError());
   return AR_OK;

@@ -300,6 +300,14 @@ __device__ __forceinline__ int thread_here() {
   return t;
 }
 
+// The only argument of the kernel, read where it is used: scalars held for later would take the place of the loop's.
+template <class ARGS>
+__device__ __forceinline__ const ARGS& args_here() {
+  uint64_t p = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(p));
+  return *(const ARGS*)reinterpret_cast<const __attribute__((address_space(4))) ARGS*>(p);
+}
+
 // Zeros that are not a constant kept from job to job either.
 __device__ __forceinline__ f32x4 zeros_here() {
   float z = 0.0f;

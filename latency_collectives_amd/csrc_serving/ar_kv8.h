@@ -57,6 +57,12 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
+#define ARD_LDS __attribute__((address_space(3)))
+template <class T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *reinterpret_cast<const ARD_LDS T*>(at);
+}
+
 // Infinities and NaN that not all of a tile's rows see: 0 times them would be NaN for those that do not. Takes them
 // out of `bytes` of values in LDS and tells whether there were any; a barrier before and behind is the caller's.
 template <int DT, int THREADS>

@@ -4,14 +4,25 @@
 
 namespace ard {
 
+// Two chunks of up to 2048 tokens against 12288, TFLOP/s (16 query heads on 4; 128: 32 on 8), and one layout beside:
+//   64    8 waves of 32 rows, twice a compute unit   759    (8 of 16, twice: 684)
+//   96    12 of 32     747    (8 of 16, twice: 654)
+//   128   12 of 32     957    (8 of 32: 864; 8 of 16, twice: 846)
+//   192   8 of 32, two units a round   860    (one: 746)
+//   256   12 of 16     831    (8 of 16: 718)
+// Short jobs would rather have small tiles: windows of 1000 in chunks of 2048 tokens, 32 heads on 8, 218 us, 190 with 8 waves of 16
+// rows; 64 chunks of 40 tokens against 500 57 and 48.
+constexpr int kJobUnits = 8;  // what starting and ending a job costs; 4 and 12 are within 1% mostly
+
 AttnKernel select_attn8_rows(int head_dim) {
-#define ARD_CASE(D, OCC) \
-  if (head_dim == D) return {kv8_attention_rows<D, kRowsColumns, OCC>, 256 * OCC}
-  ARD_CASE(64, 2);
-  ARD_CASE(96, 2);
-  ARD_CASE(128, 2);
-  ARD_CASE(192, 1);
-  ARD_CASE(256, 1);
+// rows / 16 of a wave, waves of a workgroup, units of a round, workgroups of a compute unit
+#define ARD_CASE(D, NQ, WAVES, SUB, OCC) \
+  if (head_dim == D) return {kv8_attention_rows<D, NQ, WAVES, SUB, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES, kJobUnits}
+  ARD_CASE(64, 2, 8, 4, 2);
+  ARD_CASE(96, 2, 12, 3, 1);
+  ARD_CASE(128, 2, 12, 3, 1);
+  ARD_CASE(192, 2, 8, 2, 1);
+  ARD_CASE(256, 1, 12, 1, 1);
 #undef ARD_CASE
   return {nullptr, 0};
 }

@@ -72,11 +72,6 @@ __device__ __forceinline__ void into_lds(uint32_t to, ar::rsrc_t from, uint32_t 
                : "s"(to), "v"(voffset), "s"(from), "s"(soffset)
                : "memory", "m0");
 }
-#define ARD_LDS __attribute__((address_space(3)))
-template <class T>
-__device__ __forceinline__ T lds_at(uint32_t at) {
-  return *reinterpret_cast<const ARD_LDS T*>(at);
-}
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 // Of 16 lanes that address a row's four elements each, four lanes a row: lane c gets column c of the four rows.
 __device__ __forceinline__ u32x2 lds_columns(uint32_t at) {
