@@ -32,6 +32,13 @@ __device__ __forceinline__ uint32_t encode8(const float* x, float inv) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true));
 }
+// The same of values that are at most 448 of the scale.
+__device__ __forceinline__ uint32_t scaled8(const float* x, float scale) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[0], x[1], scale, false);
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[2], x[3], scale, true));
+}
 // Four codes at another scale, `ratio` of the old to the new.
 __device__ __forceinline__ uint32_t rescale8(uint32_t w, float ratio) {
   const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
@@ -43,7 +50,8 @@ __device__ __forceinline__ uint32_t limit8(uint32_t byte) {
   return min(max(byte, static_cast<uint32_t>(kScale8Min)), static_cast<uint32_t>(kScale8Max));
 }
 
-template <int DT, int G>
+// TURN: keys may be normed and rotated.
+template <int DT, int G, bool TURN>
 __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image) {
   const ar_qk_norm_rope_args& a = p.r.a;
   const Cache& cache = p.r.cache;
@@ -59,29 +67,24 @@ __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image
   // with their slots, so the rest of a token's run is among the 15 tokens before it and the 15 after it.
   constexpr int LOOK = kBlock - 1;
   int64_t slot = -1;
+  int place = -1;  // its position, below 0 for a token that is skipped
   {
     const int t = first - LOOK + lane;
-    if (t >= 0 && t < a.ntokens && (a.positions == nullptr || a.positions[t] >= 0)) slot = a.slots[t];
-    if (slot < 0 || (slot >> shift) >= cache.num_pages) slot = -1;
+    if (t >= 0 && t < a.ntokens) {
+      slot = a.slots[t];
+      place = a.positions != nullptr ? a.positions[t] : 0;
+    }
+    if (slot < 0 || (slot >> shift) >= cache.num_pages || place < 0) slot = -1;
   }
-  // Is the token `by` places before this one in its run?
-  const int my_offset = static_cast<int>(slot) & (kBlock - 1);
-  bool leads = slot >= 0;
-  for (int by = 1; by < kBlock; ++by) {
-    const int64_t other = __shfl_up(static_cast<long long>(slot), by);
-    if (by <= my_offset && lane >= by && other == slot - by) leads = false;
-  }
-  uint64_t leaders = __ballot(leads && lane >= LOOK && lane < LOOK + p.window);
-
   const int u = lane % G, sub = lane / G;
   const bool live = u * 8 < d;
-  const bool turned = !is_v && u * 8 < rot;
+  const bool turned = TURN && !is_v && u * 8 < rot;
   const bool halves = turned && !a.interleaved;
   const int lo = !live ? 0 : halves ? 4 * u : 8 * u, hi = !live ? 4 : halves ? rot / 2 + 4 * u : 8 * u + 4;
   const void* src = is_v ? a.v : a.k;
   const int64_t token_step = is_v ? a.v_token : a.k_token;
   const int64_t head_at = head * (is_v ? a.v_head : a.k_head);
-  const bool normed = !is_v && a.k_weight != nullptr;
+  const bool normed = TURN && !is_v && a.k_weight != nullptr;
   double w[8];
   if (normed) {
     float f[8];
@@ -91,21 +94,23 @@ __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image
     for (int i = 0; i < 8; ++i) w[i] = f[i];
   }
 
-  while (leaders != 0) {
-    const int leader = __builtin_ctzll(leaders);
-    leaders &= leaders - 1;
-    const int t0 = first - LOOK + leader;
+  uint64_t left = __ballot(slot >= 0 && lane >= LOOK && lane < LOOK + p.window);
+  while (left != 0) {
+    const int leader = __builtin_ctzll(left);
     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(lane_value(static_cast<uint32_t>(slot >> 32), leader))) << 32 |
                         static_cast<uint32_t>(lane_value(static_cast<uint32_t>(slot), leader));
+    // The tokens of its run: those of the block that keep step with it.
+    const int64_t mine = static_cast<int64_t>(at);
+    const uint64_t run = __ballot((slot >> 4) == (mine >> 4) && slot - mine == lane - leader);
+    left &= ~run;
+    if (__builtin_ctzll(run) < leader) continue;  // an earlier token leads it
+    const int t0 = first - LOOK + leader;
     const int in_page = static_cast<int>(at) & (page - 1), o = in_page & (kBlock - 1);
     const int64_t owner = static_cast<int64_t>(at >> shift) * cache.heads + head;
     uint8_t* block = cache.data + (owner * 2 + is_v) * (static_cast<int64_t>(page) * d) + (in_page - o) * d;
     uint8_t* scale = cache.scales + owner * (2 * (page / kBlock)) + in_page / kBlock * 2 + is_v;
     const bool fresh = o == 0;
-    // The run's tokens, counted from its first; skipped ones may lie between.
-    const int behind = lane - leader;
-    const uint64_t members =
-        __ballot(behind >= 0 && behind < kBlock - o && slot == static_cast<int64_t>(at) + behind) >> leader;
+    const uint64_t members = run >> leader;  // counted from the first; skipped ones may lie between
     const int n = 64 - __builtin_clzll(members);
 
     typename Elem<DT>::Raw raw[TURNS][2];
@@ -124,16 +129,17 @@ __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image
       for (int i = 0; i < VECS; ++i) old[i] = reinterpret_cast<const u32x4*>(block)[min(lane + 64 * i, d - 1)];
     }
 
-    float x[TURNS][8];
+    float x[TURNS][8];  // only with TURN: else as loaded, and widened twice
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
       if (i * AT_ONCE >= n) break;
       const int row = i * AT_ONCE + sub;
-      Elem<DT>::widen(raw[i][0], x[i]), Elem<DT>::widen(raw[i][1], x[i] + 4);
-      if (normed || (!is_v && rot > 0)) {
+      float now[8];
+      Elem<DT>::widen(raw[i][0], now), Elem<DT>::widen(raw[i][1], now + 4);
+      if (TURN && (normed || (!is_v && rot > 0))) {
         // a skipped token's position is below 0: its row is computed and not used
-        const int pos = a.positions != nullptr ? max(a.positions[t0 + min(row, n - 1)], 0) : 0;
+        const int pos = max(__shfl(place, leader + min(row, n - 1)), 0);
         const bool beyond = rot > 0 && pos >= a.rows;
         double c[4], s[4], y[8];
         if (turned) {
@@ -144,25 +150,50 @@ __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image
 #pragma unroll
           for (int j = 0; j < 4; ++j) c[j] = f[j], s[j] = f[4 + j];
         }
-        norm_rotate<G>(x[i], y, normed, w, turned, c, s, a.interleaved, live, p.r.per_dim, a.eps);
+        norm_rotate<G>(now, y, normed, w, turned, c, s, a.interleaved, live, p.r.per_dim, a.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = beyond ? __uint_as_float(0x7FC00000u) : Elem<DT>::round(y[j]);
+        for (int j = 0; j < 8; ++j) now[j] = beyond ? __uint_as_float(0x7FC00000u) : Elem<DT>::round(y[j]);
       }
       if (live && (members >> row & 1) != 0)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t size = __float_as_uint(x[i][j]) & 0x7FFFFFFFu;
-          if (size < 0x7F800000u) most = max(most, size);
-        }
+        for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(now[j]) & 0x7FFFFFFFu);
+      if constexpr (TURN) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = now[j];
+      } else {
+        asm("" : "+v"(raw[i][0]), "+v"(raw[i][1]));
+      }
     }
     most = wave_max(most);
+    auto row_of = [&](int i) {
+      if constexpr (!TURN) Elem<DT>::widen(raw[i][0], x[i]), Elem<DT>::widen(raw[i][1], x[i] + 4);
+      return x[i];
+    };
+    const bool wild = most >= 0x7F800000u;
+    if (wild) {  // infinities and NaN have no part in the scale
+      most = 0;
+#pragma unroll
+      for (int i = 0; i < TURNS; ++i) {
+        if (i * AT_ONCE >= n) break;
+        const float* y = row_of(i);
+        if (live && (members >> (i * AT_ONCE + sub) & 1) != 0)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t size = __float_as_uint(y[j]) & 0x7FFFFFFFu;
+            if (size < 0x7F800000u) most = max(most, size);
+          }
+      }
+      most = wave_max(most);
+    }
     // most = m 2^E with 1 <= m < 2, and 448 = 1.75 * 2^8.
     const int need = static_cast<int>(most >> 23) - 8 + ((most & 0x7FFFFFu) > 0x600000u);
     uint32_t byte = static_cast<uint32_t>(min(max(need, kScale8Min), kScale8Max));
     const uint32_t had = limit8(uniform(static_cast<int>(old_byte)));
     if (!fresh) byte = max(byte, had);
     const bool grown = !fresh && byte > had;
-    const float inv = __uint_as_float((254u - byte) << 23);
+    // Else every value is at most 448 of the scale, and two conversions give a word.
+    const bool careful = wild || need > kScale8Max;
+    const float unit = __uint_as_float(byte << 23), inv = __uint_as_float((254u - byte) << 23);
     // 448 * 2^-30 is nothing beside the smallest code, 2^-9.
     const float ratio = byte - had < 30u ? __uint_as_float((127u - (byte - had)) << 23) : 0.0f;
 
@@ -186,7 +217,10 @@ __device__ __forceinline__ void put8(const Put8Args& p, int head, uint8_t* image
       if (i * AT_ONCE >= n) break;
       const int row = i * AT_ONCE + sub;
       if (!live || (members >> row & 1) == 0) continue;
-      const uint32_t c0 = encode8(x[i], inv), c1 = encode8(x[i] + 4, inv);
+      const float* y = row_of(i);
+      uint32_t c0, c1;
+      if (careful) c0 = encode8(y, inv), c1 = encode8(y + 4, inv);
+      else c0 = scaled8(y, unit), c1 = scaled8(y + 4, unit);
       const int token = o + row;
       if (!is_v) {
         *reinterpret_cast<uint32_t*>(image + token * d + lo) = c0;
@@ -220,7 +254,13 @@ __global__ __launch_bounds__(kRowThreads) void kv8_put(Put8Args p) {
     norm_rope_rows<DT, G, B, false, false>(p.r, nullptr);
     return;
   }
-  put8<DT, G>(p, by - p.r.q_runs, reinterpret_cast<uint8_t*>(image[threadIdx.x >> 6]));
+  put8<DT, G, true>(p, by - p.r.q_runs, reinterpret_cast<uint8_t*>(image[threadIdx.x >> 6]));
+}
+
+template <int DT, int G>
+__global__ __launch_bounds__(kRowThreads) void kv8_append(Put8Args p) {
+  __shared__ u32x4 image[kRowThreads / 64][G * 8];
+  put8<DT, G, false>(p, blockIdx.y, reinterpret_cast<uint8_t*>(image[threadIdx.x >> 6]));
 }
 
 struct Read8Args {
@@ -290,7 +330,8 @@ int launch_put(RowArgs& r, hipStream_t stream) {
   if (r.q_runs > 0) in_x = std::max(in_x, blocks(r.a.ntokens, kRowThreads / g));
   const dim3 grid(in_x, r.q_runs + heads), block(kRowThreads);
   void (*fn)(Put8Args);
-#define ARD_PICK(DT, G) fn = r.run == 1 ? kv8_put<DT, G, 1> : kv8_put<DT, G, 4>
+  const bool plain = r.q_runs == 0 && r.a.k_weight == nullptr && r.a.rot == 0;
+#define ARD_PICK(DT, G) fn = plain ? kv8_append<DT, G> : r.run == 1 ? kv8_put<DT, G, 1> : kv8_put<DT, G, 4>
   if (r.a.dtype == AR_BFLOAT16) {
     if (g == 8) ARD_PICK(DT_BF16, 8); else if (g == 16) ARD_PICK(DT_BF16, 16); else ARD_PICK(DT_BF16, 32);
   } else {
