@@ -119,16 +119,15 @@ struct Cost {
 template <int R>
 __device__ __forceinline__ Cost cost_of(const AttnArgs& args, int b) {
   const ar_kv4_attention_args& a = args.a;
-  Cost c = {0, 0, 0, 0, 1};
-  if (b < a.nreq) {
-    const int at = a.q_start[b], to = a.q_start[b + 1];
-    c.kv = max(a.kv_len[b], 0);
-    c.q0 = min(max(at, 0), a.ntokens);
-    c.m = max(min(to, a.ntokens), c.q0) - c.q0;  // an end may be any number
-    c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
-    const uint32_t seen = min(static_cast<uint32_t>(c.kv), args.most_seen);
-    c.span = static_cast<int>((seen + args.unit - 1) >> args.unit_shift) + args.job_units;
-  }
+  Cost c;
+  const int x = min(b, a.nreq - 1);  // read whether or not there is a request, so that several are read at once
+  const int at = a.q_start[x], to = a.q_start[x + 1];
+  c.kv = max(a.kv_len[x], 0);
+  c.q0 = min(max(at, 0), a.ntokens);
+  c.m = b < a.nreq ? max(min(to, a.ntokens), c.q0) - c.q0 : 0;  // an end may be any number
+  c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+  const uint32_t seen = min(static_cast<uint32_t>(c.kv), args.most_seen);
+  c.span = static_cast<int>((seen + args.unit - 1) >> args.unit_shift) + args.job_units;
   return c;
 }
 
@@ -140,23 +139,35 @@ struct Run {
   int per;   // units of a run
 };
 
+// Sums of the lanes' units, up to each and in all; false where these are 2^31 or more.
+__device__ __forceinline__ bool sums_of(uint32_t mine, uint32_t& upto, uint32_t& total) {
+  upto = wave_scan(mine);
+  total = lane_value(upto, 63);
+  // no sum of 64 wraps where the 64ths add up to less
+  return static_cast<uint32_t>(lane_value(wave_scan(mine >> 6), 63)) <= 0x7FFFFFFFu >> 6 && total <= 0x7FFFFFFFu;
+}
+
 // The run of workgroup `w`; false where there is none. Every wave computes it alone (lanes are
 // requests), with no barrier. This code runs once, from a cold instruction cache, before anything
 // else: it is kept short (32-bit sums; the host picks units large enough for them).
 template <int R>
 __device__ __forceinline__ bool find_run(const AttnArgs& args, int w, Run& run, Cost& mine) {
   const int lane = threadIdx.x & 63, heads = args.cache.heads;
-  uint32_t total = 0, longest = 0;
+  // A lane's requests, side by side.
+  const int each = (args.a.nreq + 63) >> 6;
+  uint32_t mine_units = 0, longest = 0;
   Cost c;
-  uint32_t upto;
-  for (int b = (args.a.nreq - 1) & ~63; b >= 0; b -= 64) {  // ends with the first requests at hand
-    c = cost_of<R>(args, b + lane);
-    upto = wave_scan(static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span));
-    total = __builtin_elementwise_add_sat(total, static_cast<uint32_t>(lane_value(upto, 63)));
-    longest = max(longest, wave_max(c.tiles > 0 ? c.span : 0));
+  auto units = [&] { return static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span); };
+#pragma unroll 4
+  for (int i = 0; i < each; ++i) {
+    c = cost_of<R>(args, lane * each + i);
+    mine_units = __builtin_elementwise_add_sat(mine_units, units());
+    longest = max(longest, c.tiles > 0 ? static_cast<uint32_t>(c.span) : 0u);
   }
-  // Only request starts that overlap reach this: nothing is done.
-  if (total > 0x7FFFFFFFu) return false;
+  uint32_t upto, total;
+  // Only request starts that overlap make too many: nothing is done.
+  if (!sums_of(mine_units, upto, total)) return false;
+  longest = wave_max(longest);
   // A unit for each wave at least, and no more parts of a job than units of a part: reading a part
   // back costs about what a unit does where few jobs leave the device idle.
   const int least = max((total + args.runs - 1) / args.runs,
@@ -165,15 +176,19 @@ __device__ __forceinline__ bool find_run(const AttnArgs& args, int w, Run& run, 
   if (static_cast<uint64_t>(w) * run.per >= total) return false;
   uint32_t from = w * run.per;
   run.left = min(run.per, static_cast<int>(total - from));
-  int b = 0;
-  while (__ballot(upto > from) == 0) {
-    from -= lane_value(upto, 63);
-    b += 64;
-    if (b >= args.a.nreq) return false;  // only if lengths change under the call
-    c = cost_of<R>(args, b + lane);
-    upto = wave_scan(static_cast<uint32_t>(c.tiles * heads) * static_cast<uint32_t>(c.span));
+  int who = __builtin_ctzll(__ballot(upto > from)), b = 0;
+  if (each > 1) {
+    from -= lane_value(upto - mine_units, who);
+    b = who * each;
+    for (;; b += 64) {
+      c = cost_of<R>(args, b + lane);
+      upto = wave_scan(units());
+      if (__ballot(upto > from) != 0) break;
+      from -= lane_value(upto, 63);
+      if (b + 64 >= args.a.nreq) return false;  // only if lengths change under the call
+    }
+    who = __builtin_ctzll(__ballot(upto > from));
   }
-  const int who = __builtin_ctzll(__ballot(upto > from));
   run.request = b + who;
   mine.q0 = lane_value(c.q0, who), mine.m = lane_value(c.m, who), mine.kv = lane_value(c.kv, who);
   mine.tiles = lane_value(c.tiles, who), mine.span = lane_value(c.span, who);

@@ -57,12 +57,13 @@ template <int R>
 __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
   const ar_kv4_attention_args& a = args.a;
   Series c = {0, 0, 0, 0, 1, 0.0, 0, 0};
-  if (b < a.nreq) {
-    const int at = a.q_start[b], to = a.q_start[b + 1];
-    c.kv = max(a.kv_len[b], 0);
-    c.q0 = min(max(at, 0), a.ntokens);
-    c.m = max(min(to, a.ntokens), c.q0) - c.q0;  // an end may be any number
-    c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+  const int x = min(b, a.nreq - 1);  // read whether or not there is a request, so that several are read at once
+  const int at = a.q_start[x], to = a.q_start[x + 1], kv = a.kv_len[x];
+  c.kv = max(kv, 0);
+  c.q0 = min(max(at, 0), a.ntokens);
+  c.m = b < a.nreq ? max(min(to, a.ntokens), c.q0) - c.q0 : 0;  // an end may be any number
+  c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+  if (c.tiles > 0) {
     const int end = min(c.kv, args.room);
     const int low = min(max(c.kv - c.m + min(args.tile_tokens, c.m), 0), end);
     auto units = [&](int seen) {
@@ -90,16 +91,19 @@ __device__ __forceinline__ Series wave_series(const Series& c) { return lane_ser
 template <int R, class ARGS>
 __device__ __forceinline__ bool find_rows(const ARGS& args, int w, Run& run, Series& mine, int& span) {
   const int lane = threadIdx.x & 63, heads = args.cache.heads;
-  uint32_t total = 0, longest = 0;
+  // A lane's requests, side by side.
+  const int each = (args.a.nreq + 63) >> 6;
+  uint32_t mine_units = 0, longest = 0;
   Series c;
-  uint32_t upto;
-  for (int b = (args.a.nreq - 1) & ~63; b >= 0; b -= 64) {
-    c = series_of<R>(args, b + lane);
-    upto = wave_scan(c.below(c.tiles) * heads);
-    longest = max(longest, wave_max(c.tiles > 0 ? c.below(c.tiles) - c.below(c.tiles - 1) : 0));
-    total = __builtin_elementwise_add_sat(total, static_cast<uint32_t>(lane_value(upto, 63)));
+#pragma unroll 4
+  for (int i = 0; i < each; ++i) {
+    c = series_of<R>(args, lane * each + i);
+    mine_units = __builtin_elementwise_add_sat(mine_units, c.below(c.tiles) * heads);
+    longest = max(longest, c.tiles > 0 ? c.below(c.tiles) - c.below(c.tiles - 1) : 0u);
   }
-  if (total > 0x7FFFFFFFu) return false;  // request starts that overlap
+  uint32_t upto, total;
+  if (!sums_of(mine_units, upto, total)) return false;  // request starts that overlap
+  longest = wave_max(longest);
   // Four units at least, a round of the workgroup; and parts of a job no shorter than makes reading
   // them back (one after the other, about 1.5 units each) as long as computing one.
   const int least = max((total + args.runs - 1) / args.runs,
@@ -108,15 +112,19 @@ __device__ __forceinline__ bool find_rows(const ARGS& args, int w, Run& run, Ser
   if (static_cast<uint64_t>(w) * run.per >= total) return false;
   uint32_t from = w * run.per;
   run.left = min(run.per, static_cast<int>(total - from));
-  int b = 0;
-  while (__ballot(upto > from) == 0) {
-    from -= lane_value(upto, 63);
-    b += 64;
-    if (b >= args.a.nreq) return false;  // only if lengths change under the call
-    c = series_of<R>(args, b + lane);
-    upto = wave_scan(c.below(c.tiles) * heads);
+  int who = __builtin_ctzll(__ballot(upto > from)), b = 0;
+  if (each > 1) {
+    from -= lane_value(upto - mine_units, who);
+    b = who * each;
+    for (;; b += 64) {
+      c = series_of<R>(args, b + lane);
+      upto = wave_scan(c.below(c.tiles) * heads);
+      if (__ballot(upto > from) != 0) break;
+      from -= lane_value(upto, 63);
+      if (b + 64 >= args.a.nreq) return false;  // only if lengths change under the call
+    }
+    who = __builtin_ctzll(__ballot(upto > from));
   }
-  const int who = __builtin_ctzll(__ballot(upto > from));
   run.request = b + who;
   from -= who > 0 ? lane_value(upto, who - 1) : 0;
   // What the place was found by, not read again: head and tile stay inside it whatever changes.

@@ -41,11 +41,12 @@ PromptKernel select_prompt_few(int dtype, int head_dim);  // a workgroup a tile 
 template <int R>
 __device__ __forceinline__ Series series_of(const PromptArgs& args, int b) {
   Series c = {0, 0, 0, 0, 1, 0.0, 0, 0};
-  if (b < args.a.nreq) {
-    const int at = args.a.q_start[b], to = args.a.q_start[b + 1];
-    c.q0 = min(max(at, 0), args.a.ntokens);
-    c.m = c.kv = max(min(to, args.a.ntokens), c.q0) - c.q0;  // an end may be any number
-    c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+  const int x = min(b, args.a.nreq - 1);
+  const int at = args.a.q_start[x], to = args.a.q_start[x + 1];
+  c.q0 = min(max(at, 0), args.a.ntokens);
+  c.m = c.kv = b < args.a.nreq ? max(min(to, args.a.ntokens), c.q0) - c.q0 : 0;  // an end may be any number
+  c.tiles = static_cast<int>((static_cast<uint32_t>(c.m) * static_cast<uint32_t>(args.group) + R - 1) / R);
+  if (c.tiles > 0) {
     auto units = [&](int seen) {
       return ((min(static_cast<uint32_t>(seen), args.most_seen) + args.unit - 1) >> args.unit_shift) + args.job_units;
     };

@@ -122,14 +122,15 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
   const int group = a->q_heads / h->heads;
   const int64_t all_rows = static_cast<int64_t>(a->ntokens) * group;
   if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  // The units of 32 tokens that a row sees if prompts are alike, and the kernel.
+  // The kernel, by the tiles, and the units of 32 tokens that their rows see, if prompts are alike.
   const int prompts = std::min(a->nreq, a->ntokens);
   int64_t sees = a->ntokens / prompts;
   sees = a->window > 0 ? std::min<int64_t>(sees / 2, a->window) : sees / 2;
   const int64_t units = sees / 32 + 1;
   PromptKernel k = select_prompt_few(a->dtype, h->head_dim);
   int64_t tiles = all_rows / k.rows + prompts, jobs = tiles * h->heads;
-  const bool few = jobs * (units + kFewJobUnits) <= kFewWork;
+  const int64_t alike = (all_rows / prompts + k.rows - 1) / k.rows * prompts * h->heads;
+  const bool few = alike * (units + kFewJobUnits) <= kFewWork;
   if (!few) {
     k = bf16 ? select_prompt_bf16(h->head_dim, true) : select_prompt_f32(h->head_dim);
     if (bf16 && all_rows * h->heads / k.rows * units < kLargeUnits * k.fill) k = select_prompt_bf16(h->head_dim, false);

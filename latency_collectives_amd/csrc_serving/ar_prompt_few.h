@@ -42,28 +42,37 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
   const ar_prompt_attention_args& a = args.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  // The tile: lanes are requests.
+  // The tile: a lane's requests lie side by side; where those are several, the lane's that has it then one a lane.
   uint32_t tile = blockIdx.x;
   PromptJob j;
   {
-    int b0 = 0;
-    uint32_t tiles, upto;
+    const int each = (a.nreq + 63) >> 6;
     int q0, m;
-    for (;; b0 += 64) {
-      if (b0 >= a.nreq) return;
-      q0 = m = 0;
-      if (b0 + lane < a.nreq) {
-        const int at = a.q_start[b0 + lane], to = a.q_start[b0 + lane + 1];
-        q0 = min(max(at, 0), a.ntokens);
-        m = max(min(to, a.ntokens), q0) - q0;
-      }
-      tiles = (static_cast<uint32_t>(m) * static_cast<uint32_t>(args.group) + R - 1) / R;
-      upto = wave_scan(tiles);
-      if (__ballot(upto > tile) != 0) break;
-      tile -= static_cast<uint32_t>(lane_value(upto, 63));
-    }
-    const int who = __builtin_ctzll(__ballot(upto > tile));
+    auto tiles_of = [&](int b) {
+      const int x = min(b, a.nreq - 1);
+      const int at = a.q_start[x], to = a.q_start[x + 1];
+      q0 = min(max(at, 0), a.ntokens);
+      m = b < a.nreq ? max(min(to, a.ntokens), q0) - q0 : 0;
+      return (static_cast<uint32_t>(m) * static_cast<uint32_t>(args.group) + R - 1) / R;
+    };
+    uint32_t tiles = 0;
+#pragma unroll 4
+    for (int i = 0; i < each; ++i) tiles += tiles_of(lane * each + i);
+    uint32_t upto = wave_scan(tiles);
+    if (__ballot(upto > tile) == 0) return;
+    int who = __builtin_ctzll(__ballot(upto > tile));
     tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
+    if (each > 1) {
+      for (int b = who * each;; b += 64) {
+        tiles = tiles_of(b + lane);
+        upto = wave_scan(tiles);
+        if (__ballot(upto > tile) != 0) break;
+        tile -= static_cast<uint32_t>(lane_value(upto, 63));
+        if (b + 64 >= a.nreq) return;
+      }
+      who = __builtin_ctzll(__ballot(upto > tile));
+      tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
+    }
     if (tile >= static_cast<uint32_t>(lane_value(tiles, who))) return;  // requests that overlap: their sum may have wrapped
     j.q0 = lane_value(q0, who);
     j.rows = lane_value(m, who) * args.group;
