@@ -52,7 +52,7 @@ AttnKernel select_attn_rows(int head_dim);
 struct AttnFormat {
   AttnKernel (*bf16)(int head_dim, int columns);
   AttnKernel (*f32)(int head_dim, int columns);
-  AttnKernel (*rows)(int head_dim);
+  AttnKernel (*rows)(int head_dim, bool brief);  // brief: rows that see few tokens
   int64_t (*page_bytes)(const ar_kv4* h);
   int64_t (*page_scales)(const ar_kv4* h);
 };

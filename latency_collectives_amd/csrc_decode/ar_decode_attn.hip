@@ -22,6 +22,9 @@ namespace {
 // tokens 53 for 29. Tables no wider than the step's longest request avoid it.
 constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
+// Units of 32 tokens that a row sees, below which tiles of many rows are brief (see the instances over the 8-bit cache).
+constexpr int64_t kBriefUnits = 96;
+
 // Tokens that a row of the table holds, below 2^31 by more than a wave looks ahead.
 int64_t room_of(const ar_kv4* h, const ar_kv4_attention_args* a) {
   return std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
@@ -38,12 +41,13 @@ Choice choose(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
   if (bf16 && each > 128) {
-    const ard::AttnKernel many = f.rows(h->head_dim);
     const int64_t tiles = (each + ard::kRowsTile - 1) / ard::kRowsTile * std::min(a->nreq, a->ntokens) * h->heads;
     const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
-    if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
+    if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits) {
+      const ard::AttnKernel many = f.rows(h->head_dim, units < kBriefUnits);
       return {many, many.rows, true};
+    }
   }
   // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
   // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and
@@ -90,8 +94,8 @@ ar_kv4* create_handle(const AttnFormat& f, int kv_heads, int head_dim, int page_
   for (int n = 1; n <= 2; ++n)
     for (const AttnKernel& k : {f.bf16(head_dim, n), f.f32(head_dim, n)})
       h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, 16 * n, head_dim));
-  const AttnKernel many = f.rows(head_dim);
-  h->work_bytes = std::max(h->work_bytes, part_bytes(many.fill, many.rows, head_dim));
+  for (const AttnKernel& k : {f.rows(head_dim, false), f.rows(head_dim, true)})
+    h->work_bytes = std::max(h->work_bytes, part_bytes(k.fill, k.rows, head_dim));
   int devices = 0;
   if (hipGetDeviceCount(&devices) != hipSuccess || devices == 0) {
     (void)hipGetLastError();
@@ -195,7 +199,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
 }
 
 static const AttnFormat kFormat4 = {
-    select_attn_bf16, select_attn_f32, select_attn_rows,
+    select_attn_bf16, select_attn_f32, [](int head_dim, bool) { return select_attn_rows(head_dim); },
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * h->page_size * h->head_dim; },
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32); }};
 
