@@ -252,10 +252,21 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void kv8_attention_rows(AttnArgs g
         if (more) load(h0 + 2 * SUB);
         uint32_t from = lds_base + buf * static_cast<uint32_t>(sizeof(Round));
         asm("" : "+v"(from));  // operands are offsets from it
+        // The first keys of a unit are read before the unit before it ends.
+        constexpr int EARLY = 2 * kSteps < 6 ? 2 * kSteps : 6;
+        u32x4 kf[EARLY];
+        auto read_key = [&](int sub, int i) { return lds_at<u32x4>(from + ((sub * 2 + (i & 1)) * kSteps + (i >> 1)) * 1024); };
+        auto read_first = [&](int sub) {
+#pragma unroll
+          for (int i = 0; i < EARLY; ++i) kf[i] = read_key(sub, i);
+        };
+        read_first(0);
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
           const int h = h0 + 2 * sub, t0 = t_begin + h * 16;
-          if (t0 < my_end && t0 + 32 > my_begin) {
+          if (t0 >= my_end || t0 + 32 <= my_begin) {
+            if (sub + 1 < SUB) read_first(sub + 1);
+          } else {
             const int both = static_cast<int>(seen >> (h - base)) & 3;  // the halves that have a page
             const bool masked = t0 + 32 > whole_end || t0 < whole_begin || both != 3;
             // Scores.
@@ -267,7 +278,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void kv8_attention_rows(AttnArgs g
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const bf16x8 kk = __builtin_bit_cast(bf16x8, lds_at<u32x4>(from + ((sub * 2 + u) * kSteps + i) * 1024));
+                const bf16x8 kk = __builtin_bit_cast(bf16x8, i * 2 + u < EARLY ? kf[i * 2 + u] : read_key(sub, i * 2 + u));
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) s[n][u] = mfma(kk, q[n][i], s[n][u]);
               }
@@ -319,6 +330,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void kv8_attention_rows(AttnArgs g
 #pragma unroll
             for (int j = 0; j < 4 * kSets; ++j) {
               if (j >= AHEAD) read_value(j);
+              if (j == 2 * kSets && sub + 1 < SUB) read_first(sub + 1);
 #pragma unroll
               for (int n = 0; n < NQ; ++n) acc[n][j >> 2][j & 3] = mfma(vv[j], pr[n], acc[n][j >> 2][j & 3]);
             }

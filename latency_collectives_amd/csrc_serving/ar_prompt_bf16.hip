@@ -133,10 +133,22 @@ struct PromptBf16 {
       uint32_t keys_from = key_at + turn * (2 * BYTES);
       asm("" : "+v"(keys_from));  // steps are offsets from it
       const uint32_t values_from = value_at + turn * (2 * BYTES);
+      // The first keys of a unit are read before the unit before it ends (128: six, 1535 -> 1500 us; four 1560).
+      constexpr int EARLY = 2 * kSteps < 6 ? 2 * kSteps : 6;
+      u32x4 kf[EARLY];
+      auto read_key = [&](int sub, int i) { return lds_at<u32x4>(keys_from + (sub * 2 * kSteps + (i & 1) * kSteps + (i >> 1)) * 1024); };
+      auto read_first = [&](int sub) {
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) kf[i] = read_key(sub, i);
+      };
+      read_first(0);
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub) {
         const int t0 = tr + sub * 32;
-        if (t0 >= see.my_end || t0 + 32 <= see.my_begin) continue;
+        if (t0 >= see.my_end || t0 + 32 <= see.my_begin) {
+          if (sub + 1 < SUB) read_first(sub + 1);
+          continue;
+        }
         // Scores.
         __builtin_amdgcn_s_setprio(1);
         f32x4 s[NQ][2];
@@ -146,7 +158,7 @@ struct PromptBf16 {
         for (int k = 0; k < kSteps; ++k)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const bf16x8 kk = __builtin_bit_cast(bf16x8, lds_at<u32x4>(keys_from + ((sub * 2 + u) * kSteps + k) * 1024));
+            const bf16x8 kk = __builtin_bit_cast(bf16x8, k * 2 + u < EARLY ? kf[k * 2 + u] : read_key(sub, k * 2 + u));
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[n][u] = mfma(kk, q[n][k], s[n][u]);
           }
@@ -198,6 +210,7 @@ struct PromptBf16 {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (t >= AHEAD) read_value(t);
+          if (t == kTiles / 2 && sub + 1 < SUB) read_first(sub + 1);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) o.acc[n][t] = mfma(__builtin_bit_cast(bf16x8, vv[t]), pr[n], o.acc[n][t]);
         }
@@ -216,7 +229,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void prompt_attention_bf16(PromptA
 // registers allow with 32 rows each. Four prompts of up to 8000 tokens, 16 query heads on 4, TFLOP/s:
 //   64    8 waves of 32 rows, twice a compute unit   755    (12, once: 685)
 //   96    12 of 32     900    (8: 763)
-//   128   12 of 32     999    (six prompts, 32 heads on 8; 8 of 32: 915, 8 of 16 twice: 790)
+//   128   12 of 32     1030   (six prompts, 32 heads on 8; 8 of 32: 915, 8 of 16 twice: 790)
 //   192   8 of 32      936    (12 of 16: 876)
 //   256   12 of 16     861    (8 of 16: 665)
 // Smaller calls, where a workgroup's own rows and the joins count for more: 8 waves of 16 rows, twice a compute unit.
