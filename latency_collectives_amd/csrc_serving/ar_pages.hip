@@ -391,15 +391,15 @@ int ar_pages_compact(const ar_pages_compact_args* a, void* stream) {
     return ar_fail(AR_EINVAL, "null request buffer");
   if (a->shares_out == a->shares || (a->nreq > 0 && a->table_width > 0 && a->table_out == a->table))
     return ar_fail(AR_EINVAL, "shares_out and table_out must not be the buffers that the call reads");
+  const size_t lds = ((static_cast<size_t>(a->num_pages) + 31) / 32 + 1) * 2 * sizeof(uint32_t);
+  if (lds > 65536)  // more than a kernel may use unasked
+    AR_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(pages_compact), hipFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(lds)));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (a->nreq > 0) {
     hipLaunchKernelGGL(pages_mark, dim3(std::min(a->nreq, 512)), dim3(kTableThreads), 0, s, *a, 1.0 / a->page_size);
     AR_HIP(hipGetLastError());
   }
-  const size_t lds = ((static_cast<size_t>(a->num_pages) + 31) / 32 + 1) * 2 * sizeof(uint32_t);
-  if (lds > 65536)  // more than a kernel may use unasked
-    AR_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(pages_compact), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(lds)));
   const int64_t work = a->num_pages + static_cast<int64_t>(a->nreq) * a->table_width;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(256, (work + 2 * kTableThreads - 1) / (2 * kTableThreads)));
   hipLaunchKernelGGL(pages_compact, dim3(grid), dim3(kTableThreads), lds, s, *a, 1.0 / a->page_size);
