@@ -81,6 +81,10 @@ __device__ __forceinline__ u32x2 lds_columns(uint32_t at) {
 
 __device__ __forceinline__ f32x4 mfma1(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
+// What a row's sums are worth when its maximum goes from m to `to`. Before the first token they are zeros, but for infinities
+// that were added already: times 0 they would become NaN.
+__device__ __forceinline__ float shrink(float m, float to) { return m == kLowest ? 1.0f : exp2_fast(m - to); }
+
 // A tile of rows of one request and head, and the tokens that this part of it sees.
 struct PromptJob {
   int q0, head, group, rows, row0, i0, rem0, i1;

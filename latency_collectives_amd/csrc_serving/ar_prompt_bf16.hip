@@ -192,7 +192,7 @@ struct PromptBf16 {
           top *= args.scale_log2;
           if (__any(top > o.m[n] + 8.0f)) {
             const float to = fmaxf(o.m[n], row_max(top));
-            const float f = exp2_fast(o.m[n] - to);
+            const float f = shrink(o.m[n], to);
             o.m[n] = to;
             o.l[n] *= f;
 #pragma unroll

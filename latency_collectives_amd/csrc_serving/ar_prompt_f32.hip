@@ -142,7 +142,7 @@ struct PromptF32 {
           for (int i = 1; i < 8; ++i) top = fmaxf(top, s[n][i >> 2][i & 3]);
           if (__any(top > o.m[n] + 8.0f)) {
             const float to = fmaxf(o.m[n], row_max(top));
-            const float f = exp2_fast(o.m[n] - to);
+            const float f = shrink(o.m[n], to);
             o.m[n] = to;
             o.l[n] *= f;
 #pragma unroll

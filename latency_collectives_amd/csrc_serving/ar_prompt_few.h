@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
     for (int x = 1; x < 4 * U; ++x) top = fmaxf(top, s[x >> 2][x & 3]);
     if (__any(top > m + 8.0f)) {
       const float to = fmaxf(m, row_max(top));
-      const float f = exp2_fast(m - to);
+      const float f = shrink(m, to);
       m = to;
       l *= f;
 #pragma unroll

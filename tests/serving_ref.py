@@ -191,3 +191,52 @@ def compact(kv_len, table, shares, page, nmoves):
         counts[to.get(p, p)] = shares[p]
     pad = [-1] * (nmoves - len(src))
     return out, counts, [n, len(shares)], src + pad, dst[:len(src)] + pad
+
+
+# ------------------------------------------------------------------ many rows, on any device
+
+
+def dense_attention(q, k, v, scale, window):
+    """(out, lse, bound, lse_bound) of one request in 64 bits, all rows of a head at once: q [m, hq, d] in its type
+    are the last m of the n positions of k, v [n, hkv, d] (values in any type). Definition and bounds are those of
+    decode_ref.attention; what is not finite among the values reaches the rows that see it."""
+    m, hq, d = q.shape
+    n, heads = k.shape[0], k.shape[1]
+    group, half, dev = hq // heads, R.HALF[q.dtype], q.device
+    out, bound = (torch.zeros(m, hq, d, dtype=torch.float64, device=dev) for _ in range(2))
+    lse, lse_bound = (torch.zeros(m, hq, dtype=torch.float64, device=dev) for _ in range(2))
+    pos = torch.arange(n - m, n, device=dev).repeat_interleave(group)[:, None]  # a row of s a token and head of the group
+    t = torch.arange(n, device=dev)[None]
+    see = t <= pos
+    if window > 0:
+        see &= t > pos - window
+    cnt = see.sum(-1, keepdim=True)
+    seen = see.double()
+    for h in range(heads):
+        x = q[:, h * group:(h + 1) * group].double().reshape(m * group, d)
+        kt = k[:, h].double().t().contiguous()
+        vv = v[:, h].double()
+        s = x @ kt * scale
+        delta = ((x.abs() @ kt.abs()) * (abs(scale) * d * 2.0 ** -23) + 4 * s.abs() * 2.0 ** -24)
+        delta = delta.masked_fill(~see, 0.0).amax(-1, keepdim=True)
+        s = s.masked_fill(~see, -math.inf)
+        top = s.amax(-1, keepdim=True)
+        nothing = cnt == 0
+        e = torch.exp(s - top.masked_fill(nothing, 0.0))
+        l = e.sum(-1, keepdim=True)
+        prob = e / l.masked_fill(nothing, 1.0)
+        finite = vv.nan_to_num(nan=0.0, posinf=0.0, neginf=0.0)
+        o = prob @ finite
+        rel = half + (cnt + 64) * 2.0 ** -23 + 2 * delta + 2.0 ** -21
+        b = rel * (prob @ finite.abs()) + half * o.abs() + cnt * 2.0 ** -118 * finite.abs().max()
+        if not bool(torch.isfinite(vv).all()):
+            up = seen @ (torch.isnan(vv) | (vv == math.inf)).double() > 0
+            down = seen @ (torch.isnan(vv) | (vv == -math.inf)).double() > 0
+            o = o + torch.where(up, math.inf, 0.0)
+            o = o - torch.where(down, math.inf, 0.0)
+        at = slice(h * group, (h + 1) * group)
+        out[:, at], bound[:, at] = o.view(m, group, d), b.view(m, group, d)
+        y = top + torch.log(l)
+        lse[:, at] = y.view(m, group)
+        lse_bound[:, at] = (delta + (cnt + 64) * 2.0 ** -23 + 4 * 2.0 ** -24 * y.abs()).view(m, group)
+    return out, lse, bound, lse_bound
