@@ -128,6 +128,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
   if (int rc = check_cache(a->data, a->scales, a->num_pages)) return rc;
   if (a->table_stride < a->table_width) return ar_fail(AR_EINVAL, "table_stride is below table_width");
   if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
+  if (a->nreq > INT32_MAX - 128) return ar_fail(AR_ETOOBIG, "too many requests");
   if (a->q == nullptr || a->out == nullptr) return ar_fail(AR_EINVAL, "null q or out");
   if (a->kv_len == nullptr || a->q_start == nullptr || (a->table_width > 0 && a->table == nullptr))
     return ar_fail(AR_EINVAL, "null request buffer");

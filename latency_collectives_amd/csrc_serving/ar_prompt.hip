@@ -107,6 +107,7 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
   const float scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
   if (!std::isfinite(scale_log2)) return ar_fail(AR_EINVAL, "scale must be finite in binary32, as its product with log2(e)");
   if (a->ntokens == 0 || a->nreq == 0) return AR_OK;
+  if (a->nreq > INT32_MAX - 128) return ar_fail(AR_ETOOBIG, "too many requests");
   if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr) return ar_fail(AR_EINVAL, "null q, k, v or out");
   if (a->q_start == nullptr) return ar_fail(AR_EINVAL, "null q_start");
   const bool bf16 = a->dtype == AR_BFLOAT16;

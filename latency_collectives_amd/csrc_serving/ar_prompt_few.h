@@ -59,7 +59,9 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
 #pragma unroll 4
     for (int i = 0; i < each; ++i) tiles += tiles_of(lane * each + i);
     uint32_t upto = wave_scan(tiles);
-    if (__ballot(upto > tile) == 0) return;
+    const uint32_t all = static_cast<uint32_t>(lane_value(upto, 63));
+    if (tile >= all) return;
+    tile = all - 1 - tile;  // a prompt's last tiles see most: they go first
     int who = __builtin_ctzll(__ballot(upto > tile));
     tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
     if (each > 1) {

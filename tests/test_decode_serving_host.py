@@ -392,3 +392,14 @@ def test_page_references_on_a_small_pool():
     t, shares, pool, src, dst = S.compact(kv, t, shares, 4, 4)
     assert pool == [4, 8] and src == [5, 6, -1, -1] and dst == [0, 1, -1, -1]
     assert t == [[-1] * 3, [0, 1, 3], [2, -1, -1], [-1] * 3]
+
+
+@pytest.mark.parametrize("nreq", [2 ** 31 - 1, 2 ** 31 - 128])
+def test_more_requests_than_are_counted(V, D, A, handle, nreq):
+    """The lanes' places past the last request are counted in 31 bits too."""
+    h = V.ar_prompt_create(2, 128)
+    assert V._entry.ar_prompt_attention(h, V._PROMPT.pack(*_prompt(nreq=nreq)), None) == A.AR_ETOOBIG
+    assert "requests" in A.ar_last_error()
+    V.ar_prompt_destroy(h)
+    assert V._entry.ar_kv8_attention(handle, D._ATTENTION.pack(*_attn(nreq=nreq)), None) == A.AR_ETOOBIG
+    assert "requests" in A.ar_last_error()
