@@ -8,15 +8,15 @@
 
 namespace ard {
 
-template <int D_, int NQ_, int WAVES_, int SUB_>
+template <int D_, int NQ_, int WAVES_>
 struct PromptF32 {
-  static constexpr int DT = DT_F32, D = D_, NQ = NQ_, N = 16, WAVES = WAVES_, SUB = SUB_;
+  static constexpr int DT = DT_F32, D = D_, NQ = NQ_, N = 16, WAVES = WAVES_;
   static constexpr int kSteps = D / 16, kSets = (D + 63) / 64, kTiles = 4 * kSets;
-  static constexpr int BYTES = SUB * 32 * D * 4;  // of a round's keys, or values
+  static constexpr int BYTES = 32 * D * 4;  // of a round's keys, or values
   static constexpr int kAll = BYTES / 1024, kItems = (kAll + WAVES - 1) / WAVES;
   struct Lds {
-    f32x4 keys[2][2 * SUB][kSteps][64];  // [round's turn][half]
-    f32x4 values[2][32 * SUB][D / 4];
+    f32x4 keys[2][2][kSteps][64];  // [round's turn][half]
+    f32x4 values[2][32][D / 4];
     uint32_t odd[2][WAVES];
   };
   struct Sums {
@@ -74,11 +74,11 @@ struct PromptF32 {
 
     int turn = 0;
 #pragma unroll 1
-    for (int tr = j.t_begin; tr < j.t_end; tr += SUB * 32, turn ^= 1) {
+    for (int t0 = j.t_begin; t0 < j.t_end; t0 += 32, turn ^= 1) {
       ar::wait_vm<0>();
       __syncthreads();  // the round has arrived, and the one before has been read
-      if (tr + SUB * 32 < j.t_end) load(j, tr + SUB * 32, turn ^ 1);
-      if (tr + SUB * 32 > see.odd_end || tr < see.odd_begin) {
+      if (t0 + 32 < j.t_end) load(j, t0 + 32, turn ^ 1);
+      if (t0 + 32 > see.odd_end || t0 < see.odd_begin) {
         const bool some = take_out<DT_F32, 64 * WAVES>(reinterpret_cast<uint8_t*>(lds.values[turn]), BYTES);
         if (lane == 0) lds.odd[turn][wave] = some;
         __syncthreads();
@@ -87,7 +87,7 @@ struct PromptF32 {
         for (int x = 0; x < WAVES; ++x) odd |= lds.odd[turn][x];
         if (uniform(odd) != 0) {
 #pragma unroll 1
-          for (int t = tr; t < min(tr + SUB * 32, j.t_end); ++t) {
+          for (int t = t0; t < min(t0 + 32, j.t_end); ++t) {
             int part_of = g;
             asm("" : "+v"(part_of));
 #pragma unroll
@@ -107,73 +107,69 @@ struct PromptF32 {
           }
         }
       }
-#pragma unroll 1
-      for (int sub = 0; sub < SUB; ++sub) {
-        const int t0 = tr + sub * 32;
-        if (t0 >= see.my_end || t0 + 32 <= see.my_begin) continue;
-        // Scores.
-        f32x4 s[NQ][2];
+      if (t0 >= see.my_end || t0 + 32 <= see.my_begin) continue;
+      // Scores.
+      f32x4 s[NQ][2];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+      for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const f32x4 k[2] = {lds.keys[turn][2 * sub][i][lane], lds.keys[turn][2 * sub + 1][i][lane]};
+      for (int i = 0; i < kSteps; ++i) {
+        const f32x4 k[2] = {lds.keys[turn][0][i][lane], lds.keys[turn][1][i][lane]};
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) s[n][u] = mfma1(k[u][x], q[n][i][x], s[n][u]);
+            for (int n = 0; n < NQ; ++n) s[n][u] = mfma1(k[u][x], q[n][i][x], s[n][u]);
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
+      if (t0 + 32 > see.whole_end || t0 < see.whole_begin) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!see.sees(n, t0 + (i >> 2) * 16 + g * 4 + (i & 3))) s[n][i >> 2][i & 3] = -INFINITY;
+      }
+      // Probabilities.
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float top = s[n][0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[n][i >> 2][i & 3]);
+        if (__any(top > o.m[n] + 8.0f)) {
+          const float to = fmaxf(o.m[n], row_max(top));
+          const float f = shrink(o.m[n], to);
+          o.m[n] = to;
+          o.l[n] *= f;
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) o.acc[n][t] *= f;
         }
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) s[n][0] *= args.scale_log2, s[n][1] *= args.scale_log2;
-        if (t0 + 32 > see.whole_end || t0 < see.whole_begin) {
+        for (int i = 0; i < 8; ++i) {
+          const float x = exp2_fast(s[n][i >> 2][i & 3] - o.m[n]);
+          o.l[n] += x;
+          s[n][i >> 2][i & 3] = x;
+        }
+      }
+      // Values: four elements of token 4 g + x % 4 of half x / 4 at a time.
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int e = 0; e < kSets; ++e) {
+          const f32x4 y = lds.values[turn][(x >> 2) * 16 + g * 4 + (x & 3)][min(e * 16 + c, D / 4 - 1)];
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (!see.sees(n, t0 + (i >> 2) * 16 + g * 4 + (i & 3))) s[n][i >> 2][i & 3] = -INFINITY;
+            for (int k = 0; k < 4; ++k) o.acc[n][4 * e + k] = mfma1(y[k], s[n][x >> 2][x & 3], o.acc[n][4 * e + k]);
         }
-        // Probabilities.
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float top = s[n][0][0];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) top = fmaxf(top, s[n][i >> 2][i & 3]);
-          if (__any(top > o.m[n] + 8.0f)) {
-            const float to = fmaxf(o.m[n], row_max(top));
-            const float f = shrink(o.m[n], to);
-            o.m[n] = to;
-            o.l[n] *= f;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) o.acc[n][t] *= f;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x = exp2_fast(s[n][i >> 2][i & 3] - o.m[n]);
-            o.l[n] += x;
-            s[n][i >> 2][i & 3] = x;
-          }
-        }
-        // Values: four elements of token 4 g + x % 4 of half x / 4 at a time.
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-#pragma unroll
-          for (int e = 0; e < kSets; ++e) {
-            const f32x4 y = lds.values[turn][sub * 32 + (x >> 2) * 16 + g * 4 + (x & 3)][min(e * 16 + c, D / 4 - 1)];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o.acc[n][4 * e + k] = mfma1(y[k], s[n][x >> 2][x & 3], o.acc[n][4 * e + k]);
-          }
-      }
     }
   }
 };
 
-template <int D, int NQ, int WAVES, int SUB, int OCC>
+template <int D, int NQ, int WAVES, int OCC>
 __global__ __launch_bounds__(64 * WAVES, OCC) void prompt_attention_f32(PromptArgs args) {
-  prompt_attention<PromptF32<D, NQ, WAVES, SUB>>(args);
+  prompt_attention<PromptF32<D, NQ, WAVES>>(args);
 }
 
 // Bound by the matrix units; waves cover for each other's exponentials and waits, so as many a SIMD as registers and LDS allow.
@@ -189,14 +185,14 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void prompt_attention_f32(PromptAr
 constexpr int kJobUnits = 2;
 
 PromptKernel select_prompt_f32(int head_dim) {
-// rows / 16 of a wave, waves of a workgroup, units of a round, workgroups of a compute unit
-#define ARD_CASE(D, NQ, WAVES, SUB, OCC) \
-  if (head_dim == D) return {prompt_attention_f32<D, NQ, WAVES, SUB, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES, kJobUnits}
-  ARD_CASE(64, 1, 4, 1, 4);
-  ARD_CASE(96, 1, 4, 1, 3);
-  ARD_CASE(128, 1, 8, 1, 2);
-  ARD_CASE(192, 1, 12, 1, 1);
-  ARD_CASE(256, 1, 8, 1, 1);
+// rows / 16 of a wave, waves of a workgroup, workgroups of a compute unit
+#define ARD_CASE(D, NQ, WAVES, OCC) \
+  if (head_dim == D) return {prompt_attention_f32<D, NQ, WAVES, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES, kJobUnits}
+  ARD_CASE(64, 1, 4, 4);
+  ARD_CASE(96, 1, 4, 3);
+  ARD_CASE(128, 1, 8, 2);
+  ARD_CASE(192, 1, 12, 1);
+  ARD_CASE(256, 1, 8, 1);
 #undef ARD_CASE
   return {nullptr, 0, 0, 0, 0};
 }
