@@ -15,6 +15,7 @@ struct AttnArgs {
   // The work split: units of `unit` tokens (32 << tile_shift), of which a row sees at most
   // most_seen; at most `runs` runs.
   uint32_t most_seen, unit, runs;
+  uint32_t full;      // there: tokens from which on a tile's window counts as full
   int unit_shift, tile_shift;
   int job_units;      // what starting and ending a job costs, in units
   float scale_log2;   // scale * log2(e); its absolute value for the kernel of many rows
@@ -53,6 +54,7 @@ struct AttnFormat {
   AttnKernel (*bf16)(int head_dim, int columns);
   AttnKernel (*f32)(int head_dim, int columns);
   AttnKernel (*rows)(int head_dim, bool brief);  // brief: rows that see few tokens
+  bool knows_windows;  // the split for many rows counts a full window for what it is
   int64_t (*page_bytes)(const ar_kv4* h);
   int64_t (*page_scales)(const ar_kv4* h);
 };

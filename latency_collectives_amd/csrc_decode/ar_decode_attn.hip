@@ -182,6 +182,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
   if (a->window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(a->window) + rows_per_tile / args.group + 33);
   args.room = static_cast<int>(room);
   args.most_seen = static_cast<uint32_t>(seen);
+  args.full = f.knows_windows ? args.most_seen : UINT32_MAX;
   args.unit_shift = 5;
   const auto span = [&] { return ((seen + (int64_t(1) << args.unit_shift) - 1) >> args.unit_shift) + k.job_units; };
   while (span() * jobs > 0x7FFFFFFF) ++args.unit_shift;
@@ -200,7 +201,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
 }
 
 static const AttnFormat kFormat4 = {
-    select_attn_bf16, select_attn_f32, [](int head_dim, bool) { return select_attn_rows(head_dim); },
+    select_attn_bf16, select_attn_f32, [](int head_dim, bool) { return select_attn_rows(head_dim); }, false,
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * h->page_size * h->head_dim; },
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32); }};
 

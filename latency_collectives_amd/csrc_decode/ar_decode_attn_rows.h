@@ -37,14 +37,15 @@ struct Series {
     const int s = min(r, knee);
     return static_cast<uint32_t>(s * (first + (s - 1) * half_slope)) + (r - s) * most;
   }
-  // Tile 0 sees `low` tokens, a tile R rows more than the one before, the last one `end`; units(t) of t tokens.
+  // Tile 0 sees `low` tokens, a tile R rows more than the one before, the last one `end`, a window is full at `full`;
+  // units(t) of t tokens.
   template <int R, class F>
-  __device__ void set(int low, int end, uint32_t most_seen, int group, F units) {
+  __device__ void set(int low, int end, uint32_t full, int group, F units) {
     first = units(low);
     knee = tiles, most = 0;
-    if (static_cast<uint32_t>(end) > most_seen) {
+    if (static_cast<uint32_t>(end) > full) {
       most = units(end);
-      const double rows = static_cast<uint32_t>(low) < most_seen ? static_cast<double>(most_seen - low) * group : 0.0;
+      const double rows = static_cast<uint32_t>(low) < full ? static_cast<double>(full - low) * group : 0.0;
       knee = static_cast<int>(min(rows / R + 1.0, static_cast<double>(tiles)));
       if (knee > 1) half_slope = static_cast<double>(most - first) / (2 * knee);
     } else if (tiles > 1) {
@@ -69,7 +70,7 @@ __device__ __forceinline__ Series series_of(const AttnArgs& args, int b) {
     auto units = [&](int seen) {
       return ((min(static_cast<uint32_t>(seen), args.most_seen) + args.unit - 1) >> args.unit_shift) + args.job_units;
     };
-    c.template set<R>(low, end, args.most_seen, args.group, units);
+    c.template set<R>(low, end, args.full, args.group, units);
   }
   return c;
 }

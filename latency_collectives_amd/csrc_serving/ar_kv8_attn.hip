@@ -8,7 +8,7 @@ AttnKernel select_attn8_bf16(int head_dim, int columns);
 AttnKernel select_attn8_f32(int head_dim, int columns);
 AttnKernel select_attn8_rows(int head_dim, bool brief);
 
-static const AttnFormat kFormat8 = {select_attn8_bf16, select_attn8_f32, select_attn8_rows,
+static const AttnFormat kFormat8 = {select_attn8_bf16, select_attn8_f32, select_attn8_rows, true,
                                     [](const ar_kv4* h) { return int64_t(2) * h->heads * h->page_size * h->head_dim; },
                                     [](const ar_kv4* h) { return int64_t(2) * h->heads * (h->page_size / kBlock); }};
 
