@@ -26,11 +26,13 @@ size_t prompt_part_bytes(const PromptKernel& k, int head_dim) {
 constexpr size_t kPromptArrived = 1024 * sizeof(uint32_t);  // at least every kernel's `fill`
 
 // Few rows: a workgroup for 16 rows and a kv head, which takes its units without a share for others. As long as jobs times
-// units, with kFewJobUnits for a job's start and end, stay below kFewWork. 8 query heads on one kv head of 128, us with
-// few rows' kernel and with the others: one prompt of 301 tokens 7.9 and 16.6, of 1000 (10 000) 20.3 and 28.1,
-// of 2000 (36 000) 57.5 and 41.8; 16 of up to 200, 32 heads on 8 (22 000), 38.9 and 28.9, of up to 100 (11 000), 19.3
-// and 16.2.
-constexpr int kFewJobUnits = 4, kFewWork = 10240;
+// units, with kFewJobUnits for a job's start and end, times head_dim stay below kFewWork, half as much again for
+// binary32, whose other kernels take longer to start. us with few rows' kernel and with the others, head of 128, 8 query heads
+// on one kv head: one prompt of 301 tokens 7.7 and 15.8, of 1000 (1.8 million) 20.7 and 35.6, of 1700 (4.2) 37.7 and 38.7;
+// 32 heads on 8: one of 500 (2.6) 22.8 and 24.9, of 800 (5.1) 42.8 and 30.5, 16 of up to 100 (3.0) 19.5 and 17.0. Head of
+// 64, 800 tokens (2.6) 23.2 and 22.2; of 256, 32 of up to 100 on 8 heads (2.9) 29.0 and 28.5, one of 1400 (6.1) 63.8 and 56.1.
+// Binary32, 128: 1700 tokens 76 and 102, 32 heads, 800 tokens 87 and 80.
+constexpr int kFewJobUnits = 12, kFewWork = 3 << 20;
 
 // Large tiles: where every workgroup gets so many units of its tile's rows. One prompt of 4000 tokens, 8 heads on one
 // of 128 (20): 74 us with large tiles, 64 without; eight of up to 2000, 32 on 8 (48): 163 and 174; one of 8000 (82): 151 and 168.
@@ -131,7 +133,7 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
   PromptKernel k = select_prompt_few(a->dtype, h->head_dim);
   int64_t tiles = all_rows / k.rows + prompts, jobs = tiles * h->heads;
   const int64_t alike = (all_rows / prompts + k.rows - 1) / k.rows * prompts * h->heads;
-  const bool few = alike * (units + kFewJobUnits) <= kFewWork;
+  const bool few = alike * (units + kFewJobUnits) * h->head_dim <= (bf16 ? kFewWork : kFewWork / 2 * 3);
   if (!few) {
     k = bf16 ? select_prompt_bf16(h->head_dim, true) : select_prompt_f32(h->head_dim);
     if (bf16 && all_rows * h->heads / k.rows * units < kLargeUnits * k.fill) k = select_prompt_bf16(h->head_dim, false);
