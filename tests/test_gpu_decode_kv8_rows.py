@@ -260,3 +260,47 @@ def test_tensors_that_want_gradients_are_refused(lc):
         lc.ar_kv8_append(h, k, k, slots, *cache)
     torch.cuda.synchronize()
     lc.ar_kv8_destroy(h)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_most_tokens_at_once(lc, dtype):
+    """As test_many_tokens_at_once, where a wave looks for runs in 16 tokens."""
+    g = torch.Generator().manual_seed(6)
+    heads, d, page, pages = 12, 64, 32, 100
+    pool = Pool(lc, pages, heads, d, page, dtype)
+    slots, at = [], 0
+    while at < pages * page - 120:
+        n = int(torch.randint(1, 100, (1,), generator=g))
+        slots += list(range(at, at + n)) + [-1] * int(torch.randint(0, 3, (1,), generator=g))
+        at = (at + n + 15) // 16 * 16
+    slots += [-1] * max(0, 65536 // (2 * heads) + 1 - len(slots))
+    assert len(slots) * heads * 2 >= 65536
+    k, v = rows(g, len(slots), heads, d, dtype)
+    pool.append(k, v, slots)
+    pool.check()
+    pool.done()
+
+
+@pytest.mark.parametrize("tokens", [1400, 11003])
+@pytest.mark.parametrize("prompts", [True, False])
+def test_many_tokens_joined_with_norm_and_rotation(lc, tokens, prompts):
+    """Runs of up to 16 tokens and of one, in windows of 4 and of 16: what the parts give, to the bit."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    heads, d, page = 3, 64, 64
+    h = lc.ar_kv8_create(heads, d, page)
+    pages = (tokens if prompts else tokens * 16) // page + 2
+    q, k, v = (torch.randn(tokens, n, d, generator=g, device="cuda").bfloat16() for n in (6, heads, heads))
+    at = torch.arange(tokens, device="cuda") if prompts else torch.randperm(tokens, generator=g, device="cuda") * 16 + 5
+    positions = (torch.arange(tokens, device="cuda") % 500).int()
+    positions[torch.randperm(tokens, generator=g, device="cuda")[:tokens // 20]] = -1
+    cs = torch.randn(500, d, generator=g, device="cuda")
+    w = torch.randn(d, generator=g, device="cuda").bfloat16()
+    one, two = (lc.ar_kv8_cache(h, pages) for _ in range(2))
+    q1, q2, k2 = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(k)
+    lc.ar_kv8_norm_rope_append(h, q, k, v, q1, positions, cs, at, *one, w, w)
+    lc.ar_qk_norm_rope(q, k, q2, k2, positions, cs, w, w)
+    lc.ar_kv8_append(h, k2, v, torch.where(positions < 0, -1, at), *two)
+    torch.cuda.synchronize()
+    assert torch.equal(q1, q2) and torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    assert (one[1] != 0).any()
+    lc.ar_kv8_destroy(h)
