@@ -3,14 +3,15 @@
 //
 // Such a call is bound by latency: what stands one after the other is the launch, the starts, the first keys and values, a
 // wave's units, the join. So there is no split between workgroups and no workspace; a workgroup finds its tile by one scan
-// over the starts; a wave takes every fourth unit, straight from memory into the operands' registers (a unit ahead), and
-// the four sums meet in LDS.
+// over the starts; a wave takes every fourth unit, straight from memory into the operands' registers, and the four sums
+// meet in LDS. A unit's registers take the next one's keys and values as soon as they have been used: with a second set of
+// them a compute unit held fewer workgroups (head of 192: 20.0 us for seven prompts of up to 301 tokens, 14.0 so; 500 of up to 5,
+// head of 128, 9.4 and 6.6).
 //
 //   bfloat16   a unit is 32 tokens; values: four elements of eight tokens a lane, tokens paired by one permute a word
 //   binary32   a unit is 16 tokens; values: four elements of a token a lane, as the 16x16x4 products take them
 //
-// One prompt of 301 tokens, 8 query heads on one kv head of 128, bfloat16: 7.9 us, 16.6 us by the kernels for many rows
-// (binary32: 16.6 and 24.9).
+// One prompt of 301 tokens, 8 query heads on one kv head of 128, bfloat16: 7.7 us, 15.8 by the kernels for many rows.
 #pragma once
 
 #include "ar_prompt.h"
@@ -27,8 +28,15 @@ struct FewUnit {  // a lane's share of a unit, as loaded
   V v[4 * U][kSets];  // [u * 4 + i]: token 16 u + 4 g + i
 };
 
+// At voffset + soffset of the buffer, the second the same for all lanes; both count for its end.
+template <class T>
+__device__ __forceinline__ T row_at(ar::rsrc_t from, uint32_t voffset, uint32_t soffset) {
+  if constexpr (sizeof(T) == 16) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(from, voffset, soffset, 0));
+  else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b64(from, voffset, soffset, 0));
+}
+
 template <int DT, int D>
-__global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attention_few(PromptArgs args) {
+__global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 3 : 4) void prompt_attention_few(PromptArgs args) {
   constexpr int R = 16;
   constexpr bool kBf16 = DT == DT_BF16;
   constexpr int ES = kBf16 ? 2 : 4, NC = D / 8;
@@ -40,8 +48,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
   __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
 
   const ar_prompt_attention_args& a = args.a;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int c = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   // The tile: a lane's requests lie side by side; where those are several, the lane's that has it then one a lane.
   uint32_t tile = blockIdx.x;
   PromptJob j;
@@ -89,26 +96,29 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
   const uint8_t* keys = static_cast<const uint8_t*>(a.k) + j.q0 * j.k_row + j.head * a.k_head * ES;
   const uint8_t* vals = static_cast<const uint8_t*>(a.v) + j.q0 * j.v_row + j.head * a.v_head * ES;
 
-  const uint32_t k_off = c * static_cast<uint32_t>(j.k_row) + g * 16;
-  auto load = [&](int t0, Unit& x) {
-    const ar::rsrc_t kr = rows_from(keys, j.k_row, t0, end, D * ES), vr = rows_from(vals, j.v_row, t0, end, D * ES);
+  // Places of a lane, and what is the same for all of them beside.
+  const uint32_t k_row = static_cast<uint32_t>(j.k_row), v_row = static_cast<uint32_t>(j.v_row);
+  const uint32_t k_off = c * k_row + g * 16;
+  uint32_t v_off[kSets];
+#pragma unroll
+  for (int e = 0; e < kSets; ++e) v_off[e] = g * 4 * v_row + min(e * 64 + c * 4, D - 4) * ES;  // lanes beyond the row repeat its last elements
+  auto load_keys = [&](int t0, Unit& x) {
+    const ar::rsrc_t kr = rows_from(keys, j.k_row, t0, end, D * ES);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        x.k[u][s] = ar::ld16<ar::kPlain>(kr, k_off + u * 16 * static_cast<uint32_t>(j.k_row) + s * 64);
+      for (int s = 0; s < kSteps; ++s) x.k[u][s] = row_at<u32x4>(kr, k_off, u * 16 * k_row + s * 64);
+  };
+  auto load_values = [&](int t0, Unit& x) {
+    const ar::rsrc_t vr = rows_from(vals, j.v_row, t0, end, D * ES);
 #pragma unroll
     for (int t = 0; t < 4 * U; ++t)
 #pragma unroll
-      for (int e = 0; e < kSets; ++e) {  // lanes beyond the row repeat its last elements
-        const uint32_t at = ((t >> 2) * 16 + g * 4 + (t & 3)) * static_cast<uint32_t>(j.v_row) + min(e * 64 + c * 4, D - 4) * ES;
-        if constexpr (kBf16) x.v[t][e] = ar::ld8<ar::kPlain>(vr, at);
-        else x.v[t][e] = ar::ld16<ar::kPlain>(vr, at);
-      }
+      for (int e = 0; e < kSets; ++e) x.v[t][e] = row_at<typename Unit::V>(vr, v_off[e], ((t >> 2) * 16 + (t & 3)) * v_row);
   };
-  Unit now, next;
+  Unit now;
   int t0 = begin + wave * T;
-  if (t0 < end) load(t0, now);
+  if (t0 < end) load_keys(t0, now), load_values(t0, now);
 
   // The rows, the same for every wave.
   const int r = min(c, last), i = j.i0 + j.token_of(r);
@@ -136,7 +146,6 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
 
 #pragma unroll 1
   for (; t0 < end; t0 += T * kAttnWaves) {
-    if (t0 + T * kAttnWaves < end) load(t0 + T * kAttnWaves, next);
     // Scores.
     f32x4 s[U];
 #pragma unroll
@@ -155,8 +164,10 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
       }
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] *= args.scale_log2;
+    // The next unit's keys into their registers, as its values below.
+    if (t0 + T * kAttnWaves < end) load_keys(t0 + T * kAttnWaves, now);
     auto sees = [&](int u, int x) {
-      const int t = t0 + u * 16 + g * 4 + x;
+      const int t = t0 + u * 16 + (thread_here() >> 4 & 3) * 4 + x;
       return t < hi && t >= lo;
     };
     // bfloat16: the operand of elements 64 e + 4 c + k.
@@ -175,7 +186,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
 #pragma unroll
       for (int x = 0; x < 4 * U; ++x)
         if (!sees(x >> 2, x & 3)) s[x >> 2][x & 3] = -INFINITY;
-      // Infinities and NaN that not all rows see: added by products of their own for the rows that do.
+      // Infinities and NaN that not all rows see: added for the rows that do, and taken out.
       bool odd = false;
 #pragma unroll
       for (int t = 0; t < 4 * U; ++t)
@@ -187,30 +198,29 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
             odd |= kBf16 ? finite_only(w) != w : (w & 0x7F800000u) == 0x7F800000u;
           }
       if (__any(odd)) {
-        bf16x8 visible;
-        if constexpr (kBf16) visible = visible_of(sees);
+#pragma unroll 1
+        for (int t = t0; t < min(t0 + T, end); ++t) {
+          if (t >= hi || t < lo) continue;
+          const int from = (thread_here() >> 4 & 3) * 16;
 #pragma unroll
-        for (int e = 0; e < kSets; ++e)
+          for (int e = 0; e < kSets; ++e) {
+            if (64 * e + from >= D) continue;
+            const u32x4* p = reinterpret_cast<const u32x4*>(vals + t * j.v_row + (64 * e + from) * ES);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (kBf16) {
-              add_infinite(value_of(e, k), visible, acc[e][k]);
-            } else {
-              f32x4 up = {0, 0, 0, 0}, down = {0, 0, 0, 0};
-#pragma unroll
-              for (int t = 0; t < 4 * U; ++t) {
-                const float y = __uint_as_float(now.v[t][e][k]), one = sees(t >> 2, t & 3) ? 1.0f : 0.0f;
-                up = mfma1(y <= 3.4028235e38f ? 0.0f : 1.0f, one, up);
-                down = mfma1(y >= -3.4028235e38f ? 0.0f : 1.0f, one, down);
+            for (int x = 0; x < 4; ++x) {
+              f32x4 y;
+              if constexpr (kBf16) {
+                const u32x2 w = reinterpret_cast<const u32x2*>(p)[x];
+                y = f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+              } else {
+                y = __builtin_bit_cast(f32x4, p[x]);
               }
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                if (up[x] > 0.0f) acc[e][k][x] += INFINITY;
-                if (down[x] > 0.0f) acc[e][k][x] -= INFINITY;
-              }
+              for (int k = 0; k < 4; ++k)
+                if (!(fabsf(y[k]) < INFINITY)) acc[e][k][x] += y[k];
             }
-            __builtin_amdgcn_sched_barrier(0);
           }
+        }
 #pragma unroll
         for (int t = 0; t < 4 * U; ++t)
 #pragma unroll
@@ -258,45 +268,48 @@ __global__ __launch_bounds__(kAttnThreads, D > 128 ? 1 : 2) void prompt_attentio
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[e][k] = mfma1(__uint_as_float(now.v[t][e][k]), p[t], acc[e][k]);
     }
-    now = next;
+    if (t0 + T * kAttnWaves < end) load_values(t0 + T * kAttnWaves, now);
   }
 
-  // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
-  l = row_sum(l);
-  if (g == 0) stat_m[wave][c] = m, stat_l[wave][c] = l;
-  __syncthreads();
-  float most = stat_m[0][c];
+  {
+    // Join the waves: every wave's sums in units of the workgroup's maximum, added through LDS.
+    const int tid = thread_here(), c = tid & 15, g = tid >> 4 & 3;
+    l = row_sum(l);
+    if (g == 0) stat_m[wave][c] = m, stat_l[wave][c] = l;
+    __syncthreads();
+    float most = stat_m[0][c];
 #pragma unroll
-  for (int x = 1; x < kAttnWaves; ++x) most = fmaxf(most, stat_m[x][c]);
-  const float f = exp2_fast(m - most);
-  float* mine = join + (wave * 16 + c) * kPitch + g * 16;
+    for (int x = 1; x < kAttnWaves; ++x) most = fmaxf(most, stat_m[x][c]);
+    const float f = exp2_fast(m - most);
+    float* mine = join + (wave * 16 + c) * kPitch + g * 16;
 #pragma unroll
-  for (int e = 0; e < kSets; ++e)
+    for (int e = 0; e < kSets; ++e)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (e * 64 + g * 16 + x * 4 >= D) continue;
-      f32x4 v;
+      for (int x = 0; x < 4; ++x) {
+        if (e * 64 + g * 16 + x * 4 >= D) continue;
+        f32x4 v;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = acc[e][k][x] * f;
-      *reinterpret_cast<f32x4*>(mine + e * 64 + x * 4) = v;
+        for (int k = 0; k < 4; ++k) v[k] = acc[e][k][x] * f;
+        *reinterpret_cast<f32x4*>(mine + e * 64 + x * 4) = v;
+      }
+    __syncthreads();
+    for (int x = tid; x < 16 * NC; x += kAttnThreads) {
+      const int row = x / NC, seg = x - row * NC;
+      if (row > last) continue;
+      f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+      float rm = stat_m[0][row], rl = 0.0f;
+#pragma unroll
+      for (int y = 1; y < kAttnWaves; ++y) rm = fmaxf(rm, stat_m[y][row]);
+#pragma unroll
+      for (int y = 0; y < kAttnWaves; ++y) {
+        const float* from = join + (y * 16 + row) * kPitch + seg * 8;
+        o0 += *reinterpret_cast<const f32x4*>(from);
+        o1 += *reinterpret_cast<const f32x4*>(from + 4);
+        rl += stat_l[y][row] * exp2_fast(stat_m[y][row] - rm);
+      }
+      const int token = j.i0 + j.token_of(row);
+      finish_row<DT>(a, j.q0 + token, j.head * j.group + j.row0 + row - token * j.group, seg, o0, o1, rm, rl);
     }
-  __syncthreads();
-  for (int x = tid; x < 16 * NC; x += kAttnThreads) {
-    const int row = x / NC, seg = x - row * NC;
-    if (row > last) continue;
-    f32x4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
-    float rm = stat_m[0][row], rl = 0.0f;
-#pragma unroll
-    for (int y = 1; y < kAttnWaves; ++y) rm = fmaxf(rm, stat_m[y][row]);
-#pragma unroll
-    for (int y = 0; y < kAttnWaves; ++y) {
-      const float* from = join + (y * 16 + row) * kPitch + seg * 8;
-      o0 += *reinterpret_cast<const f32x4*>(from);
-      o1 += *reinterpret_cast<const f32x4*>(from + 4);
-      rl += stat_l[y][row] * exp2_fast(stat_m[y][row] - rm);
-    }
-    const int token = j.i0 + j.token_of(row);
-    finish_row<DT>(a, j.q0 + token, j.head * j.group + j.row0 + row - token * j.group, seg, o0, o1, rm, rl);
   }
 }
 
