@@ -210,7 +210,9 @@ int ar_pages_copy(const ar_pages_copy_args* a, void* stream);
  * ar_kv4_attention: probabilities are rounded to bfloat16 for AR_BFLOAT16; AR_FLOAT32 calls multiply in
  * binary32. A NaN or infinity of a masked place does not reach a result. Starts are taken between 0 and
  * ntokens; tokens that no request covers keep their rows of out and lse, those of requests that overlap are
- * undefined. q, k, v and out are 16-byte aligned, their strides multiples of 16 bytes.
+ * undefined and the others' are not (but overlaps that make 256 times the tokens, or 2^31 units of a tile's rows and
+ * 32 tokens, may leave every row as it was). q, k, v and out are 16-byte aligned, their strides multiples of
+ * 16 bytes, those of tokens of k and v 2^23 bytes at most.
  *
  * ar_prompt_create: a handle with the workspace (partial results), for kv_heads 1..1024 and head_dim 64,
  * 96, 128, 192 or 256. Calls on one handle are issued in order on one stream, on the GPU that was

@@ -159,6 +159,7 @@ int ar_prompt_attention(ar_prompt* h, const ar_prompt_attention_args* a, void* s
     args.scale_log2 = std::max(std::fabs(args.scale_log2), 1e-38f);
   }
   if (few) {
+    args.runs = static_cast<uint32_t>(tiles);
     hipLaunchKernelGGL(k.fn, dim3(static_cast<unsigned>(tiles), h->heads), dim3(k.threads), 0, static_cast<hipStream_t>(stream), args);
     AR_HIP(hipGetLastError());
     return AR_OK;

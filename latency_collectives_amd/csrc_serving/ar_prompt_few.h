@@ -35,8 +35,10 @@ __device__ __forceinline__ T row_at(ar::rsrc_t from, uint32_t voffset, uint32_t 
   else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b64(from, voffset, soffset, 0));
 }
 
+// Tile `x` from the last; tells whether there is one a grid further, which takes requests that overlap: the grid (`runs`)
+// has the tiles of tokens that each belong to one request.
 template <int DT, int D>
-__global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 3 : 4) void prompt_attention_few(PromptArgs args) {
+__device__ __forceinline__ bool few_tile(const PromptArgs& args, uint32_t x) {
   constexpr int R = 16;
   constexpr bool kBf16 = DT == DT_BF16;
   constexpr int ES = kBf16 ? 2 : 4, NC = D / 8;
@@ -46,11 +48,12 @@ __global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 
   constexpr int kPitch = D + 4;  // LDS row: 16 rows' 16-byte accesses fall into different banks
   __shared__ float join[kAttnWaves * 16 * kPitch];
   __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
+  __shared__ uint32_t tiles_in_all;
 
   const ar_prompt_attention_args& a = args.a;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
+  const int lane = thread_here() & 63, wave = uniform(thread_here() >> 6), c = lane & 15, g = lane >> 4;
   // The tile: a lane's requests lie side by side; where those are several, the lane's that has it then one a lane.
-  uint32_t tile = blockIdx.x;
+  uint32_t tile;
   PromptJob j;
   {
     const int each = (a.nreq + 63) >> 6;
@@ -64,11 +67,12 @@ __global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 
     };
     uint32_t tiles = 0;
 #pragma unroll 4
-    for (int i = 0; i < each; ++i) tiles += tiles_of(lane * each + i);
+    for (int i = 0; i < each; ++i) tiles = __builtin_elementwise_add_sat(tiles, tiles_of(lane * each + i));
     uint32_t upto = wave_scan(tiles);
     const uint32_t all = static_cast<uint32_t>(lane_value(upto, 63));
-    if (tile >= all) return;
-    tile = all - 1 - tile;  // a prompt's last tiles see most: they go first
+    if (x >= all || all >> 8 > args.runs) return false;  // an end to what overlaps can ask for
+    if (threadIdx.x == 0) tiles_in_all = all;  // kept there: the loop needs the registers
+    tile = all - 1 - x;  // a prompt's last tiles see most: they go first
     int who = __builtin_ctzll(__ballot(upto > tile));
     tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
     if (each > 1) {
@@ -77,12 +81,11 @@ __global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 
         upto = wave_scan(tiles);
         if (__ballot(upto > tile) != 0) break;
         tile -= static_cast<uint32_t>(lane_value(upto, 63));
-        if (b + 64 >= a.nreq) return;
+        if (b + 64 >= a.nreq) return false;  // only if starts change under the call
       }
       who = __builtin_ctzll(__ballot(upto > tile));
       tile -= static_cast<uint32_t>(lane_value(upto - tiles, who));
     }
-    if (tile >= static_cast<uint32_t>(lane_value(tiles, who))) return;  // requests that overlap: their sum may have wrapped
     j.q0 = lane_value(q0, who);
     j.rows = lane_value(m, who) * args.group;
   }
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 
 #pragma unroll
   for (int e = 0; e < kSets; ++e)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[e][k] = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < 4; ++k) acc[e][k] = zeros_here();
 
 #pragma unroll 1
   for (; t0 < end; t0 += T * kAttnWaves) {
@@ -310,6 +313,17 @@ __global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 
       const int token = j.i0 + j.token_of(row);
       finish_row<DT>(a, j.q0 + token, j.head * j.group + j.row0 + row - token * j.group, seg, o0, o1, rm, rl);
     }
+  }
+  return uniform(tiles_in_all) - x > args_here<PromptArgs>().runs;
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kAttnThreads, D > 192 ? 1 : D > 128 ? 2 : D > 64 ? 3 : 4) void prompt_attention_few(PromptArgs args) {
+  // The first tile's code is its own: in the loop's it took 0.3 us longer (registers, a cold cache of instructions).
+  if (__builtin_expect(!few_tile<DT, D>(args, blockIdx.x), 1)) return;
+  for (uint32_t x = blockIdx.x + args.runs;; x += args.runs) {
+    __syncthreads();  // the next tile uses the same LDS
+    if (!few_tile<DT, D>(args_here<PromptArgs>(), x)) return;
   }
 }
 
