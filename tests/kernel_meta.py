@@ -42,7 +42,9 @@ def tools_available() -> bool:
 def code_objects(lib: str, workdir: str) -> list:
     """Unbundle every translation unit's gfx950 code object out of `lib` into `workdir`."""
     fat = os.path.join(workdir, "fat.bin")
-    subprocess.run(["objcopy", "--dump-section", f".hip_fatbin={fat}", lib], check=True)
+    # an output of its own: without one objcopy writes the library anew, under whoever has it mapped
+    subprocess.run(["objcopy", "--dump-section", f".hip_fatbin={fat}", lib, os.path.join(workdir, "copy")],
+                   check=True)
     # one offload bundle per translation unit, concatenated (each starts with the magic string)
     magic = b"__CLANG_OFFLOAD_BUNDLE__"
     raw = open(fat, "rb").read()
