@@ -181,7 +181,7 @@ def main(argv=None) -> None:
     a = p.parse_args(argv)
     prompts = [1 + (a.prompt - 1) * (i + 1) // a.requests for i in range(a.requests)]
     rows = a.requests * a.samples
-    run = DecodeStep(a.ranks, a.layers, rows, a.prompt + a.steps, max(sum(prompts), rows), bits=a.bits)
+    run = DecodeStep(a.ranks, a.layers, rows, a.prompt + a.steps + (a.samples > 1), max(sum(prompts), rows), bits=a.bits)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
 
@@ -208,7 +208,16 @@ def main(argv=None) -> None:
     if int(run.refusals.sum()) or run.lengths.tolist() != [n + a.steps for n in prompts] * a.samples:
         raise AssertionError("a request was refused")
     if a.samples > 1:
-        run.release(torch.arange(rows, dtype=torch.int32, device="cuda"))
+        # the last copies leave, the pages in use move together, the others go on
+        stay = rows - a.requests
+        run.release(torch.arange(stay, rows, dtype=torch.int32, device="cuda"))
+        run.compact()
+        xs = run(x[:stay], (torch.arange(rows, device="cuda") < stay).int())
+        if any(not torch.equal(y, xs[0]) for y in xs) or not torch.isfinite(xs[0].float()).all():
+            raise AssertionError("the ranks' results differ after the pages have moved")
+        if run.lengths.tolist() != [n + a.steps + 1 for n in prompts] * (a.samples - 1) + [0] * a.requests:
+            raise AssertionError("a request was refused")
+        run.release(torch.arange(stay, dtype=torch.int32, device="cuda"))
         if int(run.pool[run.turn][0]) or int(run.shares.abs().sum()):
             raise AssertionError("pages were not given back")
     run.close()

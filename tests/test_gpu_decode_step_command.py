@@ -1,0 +1,46 @@
+"""latency_collectives_amd.decode_step as a command: what its texts say that it runs, it runs."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The names of the package's calls, in order."""
+    import latency_collectives_amd as lc
+    from latency_collectives_amd import decode_step
+
+    seen = []
+
+    class Spy:
+        def __getattr__(self, name):
+            inner = getattr(lc, name)
+            if not callable(inner):
+                return inner
+
+            def call(*a, **k):
+                seen.append(name)
+                return inner(*a, **k)
+
+            return call
+
+    monkeypatch.setattr(decode_step, "lc", Spy())
+    return seen
+
+
+def run(*extra):
+    from latency_collectives_amd import decode_step
+
+    decode_step.main(["--ranks", "2", "--layers", "1", "--requests", "5", "--prompt", "70", "--steps", "3", *extra])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bits", ["4", "8"])
+def test_samples_are_forked_freed_and_moved_together(calls, bits):
+    run("--bits", bits, "--samples", "3")
+    pages = [n for n in calls if n.startswith("ar_pages_") and n != "ar_pages_scratch"]
+    assert pages == ["ar_pages_fork", "ar_pages_copy", "ar_pages_free", "ar_pages_compact", "ar_pages_copy", "ar_pages_free"]
+    # a step after the pages have moved
+    assert f"ar_kv{bits}_attention" in calls[calls.index("ar_pages_compact"):]
