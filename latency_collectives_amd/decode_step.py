@@ -59,7 +59,7 @@ class DecodeStep:
             for name in ("create", "cache", "append", "norm_rope_append", "attention", "destroy"))
         self.kv = create(self.hkv, head_dim, page)
         self.cache = [[cache(self.kv, pages) for _ in range(ranks)] for _ in range(layers)]
-        self.prompt = lc.ar_prompt_create(self.hkv, head_dim)
+        self.prompt = None  # made with the first step of packed prompts
         self.sum = lc.ar_create(ranks, max_tokens * hidden * 2, lc.AR_BFLOAT16)
 
         def i32(*shape):
@@ -144,6 +144,8 @@ class DecodeStep:
                 data, scales = self.cache[layer][r]
                 q_out, out = self.q_out[r][:t], self.attended[r][:t]
                 if fresh:
+                    if self.prompt is None:
+                        self.prompt = lc.ar_prompt_create(self.hkv, self.dim)
                     k_out = torch.empty_like(k)
                     lc.ar_qk_norm_rope(q, k, q_out, k_out, positions, self.cos_sin, self.q_norm, self.k_norm)
                     self._append(self.kv, k_out, v, slots, data, scales)
@@ -165,7 +167,8 @@ class DecodeStep:
         lc.ar_check(self.sum)
         lc.ar_destroy(self.sum)
         self._destroy(self.kv)
-        lc.ar_prompt_destroy(self.prompt)
+        if self.prompt is not None:
+            lc.ar_prompt_destroy(self.prompt)
 
 
 def main(argv=None) -> None:

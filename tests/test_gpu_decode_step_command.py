@@ -44,3 +44,10 @@ def test_samples_are_forked_freed_and_moved_together(calls, bits):
     assert pages == ["ar_pages_fork", "ar_pages_copy", "ar_pages_free", "ar_pages_compact", "ar_pages_copy", "ar_pages_free"]
     # a step after the pages have moved
     assert f"ar_kv{bits}_attention" in calls[calls.index("ar_pages_compact"):]
+
+
+def test_only_packed_prompts_take_their_workspace(calls):
+    run("--bits", "8")
+    assert "ar_prompt_create" not in calls and "ar_prompt_destroy" not in calls
+    run("--bits", "8", "--packed")
+    assert calls.count("ar_prompt_create") == calls.count("ar_prompt_destroy") == 1
