@@ -55,8 +55,13 @@ __device__ __forceinline__ Series series_of(const PromptArgs& args, int b) {
   return c;
 }
 
+// Bytes between two tokens' keys or values, at most: offsets in a round of up to 96 tokens stay below 2^30, and so does
+// their sum with those of its end, which the hardware compares with the buffer's size.
+constexpr int64_t kMostStride = int64_t(1) << 23;
+constexpr bool offsets_fit(int tokens) { return tokens * kMostStride < int64_t(1) << 30; }
+
 // A request's keys or values of one head from token t0 on, as a buffer that ends with its last token; what lies
-// beyond reads as zero. A round's offsets stay below 2^30 (the host limits the stride).
+// beyond reads as zero.
 __device__ __forceinline__ ar::rsrc_t rows_from(const uint8_t* base, int64_t row_bytes, int t0, int tokens, int width) {
   const int left = tokens - t0;
   const int64_t bytes = left > 0 ? (left - 1) * row_bytes + width : 0;

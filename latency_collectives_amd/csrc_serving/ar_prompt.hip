@@ -38,9 +38,6 @@ constexpr int kFewJobUnits = 12, kFewWork = 3 << 20;
 // of 128 (20): 74 us with large tiles, 64 without; eight of up to 2000, 32 on 8 (48): 163 and 174; one of 8000 (82): 151 and 168.
 constexpr int kLargeUnits = 40;
 
-// Bytes between two tokens' keys or values: a round's 128 tokens stay below 2^31.
-constexpr int64_t kMostStride = int64_t(1) << 23;
-
 }  // namespace
 }  // namespace ard
 

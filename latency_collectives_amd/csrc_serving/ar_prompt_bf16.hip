@@ -15,6 +15,7 @@ struct PromptBf16 {
   static constexpr int BYTES = SUB * 32 * D * 2;  // of a round's keys, or values
   static constexpr int kAll = BYTES / 1024, kItems = (kAll + WAVES - 1) / WAVES;
   static constexpr int kPieces = D / 8;  // of 16 bytes, of a row
+  static_assert(offsets_fit(SUB * 32));
   struct alignas(256) Lds {
     uint8_t round[2][2][BYTES];
     uint32_t odd[2][WAVES];

@@ -14,6 +14,7 @@ struct PromptF32 {
   static constexpr int kSteps = D / 16, kSets = (D + 63) / 64, kTiles = 4 * kSets;
   static constexpr int BYTES = 32 * D * 4;  // of a round's keys, or values
   static constexpr int kAll = BYTES / 1024, kItems = (kAll + WAVES - 1) / WAVES;
+  static_assert(offsets_fit(32));
   struct Lds {
     f32x4 keys[2][2][kSteps][64];  // [round's turn][half]
     f32x4 values[2][32][D / 4];

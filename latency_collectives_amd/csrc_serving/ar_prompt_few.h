@@ -45,6 +45,7 @@ __device__ __forceinline__ bool few_tile(const PromptArgs& args, uint32_t x) {
   typedef FewUnit<DT, D> Unit;
   typedef typename std::conditional<kBf16, bf16x8, f32x4>::type Q;
   constexpr int kSteps = Unit::kSteps, kSets = Unit::kSets, U = Unit::U, T = 16 * U;
+  static_assert(offsets_fit(T));
   constexpr int kPitch = D + 4;  // LDS row: 16 rows' 16-byte accesses fall into different banks
   __shared__ float join[kAttnWaves * 16 * kPitch];
   __shared__ float stat_m[kAttnWaves][R], stat_l[kAttnWaves][R];
