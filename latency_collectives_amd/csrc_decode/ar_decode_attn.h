@@ -34,6 +34,12 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 // Many rows a request: 32 rows for each of a workgroup's waves, if the kernel does not say otherwise.
 constexpr int kRowsColumns = 2, kRowsTile = 16 * kRowsColumns * kAttnWaves;
 
+// What a call takes of a kernel, about, in us: where it starts and ends, a unit of a run, what a unit takes besides if the
+// tile is full of rows, reading back one part of a job with such a tile.
+struct AttnTimes {
+  float start, unit, rows, part;
+};
+
 // A kernel and the workgroups of it that fill the device's 256 compute units.
 struct AttnKernel {
   void (*fn)(AttnArgs);
@@ -43,17 +49,28 @@ struct AttnKernel {
   // Finding a job, its queries and its end take about what twelve units of 32 tokens take while the
   // whole device reads; without them in the split, a run of many short requests ended last.
   int job_units = 12;
+  AttnTimes times = {};  // where the choice goes by them
 };
 AttnKernel select_attn_bf16(int head_dim, int columns);
 AttnKernel select_attn_f32(int head_dim, int columns);
 AttnKernel select_attn_rows(int head_dim);
 
+// The kernel for a call.
+struct Choice {
+  AttnKernel k;
+  int rows;  // of a tile
+  bool many;
+};
+
+// Tokens that a row of the table holds, below 2^31 by more than a wave looks ahead.
+int64_t room_of(const ar_kv4* h, const ar_kv4_attention_args* a);
 
 // A cache's format as the host sees it: its kernels, and the bytes of a page's heads in data and scales.
 struct AttnFormat {
   AttnKernel (*bf16)(int head_dim, int columns);
   AttnKernel (*f32)(int head_dim, int columns);
-  AttnKernel (*rows)(int head_dim, bool brief);  // brief: rows that see few tokens
+  AttnKernel (*rows)(int head_dim, bool brief);  // brief: the smaller tiles, where there are two
+  Choice (*choose)(const AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a);
   bool knows_windows;  // the split for many rows counts a full window for what it is
   int64_t (*page_bytes)(const ar_kv4* h);
   int64_t (*page_scales)(const ar_kv4* h);

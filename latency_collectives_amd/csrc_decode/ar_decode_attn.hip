@@ -8,7 +8,7 @@
 
 namespace {
 
-// The kernel for a call. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose
+// The kernel for a call over the 4-bit cache. Tiles of 16 or 32 rows, four waves on different tokens: short jobs, whose
 // parts join quickly. Tiles of 128 rows, waves on different rows: values are converted once for all
 // of them, but a job is four times as long and so is its join, so they pay where the tiles alone
 // fill the device's 512 places and have some tokens to read, or where the tokens behind them are many.
@@ -22,21 +22,11 @@ namespace {
 // tokens 53 for 29. Tables no wider than the step's longest request avoid it.
 constexpr int64_t kManyTiles = 512, kManyUnits = 1 << 16, kFewTiles = 128;
 
-// Units of 32 tokens that a row sees, below which tiles of many rows are brief (see the instances over the 8-bit cache).
-constexpr int64_t kBriefUnits = 96;
+using ard::AttnKernel;
+using ard::Choice;
+using ard::room_of;
 
-// Tokens that a row of the table holds, below 2^31 by more than a wave looks ahead.
-int64_t room_of(const ar_kv4* h, const ar_kv4_attention_args* a) {
-  return std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
-}
-
-struct Choice {
-  ard::AttnKernel k;
-  int rows;  // of a tile
-  bool many;
-};
-
-Choice choose(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a) {
+Choice choose4(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   const int64_t each = (rows + a->nreq - 1) / a->nreq;
   const bool bf16 = a->dtype == AR_BFLOAT16;
@@ -44,19 +34,15 @@ Choice choose(const ard::AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_
     const int64_t tiles = (each + ard::kRowsTile - 1) / ard::kRowsTile * std::min(a->nreq, a->ntokens) * h->heads;
     const int64_t tokens = room_of(h, a);
     const int64_t units = (a->window > 0 ? std::min<int64_t>(tokens, a->window) : tokens) / 32 + 1;
-    if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits) {
-      const ard::AttnKernel many = f.rows(h->head_dim, units < kBriefUnits);
-      return {many, many.rows, true};
-    }
+    if ((tiles >= kManyTiles && units >= 16) || tiles * units >= kManyUnits)
+      return {f.rows(h->head_dim, false), ard::kRowsTile, true};
   }
   // Twice the rows for one reading of the cache, where enough tiles are left for the device (bfloat16,
   // head_dim 128, 4 kv heads, 16 rows a tile and 32: 64 requests of 64 rows, 2048 tokens 55 and
-  // 30 us; one of 32 rows, 4096 tokens 11.8 and 15.7), and where there is such an instance: binary32 gains from it at
-  // head_dim 64 only.
+  // 30 us; one of 32 rows, 4096 tokens 11.8 and 15.7). Binary32 gains from it at head_dim 64 only.
   const int64_t tiles = (each + 31) / 32 * std::min(a->nreq, a->ntokens) * h->heads;
-  const auto select = bf16 ? f.bf16 : f.f32;
-  const int columns = each > 16 && tiles >= kFewTiles && select(h->head_dim, 2).fn != nullptr ? 2 : 1;
-  return {select(h->head_dim, columns), 16 * columns, false};
+  const int columns = each > 16 && tiles >= kFewTiles && (bf16 || h->head_dim == 64) ? 2 : 1;
+  return {bf16 ? f.bf16(h->head_dim, columns) : f.f32(h->head_dim, columns), 16 * columns, false};
 }
 
 // Partial results of a launch: two slots a workgroup (the job it ends, the job it begins), each
@@ -71,6 +57,10 @@ constexpr size_t kArrivedBytes = kMostRuns * sizeof(uint32_t);
 }  // namespace
 
 namespace ard {
+
+int64_t room_of(const ar_kv4* h, const ar_kv4_attention_args* a) {
+  return std::min<int64_t>(static_cast<int64_t>(a->table_width) << h->page_shift, 0x7FF00000);
+}
 
 ar_kv4* create_handle(const AttnFormat& f, int kv_heads, int head_dim, int page_size, const char* name) {
   if (kv_heads < 1 || kv_heads > 1024) {
@@ -141,7 +131,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
   // Rows of a kv head, and a unit of every job beside what its start and end count for, in 31 bits.
   const int64_t all_rows = static_cast<int64_t>(a->ntokens) * (a->q_heads / h->heads);
   if (all_rows > 0x7FFFFFFF) return ar_fail(AR_ETOOBIG, "too many rows");
-  const Choice choice = choose(f, h, a);
+  const Choice choice = f.choose(f, h, a);
   const AttnKernel& k = choice.k;
   if (k.fn == nullptr) return ar_fail(AR_ENOTSUP, "no kernel for head_dim %d", h->head_dim);
   const int rows_per_tile = choice.rows;
@@ -201,7 +191,7 @@ int launch_attention(const AttnFormat& f, ar_kv4* h, const ar_kv4_attention_args
 }
 
 static const AttnFormat kFormat4 = {
-    select_attn_bf16, select_attn_f32, [](int head_dim, bool) { return select_attn_rows(head_dim); }, false,
+    select_attn_bf16, select_attn_f32, [](int head_dim, bool) { return select_attn_rows(head_dim); }, choose4, false,
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * h->page_size * h->head_dim; },
     [](const ar_kv4* h) { return static_cast<int64_t>(h->heads) * 2 * h->page_size * (h->head_dim / 32); }};
 

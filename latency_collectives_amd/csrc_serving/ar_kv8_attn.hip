@@ -1,5 +1,8 @@
 // Host side of the 8-bit paged cache: the handle and the attention's launch, both as for the 4-bit one.
 
+#include <algorithm>
+#include <cmath>
+
 #include "ar_kv8.h"
 
 namespace ard {
@@ -8,7 +11,49 @@ AttnKernel select_attn8_bf16(int head_dim, int columns);
 AttnKernel select_attn8_f32(int head_dim, int columns);
 AttnKernel select_attn8_rows(int head_dim, bool brief);
 
-static const AttnFormat kFormat8 = {select_attn8_bf16, select_attn8_f32, select_attn8_rows, true,
+namespace {
+
+// What a kernel takes for a call, by the call's averages: `reqs` requests of `tokens` new ones, seeing `seen` in the mean.
+double time_of(const AttnKernel& k, double reqs, double tokens, double seen, int group, int heads, int window) {
+  const double each = tokens * group, tiles = std::ceil(each / k.rows), full = each / (tiles * k.rows);
+  if (window > 0) seen = std::min(seen, window + static_cast<double>(k.rows) / group);
+  const double units = seen / 32 + k.job_units, share = tiles * reqs * heads * units / k.fill;
+  // a run of the split, and the parts that it leaves of a job
+  const double run = std::max({4.0, share, std::sqrt(units)}), parts = units > run ? units / run : 0.0;
+  return k.times.start + k.times.unit * std::min(run, share) + (k.times.rows * run + k.times.part * parts) * full;
+}
+
+// The kernel for a call: tiles of 16 or 32 rows with the waves on different tokens, whose parts join quickly, or of 128 to 384
+// rows on the same tokens, which convert keys and values once for all of them. It is the one that takes least by its times, which
+// stand beside the instances and come from every kernel's time for 1200 to 1300 calls a head size (bfloat16, 1 to 200 requests of
+// 1 to 4096 tokens against 200 to 100000, 1 to 32 query heads, some with windows; binary32 140 with heads of 64). For 1820 others
+// the choice takes 0.4 to 3.4 % longer than the best kernel in the mean, by head size, and up to 3 to 18 % at nineteen of
+// twenty; the rule of the 4-bit cache, whose tiles have 128 rows, 3 to 21 % and 22 to 102 %. Head of 128, 8 kv heads of 4,
+// us with small tiles, tiles of 128 rows and of 384: 8 requests of 66 tokens against 8192 190, 130, 114; of 98 tokens 260, 164,
+// 188; 32 of 33 tokens against 600 46, 30, 28; one of 98 against 32768 247, 128, 185; one of 400 against 2048 36, 58, 79.
+// What the host does not know, lengths below the tables' width and how requests differ, is not in it.
+Choice choose8(const AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a) {
+  const bool bf16 = a->dtype == AR_BFLOAT16;
+  const int group = a->q_heads / h->heads;
+  const double reqs = std::min(a->nreq, a->ntokens), tokens = a->ntokens / reqs;
+  const AttnKernel least = (bf16 ? f.bf16 : f.f32)(h->head_dim, 1);
+  Choice best = {least, least.rows, false};
+  if (tokens * group <= least.rows) return best;
+  const double seen = std::max(static_cast<double>(room_of(h, a)) - tokens / 2, 1.0);
+  auto time = [&](const AttnKernel& k) { return time_of(k, reqs, tokens, seen, group, h->heads, a->window); };
+  double took = time(least);
+  auto look = [&](const AttnKernel& k, bool many) {
+    if (k.fn == nullptr || !(time(k) < took)) return;
+    best = {k, k.rows, many}, took = time(k);
+  };
+  look((bf16 ? f.bf16 : f.f32)(h->head_dim, 2), false);
+  if (bf16) look(f.rows(h->head_dim, true), true), look(f.rows(h->head_dim, false), true);
+  return best;
+}
+
+}  // namespace
+
+static const AttnFormat kFormat8 = {select_attn8_bf16, select_attn8_f32, select_attn8_rows, choose8, true,
                                     [](const ar_kv4* h) { return int64_t(2) * h->heads * h->page_size * h->head_dim; },
                                     [](const ar_kv4* h) { return int64_t(2) * h->heads * (h->page_size / kBlock); }};
 
