@@ -42,8 +42,8 @@ extern "C" {
  * that, infinities and NaN become NaN (that element alone). A reader takes scales outside 2^-100 to
  * 2^119 as the nearer of the two.
  *
- * ar_kv8_create: a handle for caches of one geometry, with the conditions, workspace and rules of
- * ar_kv4_create.
+ * ar_kv8_create: a handle for caches of one geometry, with the conditions and rules of ar_kv4_create. Its
+ * workspace is 69 to 102 MB.
  */
 typedef struct ar_kv8 ar_kv8;
 ar_kv8* ar_kv8_create(int kv_heads, int head_dim, int page_size);
@@ -214,7 +214,7 @@ int ar_pages_copy(const ar_pages_copy_args* a, void* stream);
  * 32 tokens, may leave every row as it was). q, k, v and out are 16-byte aligned, their strides multiples of
  * 16 bytes, those of tokens of k and v 2^23 bytes at most.
  *
- * ar_prompt_create: a handle with the workspace (partial results), for kv_heads 1..1024 and head_dim 64,
+ * ar_prompt_create: a handle with the workspace (partial results, 69 to 102 MB), for kv_heads 1..1024 and head_dim 64,
  * 96, 128, 192 or 256. Calls on one handle are issued in order on one stream, on the GPU that was
  * current when it was created.
  */

@@ -51,3 +51,17 @@ def test_only_packed_prompts_take_their_workspace(calls):
     assert "ar_prompt_create" not in calls and "ar_prompt_destroy" not in calls
     run("--bits", "8", "--packed")
     assert calls.count("ar_prompt_create") == calls.count("ar_prompt_destroy") == 1
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
+def test_workspaces_have_the_sizes_that_the_header_gives(d):
+    """69 to 102 MB, in whole steps of the allocator's 2 MiB."""
+    import latency_collectives_amd as lc
+
+    for make, end in ((lambda: lc.ar_kv8_create(2, d, 16), lc.ar_kv8_destroy), (lambda: lc.ar_prompt_create(2, d), lc.ar_prompt_destroy)):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        h = make()
+        took = before - torch.cuda.mem_get_info()[0]
+        end(h)
+        assert 69e6 - 1 <= took <= 102.5e6 + 2 * 2 ** 20, took
