@@ -9,11 +9,13 @@
 //   O^T [D x 16 rows] += V^T P^T   a lane reads four elements of four tokens in one load; a word is one
 //                 element of four tokens, which two conversions make half an operand: no permutes.
 //
+// Probabilities of bfloat16 calls are one bfloat16, as there; of binary32 calls three, as the query is.
+//
 // Two codes are one conversion, scaled by their block's power of two, exactly; a block of 16 tokens is
 // half a tile, so its scales are scalars of the wave.
 //
-// Bound by the cache's bytes: 64 requests of up to 8192 tokens, 8 kv heads of 128 (536 MB), 102 us, 5.2 TB/s; head of 64 49 us, of 256
-// 200; binary32 111; one request of 2000 tokens, one kv head, 8.1, bound by latency.
+// Bound by the cache's bytes: 64 requests of up to 8192 tokens, 8 kv heads of 128 (536 MB), 102 us, 5.2 TB/s; head of 64 46 us, of 256
+// 189; binary32 108; one request of 2000 tokens, one kv head, 8.1, bound by latency.
 #pragma once
 
 #include "ar_kv8.h"

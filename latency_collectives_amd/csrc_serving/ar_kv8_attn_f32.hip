@@ -5,6 +5,8 @@
 
 namespace ard {
 
+// Three products for one of bfloat16, in tiles of few rows. Two chunks of up to 2048 tokens against 12288, 16 query heads on 4: 575, 929,
+// 1099, 1869 and 2522 us for heads of 64, 96, 128, 192 and 256 (240 to 270 TFLOP/s), a third to a quarter of bfloat16's rate.
 AttnKernel select_attn8_f32(int head_dim, int columns) {
 // rows / 16, workgroups of a compute unit, times (where there is a choice)
 #define ARD_CASE(D, NQ, OCC, ...) \

@@ -4,12 +4,12 @@
 
 namespace ard {
 
-// Two chunks of up to 2048 tokens against 12288, TFLOP/s (16 query heads on 4; 128: 32 on 8), and one layout beside:
-//   64    8 waves of 32 rows, twice a compute unit   759    (8 of 16, twice: 684)
-//   96    12 of 32     747    (8 of 16, twice: 654)
-//   128   12 of 32     957    (8 of 32: 864; 8 of 16, twice: 846)
-//   192   12 of 16     831    (8 of 32: 798)
-//   256   12 of 16     831    (8 of 16: 718)
+// Two chunks of up to 2048 tokens against 12288, TFLOP/s, 16 query heads on 4 (128 with 32 on 8: 1030 to 1050), and one layout beside:
+//   64    8 waves of 32 rows, twice a compute unit   770    (8 of 16, twice: 697)
+//   96    12 of 32     769    (8 of 16, twice: 657)
+//   128   12 of 32     952    (8 of 32: 878; 8 of 16, twice: 810)
+//   192   12 of 16     905    (8 of 32: 900)
+//   256   12 of 16     834    (8 of 16: 732)
 // Tiles of 12 waves of 32 rows are large for requests of few rows or tokens: heads of 96 and 128 have 8 waves of 16 beside.
 constexpr int kJobUnits = 8;  // what starting and ending a job costs; 4 and 12 are within 1% mostly
 

@@ -27,15 +27,19 @@ constexpr size_t kPromptArrived = 1024 * sizeof(uint32_t);  // at least every ke
 
 // Few rows: a workgroup for 16 rows and a kv head, which takes its units without a share for others. As long as jobs times
 // units, with kFewJobUnits for a job's start and end, times head_dim stay below kFewWork, half as much again for
-// binary32, whose other kernels take longer to start. us with few rows' kernel and with the others, head of 128, 8 query heads
-// on one kv head: one prompt of 301 tokens 7.7 and 15.8, of 1000 (1.8 million) 20.7 and 35.6, of 1700 (4.2) 37.7 and 38.7;
-// 32 heads on 8: one of 500 (2.6) 22.8 and 24.9, of 800 (5.1) 42.8 and 30.5, 16 of up to 100 (3.0) 19.5 and 17.0. Head of
-// 64, 800 tokens (2.6) 23.2 and 22.2; of 256, 32 of up to 100 on 8 heads (2.9) 29.0 and 28.5, one of 1400 (6.1) 63.8 and 56.1.
-// Binary32, 128: 1700 tokens 76 and 102, 32 heads, 800 tokens 87 and 80.
+// binary32, whose other kernels take longer to start. us with few rows' kernel and with the others (and that product, in
+// 2^20), head of 128, 8 query heads on one kv head: one prompt of 301 tokens (0.3) 7.9 and 16.2, of 1000 (1.7) 21.0 and 35.4, of 1500
+// (3.3) 36.2 and 39.8, of 1700 (4.0) 42.4 and 40.2; 32 heads on 8: one of 500 (2.4) 21.9 and 25.2, of 600 (3.2) 29.3 and 27.1, of
+// 800 (4.9) 42.8 and 30.7, 16 of up to 100 (2.8) 15.6 and 16.9. Head of 64, 32 on 8, 800 tokens (2.4) 25.8 and 22.5; of 256, 8 on
+// 8, 20 of up to 100 (2.0) 22.5 and 22.1, 8 on one, 900 tokens (3.0) 30.5 and 54.6, 1400 (5.8) 62.0 and 57.3. Binary32, 128: 1700
+// tokens (4.0) 74.5 and 102.6, 32 heads, 800 (4.9) 81.5 and 80.7. With the rule below, on 4100 random calls (one long prompt
+// among short ones in a quarter of them) the choice takes 0.7 to 4 % longer than the best kernel in the mean, by type and head, 4
+// to 17 % at nineteen of twenty; 2.8 times at worst (binary32, head of 192, 280 prompts of a token or eight, 64 heads on 8).
 constexpr int kFewJobUnits = 12, kFewWork = 3 << 20;
 
-// Large tiles: where every workgroup gets so many units of its tile's rows. One prompt of 4000 tokens, 8 heads on one
-// of 128 (20): 74 us with large tiles, 64 without; eight of up to 2000, 32 on 8 (48): 163 and 174; one of 8000 (82): 151 and 168.
+// Large tiles: where every workgroup gets so many units of its tile's rows. us without and with them, head of 128: one prompt of
+// 4000 tokens, 8 heads on one (20), 65 and 76, of 6000 (46) 104 and 107, of 8000 (82) 163 and 146; eight of up to 2000, 32 on 8
+// (48), 168 and 153.
 constexpr int kLargeUnits = 40;
 
 }  // namespace

@@ -228,11 +228,13 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void prompt_attention_bf16(PromptA
 // What bounds it: a unit of 32 tokens and 32 rows of 128 takes the matrix units 512 cycles and the others about 600 (one
 // exponential a score, a comparison, conversions), so waves have to cover for each other: three a SIMD, as many as their
 // registers allow with 32 rows each. Four prompts of up to 8000 tokens, 16 query heads on 4, TFLOP/s:
-//   64    8 waves of 32 rows, twice a compute unit   755    (12, once: 685)
-//   96    12 of 32     900    (8: 763)
-//   128   12 of 32     1030   (six prompts, 32 heads on 8; 8 of 32: 915, 8 of 16 twice: 790)
-//   192   8 of 32      936    (12 of 16: 876)
-//   256   12 of 16     861    (8 of 16: 665)
+//   64    8 waves of 32 rows, twice a compute unit   845    (12, once: 787)
+//   96    12 of 32     970    (8: 767)
+//   128   12 of 32     1057   (8 of 32: 845; six prompts of up to 8191, 32 heads on 8, 1050, and 8 of 16 twice 820)
+//   192   8 of 32      985    (12 of 16: 910)
+//   256   12 of 16     873    (8 of 16: 720)
+// A head of 64 has half the products of one of 128 for the same exponentials; rows of 192 and 256 leave a wave registers for fewer
+// rows (256: 16, so that an operand from LDS feeds one product) or a SIMD for fewer waves (192: two).
 // Smaller calls, where a workgroup's own rows and the joins count for more: 8 waves of 16 rows, twice a compute unit.
 // Six prompts of up to 8191 tokens, 32 heads on 8, us with a job's start and end taken for 2, 4, 6, 8 and 12 units: 1679, 1612,
 // 1560, 1551, 1567 (head of 256, four of up to 8000: 1446, 1371, 1318, 1291, 1302).
