@@ -159,7 +159,8 @@ struct RowArgs {
 // stage: kRowThreads * 8 floats of LDS with CACHE. A rotated row's elements pass through it on their way to the
 // cache: the rotation pairs elements half a row apart, the cache's groups are consecutive.
 template <int DT, int G, int B, bool CACHE, bool PASS>
-__device__ __forceinline__ void norm_rope_rows(const RowArgs& r, float* stage) {
+__device__ __forceinline__ void norm_rope_rows(const RowArgs& given, float* stage) {
+  const RowArgs r = given;  // read at once: read where they are used, 3000 tokens of 8 heads of 96 into the cache took 6.7 us for 6.1
   const ar_qk_norm_rope_args& a = r.a;
   const int d = a.head_dim, rot = a.rot;
   const int by = blockIdx.y;
