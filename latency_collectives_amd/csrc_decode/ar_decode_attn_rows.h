@@ -515,9 +515,9 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv4_attention_rows(AttnArgs
         };
         if (arrive(args.arrived + first_wg, parts, &last)) {
           const int real = min(R, rows - row0);
-          if (parts == 2) join_few<D, R, 2, 4>(part, args.stats_at, first_wg, parts, real, finish);
-          else if (parts <= 4) join_few<D, R, 4, 2>(part, args.stats_at, first_wg, parts, real, finish);
-          else join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, real, reinterpret_cast<float*>(values), finish);
+          if (parts == 2) join_few<D, R, 2, 4, false>(part, args.stats_at, first_wg, parts, real, finish);
+          else if (parts <= 4) join_few<D, R, 4, 2, false>(part, args.stats_at, first_wg, parts, real, finish);
+          else join_parts<D, R, 8, false>(part, args.stats_at, first_wg, parts, real, reinterpret_cast<float*>(values), finish);
         }
       }
     }

@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kAttnThreads, OCC) void kv8_attention(AttnArgs args
         if (n + 1 < NQ) __syncthreads();
       }
       if (!alone && arrive(args.arrived + first_wg, parts, &last))
-        join_parts<D, R, 8>(part, args.stats_at, first_wg, parts, min(R, rows - row0), join, finish);
+        join_parts<D, R, 8, true>(part, args.stats_at, first_wg, parts, min(R, rows - row0), join, finish);
     }
     if (run.left <= 0) return;
     next_job<R>(args, run, me);

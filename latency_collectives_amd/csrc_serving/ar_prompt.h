@@ -234,9 +234,9 @@ __device__ __forceinline__ void prompt_attention(const PromptArgs& args) {
         };
         if (arrive(args.arrived + first_wg, parts, &last)) {
           const int real = min(R, j.rows - j.row0);
-          if (parts == 2) join_few<D, R, 2, 4, THREADS>(part, args.stats_at, first_wg, parts, real, finish);
-          else if (parts <= 4) join_few<D, R, 4, 2, THREADS>(part, args.stats_at, first_wg, parts, real, finish);
-          else join_parts<D, R, 8, THREADS>(part, args.stats_at, first_wg, parts, real, reinterpret_cast<float*>(&lds), finish);
+          if (parts == 2) join_few<D, R, 2, 4, true, THREADS>(part, args.stats_at, first_wg, parts, real, finish);
+          else if (parts <= 4) join_few<D, R, 4, 2, true, THREADS>(part, args.stats_at, first_wg, parts, real, finish);
+          else join_parts<D, R, 8, true, THREADS>(part, args.stats_at, first_wg, parts, real, reinterpret_cast<float*>(&lds), finish);
         }
       }
     }
