@@ -208,8 +208,8 @@ int ar_pages_copy(const ar_pages_copy_args* a, void* stream);
  * t > i - window, t counted from the request's first token. q has q_heads = kv_heads * group heads,
  * head h reads kv head h / group. lse, types, statistics and special values are as in
  * ar_kv4_attention: probabilities are rounded to bfloat16 for AR_BFLOAT16; AR_FLOAT32 calls multiply in
- * binary32. A NaN or infinity of a masked place does not reach a result; a value's infinity that a row sees is NaN there
- * if its probability is zero in binary32. Starts are taken between 0 and
+ * binary32. A NaN or infinity of a masked place does not reach a result; a value's infinity that a row sees may be NaN
+ * there if its probability is zero in binary32. Starts are taken between 0 and
  * ntokens; tokens that no request covers keep their rows of out and lse, those of requests that overlap are
  * undefined and the others' are not (but overlaps that make 256 times the tokens, or 2^31 units of a tile's rows and
  * 32 tokens, may leave every row as it was). q, k, v and out are 16-byte aligned, their strides multiples of
