@@ -25,13 +25,15 @@ double time_of(const AttnKernel& k, double reqs, double tokens, double seen, int
 
 // The kernel for a call: tiles of 16 or 32 rows with the waves on different tokens, whose parts join quickly, or of 128 to 384
 // rows on the same tokens, which convert keys and values once for all of them. It is the one that takes least by its times, which
-// stand beside the instances and come from every kernel's time for 1200 to 1300 calls a head size (bfloat16, 1 to 200 requests of
-// 1 to 4096 tokens against 200 to 100000, 1 to 32 query heads, some with windows; binary32 140 with heads of 64). For 1820 others
-// the choice takes 0.4 to 3.4 % longer than the best kernel in the mean, by head size, and up to 3 to 18 % at nineteen of
-// twenty; the rule of the 4-bit cache, whose tiles have 128 rows, 3 to 21 % and 22 to 102 %. Head of 128, 8 kv heads of 4,
-// us with small tiles, tiles of 128 rows and of 384: 8 requests of 66 tokens against 8192 190, 130, 114; of 98 tokens 260, 164,
+// stand beside the instances and come from every kernel's time for 1400 to 1900 calls a head size (bfloat16, 1 to 200 requests of
+// 1 to 4096 tokens against 200 to 100000, 1 to 32 query heads, some with windows; binary32 400 with heads of 64). The host
+// knows lengths by the tables' width alone, which a program may keep for its longest request: what counts is the product of the
+// times for such lengths and for a quarter of them. How far above the best kernel the choice is in the mean, by head size (and
+// at most, for nineteen of twenty), on calls that the times did not come from: 1820 with tables as wide as their lengths 0.4
+// to 4.0 % (7 to 25 %), where the rule of the 4-bit cache, whose tiles have 128 rows, was 3 to 21 % (22 to 102 %); 266 four times as
+// wide 0.8 to 5 %, and 6 to 9 %; 294 sixteen times as wide 9 to 16 %, and 2 to 27 %. Head of 128, 8 kv heads of 4, us with
+// small tiles, tiles of 128 rows and of 384: 8 requests of 66 tokens against 8192 190, 130, 114; of 98 tokens 260, 164,
 // 188; 32 of 33 tokens against 600 46, 30, 28; one of 98 against 32768 247, 128, 185; one of 400 against 2048 36, 58, 79.
-// What the host does not know, lengths below the tables' width and how requests differ, is not in it.
 Choice choose8(const AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args* a) {
   const bool bf16 = a->dtype == AR_BFLOAT16;
   const int group = a->q_heads / h->heads;
@@ -39,12 +41,15 @@ Choice choose8(const AttnFormat& f, const ar_kv4* h, const ar_kv4_attention_args
   const AttnKernel least = (bf16 ? f.bf16 : f.f32)(h->head_dim, 1);
   Choice best = {least, least.rows, false};
   if (tokens * group <= least.rows) return best;
-  const double seen = std::max(static_cast<double>(room_of(h, a)) - tokens / 2, 1.0);
-  auto time = [&](const AttnKernel& k) { return time_of(k, reqs, tokens, seen, group, h->heads, a->window); };
-  double took = time(least);
+  const double room = static_cast<double>(room_of(h, a)), own = std::min(tokens, room) / 2;
+  auto time = [&](const AttnKernel& k, double length) {
+    return time_of(k, reqs, tokens, std::max({length - tokens / 2, own, 1.0}), group, h->heads, a->window);
+  };
+  auto score = [&](const AttnKernel& k) { return time(k, room) * time(k, room / 4); };
+  double lowest = score(least);
   auto look = [&](const AttnKernel& k, bool many) {
-    if (k.fn == nullptr || !(time(k) < took)) return;
-    best = {k, k.rows, many}, took = time(k);
+    if (k.fn == nullptr || !(score(k) < lowest)) return;
+    best = {k, k.rows, many}, lowest = score(k);
   };
   look((bf16 ? f.bf16 : f.f32)(h->head_dim, 2), false);
   if (bf16) look(f.rows(h->head_dim, true), true), look(f.rows(h->head_dim, false), true);

@@ -11,8 +11,8 @@ AttnKernel select_attn8_f32(int head_dim, int columns) {
 // rows / 16, workgroups of a compute unit, times (where there is a choice)
 #define ARD_CASE(D, NQ, OCC, ...) \
   if (head_dim == D && columns == NQ) return {kv8_attention<DT_F32, D, NQ, OCC>, 256 * OCC, 16 * NQ, kAttnThreads, 12, {__VA_ARGS__}}
-  ARD_CASE(64, 1, 3, 6.4f, 0.41f, 0.0f, 0.3f);
-  ARD_CASE(64, 2, 2, 12.1f, 0.43f, 0.0f, 0.19f);
+  ARD_CASE(64, 1, 3, 6.4f, 0.5f, 0.0f, 0.24f);
+  ARD_CASE(64, 2, 2, 10.9f, 0.43f, 0.0f, 0.19f);
   ARD_CASE(96, 1, 2);
   ARD_CASE(128, 1, 2);
   ARD_CASE(192, 1, 1);

@@ -20,14 +20,14 @@ AttnKernel select_attn8_rows(int head_dim, bool brief) {
     return {kv8_attention_rows<D, NQ, WAVES, SUB, OCC * WAVES / 4>, 256 * OCC, 16 * NQ * WAVES, 64 * WAVES, kJobUnits,               \
             {START, UNIT, ROWS, PART}}
   if (brief) {
-    ARD_CASE(96, 1, 8, 2, 2, 10.6f, 0.73f, 0.38f, 3.9f);
-    ARD_CASE(128, 1, 8, 2, 2, 13.3f, 0.6f, 0.51f, 3.0f);
+    ARD_CASE(96, 1, 8, 2, 2, 11.0f, 0.73f, 0.36f, 5.2f);
+    ARD_CASE(128, 1, 8, 2, 2, 13.4f, 0.6f, 0.46f, 2.9f);
   }
-  ARD_CASE(64, 2, 8, 4, 2, 12.3f, 0.43f, 0.76f, 7.3f);
-  ARD_CASE(96, 2, 12, 3, 1, 14.6f, 0.64f, 0.87f, 4.1f);
-  ARD_CASE(128, 2, 12, 3, 1, 9.9f, 0.47f, 0.95f, 12.0f);
-  ARD_CASE(192, 1, 12, 2, 1, 9.2f, 0.53f, 0.72f, 7.4f);
-  ARD_CASE(256, 1, 12, 1, 1, 15.2f, 0.9f, 0.93f, 7.9f);
+  ARD_CASE(64, 2, 8, 4, 2, 12.2f, 0.42f, 0.67f, 6.0f);
+  ARD_CASE(96, 2, 12, 3, 1, 18.4f, 0.65f, 0.66f, 3.5f);
+  ARD_CASE(128, 2, 12, 3, 1, 11.7f, 0.49f, 0.8f, 8.5f);
+  ARD_CASE(192, 1, 12, 2, 1, 10.5f, 0.55f, 0.45f, 6.3f);
+  ARD_CASE(256, 1, 12, 1, 1, 24.3f, 0.92f, 0.94f, 3.9f);
 #undef ARD_CASE
   return {nullptr, 0};
 }

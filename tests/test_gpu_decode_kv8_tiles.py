@@ -68,7 +68,7 @@ class Batch:
         self.lc.ar_kv8_destroy(self.h)
 
 
-# Heads of 64, 96, 128, 192 and 256 take tiles of: 32, 16, 32, 192, 192; 32, 128, 128, 192, 192; 256, 384, 384, 192, 192.
+# Heads of 64, 96, 128, 192 and 256 take tiles of: 32, 32, 32, 192, 192; 32, 128, 128, 192, 192; 256, 384, 384, 192, 192.
 SIZES = [(24, 24, 500), (24, 64, 900), (24, 190, 900)]
 
 
