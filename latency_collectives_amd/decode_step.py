@@ -191,8 +191,8 @@ def main(argv=None) -> None:
     def tokens(n):
         return torch.randn(n, run.hidden, device="cuda", generator=g).bfloat16()
 
-    run(tokens(sum(prompts)), torch.tensor(prompts + [0] * (rows - a.requests), dtype=torch.int32, device="cuda"),
-        fresh=a.packed)
+    xs = run(tokens(sum(prompts)), torch.tensor(prompts + [0] * (rows - a.requests), dtype=torch.int32, device="cuda"),
+             fresh=a.packed)
     if a.samples > 1:
         copies = torch.arange(a.requests, rows, dtype=torch.int32, device="cuda")
         if int(run.fork(copies % a.requests, copies).sum()):

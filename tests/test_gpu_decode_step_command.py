@@ -65,3 +65,8 @@ def test_workspaces_have_the_sizes_that_the_header_gives(d):
         took = before - torch.cuda.mem_get_info()[0]
         end(h)
         assert 69e6 - 1 <= took <= 102.5e6 + 2 * 2 ** 20, took
+
+
+def test_prompts_without_steps(capsys):
+    run("--steps", "0")
+    assert "us a decode step" in capsys.readouterr().out
