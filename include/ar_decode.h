@@ -171,8 +171,9 @@ int ar_kv4_norm_rope_append(ar_kv4* h, const ar_qk_norm_rope_args* a, void* stre
  * the lengths when it chooses between kernels: the width that the step needs serves better than the
  * buffer's. Lengths and starts must not change while a call runs: it stays inside its buffers, but
  * its results and those of the handle's later calls may be wrong; a new handle is needed then.
- * Tokens that no request covers keep their rows of out. q and out 16-byte aligned, their strides
- * multiples of 16 bytes.
+ * Tokens that no request covers keep their rows of out, those of requests that overlap are undefined (and
+ * overlaps that make 2^31 units of a tile's rows and 32 tokens may leave every row as it was). q and out
+ * 16-byte aligned, their strides multiples of 16 bytes.
  */
 typedef struct {
   const void* q;

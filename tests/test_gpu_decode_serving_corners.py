@@ -171,3 +171,24 @@ def test_compaction_captured_and_replayed(lc):  # noqa: F811
         run()
         torch.cuda.synchronize()
         assert got == [x.tolist() for x in (table, shares, pool, *moves)]
+
+
+@pytest.mark.parametrize("d,size", [(64, (24, 24, 500)), (64, (24, 190, 900)), (96, (24, 64, 900)), (128, (24, 64, 900)), (128, (24, 190, 900)),
+                                    (192, (24, 24, 500)), (256, (24, 64, 900)), (128, (24, 3, 500))])
+def test_chunks_that_overlap_beside_ones_that_do_not(lc, d, size):  # noqa: F811
+    """Starts that go back and forth: eleven requests over the same tokens. The first and the last are alone, and right."""
+    c = Batch(lc, d, *size)
+    t, first, last = c.starts[-1], c.new[0], max(c.new[-1], 1)
+    c.starts = [0, first] + [t - last, first] * 11 + [t]
+    c.starts[-2] = t - last
+    c.new = [max(b - a, 0) for a, b in zip(c.starts, c.starts[1:])]
+    out, lse = c.call()
+    values = S.unpack(c.data.cpu(), c.scales.cpu(), d)[0].cuda()
+    for b in (0, 23):
+        m, n = c.new[b], c.kv[b]
+        kv = values[c.table[b].long()].permute(2, 0, 3, 1, 4).reshape(2, -1, c.hkv, d)[:, :n]
+        a = slice(c.starts[b], c.starts[b + 1])
+        assert 0 < m <= n
+        compare(out[a], lse[a], S.dense_attention(c.q[a], kv[0], kv[1], 0.02, 0))
+    assert (lse[first:t - last] != 7).all()
+    c.done()
